@@ -286,6 +286,102 @@ PA_API int pa_swap_in(pa_pool* pool, int n, const int32_t* ids_dev, const void* 
 PA_API int pa_reshape_and_cache(pa_pool* pool, int layer, const void* k, const void* v,
                          const int64_t* slot_mapping_dev, int T, void* stream);
 
+/* ---- rotary positions ----
+ * A rotary embedding turns pairs of a head's first rot_dim dimensions by an
+ * angle proportional to the token's position p: with c = gain cos(p f_i),
+ * s = gain sin(p f_i), the pair (a, b) becomes (a c - b s, b c + a s); the
+ * dimensions from rot_dim on stay as they are.  Pair i, i < rot_dim / 2, is */
+#define PA_ROPE_HALF 0        /* dimensions i and i + rot_dim / 2 */
+#define PA_ROPE_INTERLEAVED 1 /* dimensions 2i and 2i + 1 */
+
+/* Its speed starts from f_i = theta^(-2i / rot_dim) (radians per position)
+ * and is scaled for contexts longer than a model was trained on: */
+#define PA_ROPE_SCALE_NONE 0
+#define PA_ROPE_SCALE_LINEAR 1 /* f_i / factor */
+/* theta raised to theta factor^(rot_dim / (rot_dim - 2)), so the slowest pair
+ * slows down by `factor` and the fastest stays (rot_dim > 2) */
+#define PA_ROPE_SCALE_NTK 2
+/* g f_i + (1 - g) f_i / factor, where g rises from 0 to 1 with the number of
+ * turns r = original_len f_i / (2 pi) the pair makes over the trained length,
+ * between r = low and r = high */
+#define PA_ROPE_SCALE_BANDS 3
+/* the same blend with g falling linearly in i, from 1 at the pair that turns
+ * `high` times (its index rounded down, at least 0) to 0 at the one that turns
+ * `low` times (rounded up, at most rot_dim - 1); a model so scaled usually
+ * takes gain = 0.1 ln(factor) + 1 */
+#define PA_ROPE_SCALE_YARN 4
+
+/* Description of a rotary embedding.
+ *   layout        PA_ROPE_HALF or PA_ROPE_INTERLEAVED
+ *   rot_dim       dimensions turned, even, 2 .. 128 (at most the head_dim of
+ *                 the pool it is used with)
+ *   scaling       PA_ROPE_SCALE_*
+ *   theta         base, > 1
+ *   factor        how far contexts are stretched, > 0 (unused: NONE)
+ *   original_len  trained context length, > 0; low < high, > 0 (BANDS, YARN)
+ *   gain          multiplies the turned dimensions, finite; 1 for none */
+typedef struct pa_rope_desc {
+  int layout;
+  int rot_dim;
+  int scaling;
+  double theta;
+  double factor;
+  double original_len;
+  double low;
+  double high;
+  double gain;
+} pa_rope_desc;
+
+/* A rotary embedding ready for use: plain data, to be filled by pa_rope_init
+ * and copied freely.  step[i] is pair i's speed as a 64-bit binary fraction of
+ * a turn per position, so position times step, modulo 2^64, is the pair's
+ * angle with no error that grows with the position (2^-34 of a turn at 2^31). */
+typedef struct pa_rope {
+  int layout;
+  int rot_dim;
+  float gain;
+  int reserved;
+  uint64_t step[64];
+} pa_rope;
+
+/* Fills *out from *desc.  divisors: NULL, or rot_dim / 2 finite positive
+ * numbers; f_i is then divided by divisors[i] after the scaling (stretches
+ * that are given pair by pair).  Host only.  PA_ERR_INVALID for parameters
+ * outside the ranges above. */
+PA_API int pa_rope_init(const pa_rope_desc* desc, const double* divisors, pa_rope* out);
+
+/* Rotates T tokens' queries and keys and writes their keys and values into
+ * their slots of layer `layer`: one pass in the place of a rotation of q, a
+ * rotation of k and a pa_reshape_and_cache.
+ *   q             device [T][n_q_heads][head_dim], the pool's input dtype;
+ *                 token t at element t * q_stride (heads and dimensions of a
+ *                 token are contiguous), likewise k and v: strides in
+ *                 elements, multiples of 8, at least heads * head_dim (and below
+ *                 2^40), so the
+ *                 three may be parts of one [T][n_q_heads + 2 n_kv_heads]
+ *                 [head_dim] tensor
+ *   q_out         device [T][n_q_heads][head_dim], contiguous: the rotated
+ *                 queries.  May be q itself when q is contiguous; any other
+ *                 overlap with q, k or v is not allowed
+ *   k, v          device [T][n_kv_heads][head_dim] with strides as for q
+ *   positions_dev device int32 [T]: each token's position, which need not be
+ *                 its place in the cache (any value; a negative one turns the
+ *                 other way)
+ *   slot_mapping_dev  as for pa_reshape_and_cache: a negative slot skips the
+ *                 write (the token's query is rotated all the same), a slot
+ *                 past the pool is skipped and sets PA_ERR_BOUNDS
+ * Angles are exact to 2^-34 of a turn; the rotation is done in fp32 and
+ * rounded once: to 16 bits for q_out and 16-bit pools, and for FP8 pools to the
+ * code that pa_reshape_and_cache gives the fp32 value (not its 16-bit
+ * rounding).  PA_FP8_E4M3_BLOCK pools take runs and tile scales as described
+ * there, from the rotated fp32 keys.  v is stored as pa_reshape_and_cache
+ * stores it. */
+PA_API int pa_rope_and_cache(pa_pool* pool, int layer, const pa_rope* rope, const void* q,
+                             size_t q_stride, void* q_out, int n_q_heads, const void* k,
+                             size_t k_stride, const void* v, size_t v_stride,
+                             const int32_t* positions_dev, const int64_t* slot_mapping_dev, int T,
+                             void* stream);
+
 /* num_splits value that asks pa_decode for the balanced schedule (batches of
  * at most 4096 sequences, else PA_ERR_UNSUPPORTED): one CTA per resident slot
  * of the GPU, four per SM (the kernel's shared memory keeps a fifth off); the

@@ -30,6 +30,14 @@ PA_FP8_E4M3 = 2
 PA_FP32 = 3
 PA_FP8_E4M3_BLOCK = 4
 
+PA_ROPE_HALF = 0
+PA_ROPE_INTERLEAVED = 1
+PA_ROPE_SCALE_NONE = 0
+PA_ROPE_SCALE_LINEAR = 1
+PA_ROPE_SCALE_NTK = 2
+PA_ROPE_SCALE_BANDS = 3
+PA_ROPE_SCALE_YARN = 4
+
 PA_SPLITS_BALANCED = -1  # num_splits: the balanced decode schedule
 
 ERROR_NAMES = {PA_OK: "PA_OK", PA_ERR_INVALID: "PA_ERR_INVALID",
@@ -50,6 +58,18 @@ class pa_pool_desc(ctypes.Structure):
                 ("block_size", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
                 ("head_dim", ctypes.c_int), ("kv_dtype", ctypes.c_int),
                 ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class pa_rope_desc(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int), ("rot_dim", ctypes.c_int), ("scaling", ctypes.c_int),
+                ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("gain", ctypes.c_double)]
+
+
+class pa_rope(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int), ("rot_dim", ctypes.c_int), ("gain", ctypes.c_float),
+                ("reserved", ctypes.c_int), ("step", ctypes.c_uint64 * 64)]
 
 
 _lock = threading.Lock()
@@ -85,6 +105,9 @@ _SIGS = [
     ("pa_swap_out", [_P, _I, _P, _P, _P]),
     ("pa_swap_in", [_P, _I, _P, _P, _P]),
     ("pa_reshape_and_cache", [_P, _I, _P, _P, _P, _I, _P]),
+    ("pa_rope_init", [ctypes.POINTER(pa_rope_desc), _P, ctypes.POINTER(pa_rope)]),
+    ("pa_rope_and_cache", [_P, _I, ctypes.POINTER(pa_rope), _P, _SZ, _P, _I, _P, _SZ, _P, _SZ, _P,
+                           _P, _I, _P]),
     ("pa_decode_num_splits", [_P, _I, _I, _I, ctypes.POINTER(_I)]),
     ("pa_decode_workspace_bytes", [_P, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
     ("pa_decode", [_P, _I, _P, _I, _P, _P, _I, _P, _I, _I, ctypes.c_float, _I, _P, _SZ, _P]),
@@ -254,6 +277,18 @@ def pa_prefix_stats(pool: int):
     return e.value, lk.value, h.value
 
 
+def pa_rope_init(desc: pa_rope_desc, divisors=None) -> pa_rope:
+    """A rotary embedding from its description (and rot_dim / 2 divisors of its speeds)."""
+    out = pa_rope()
+    if divisors is not None:
+        divisors = np.ascontiguousarray(divisors, dtype=np.float64)
+        if divisors.shape != (max(desc.rot_dim // 2, 0),):
+            raise ValueError("divisors must hold rot_dim / 2 numbers")
+    _check(lib().pa_rope_init(ctypes.byref(desc), None if divisors is None else _arr_ptr(divisors),
+                              ctypes.byref(out)))
+    return out
+
+
 # ---------------------------------------------------------------- device calls
 def pa_copy_blocks(pool: int, layer: int, pairs_ptr: int, n_pairs: int, stream: int) -> None:
     _check(lib().pa_copy_blocks(pool, layer, pairs_ptr, n_pairs, stream))
@@ -276,6 +311,14 @@ def pa_swap_in(pool: int, n: int, ids_ptr: int, host_ptr: int, stream: int) -> N
 def pa_reshape_and_cache(pool: int, layer: int, k_ptr: int, v_ptr: int, slot_mapping_ptr: int,
                          T: int, stream: int) -> None:
     _check(lib().pa_reshape_and_cache(pool, layer, k_ptr, v_ptr, slot_mapping_ptr, T, stream))
+
+
+def pa_rope_and_cache(pool: int, layer: int, rope: pa_rope, q_ptr: int, q_stride: int, q_out_ptr: int,
+                      n_q_heads: int, k_ptr: int, k_stride: int, v_ptr: int, v_stride: int,
+                      positions_ptr: int, slot_mapping_ptr: int, T: int, stream: int) -> None:
+    _check(lib().pa_rope_and_cache(pool, layer, rope, q_ptr, q_stride, q_out_ptr, n_q_heads, k_ptr,
+                                   k_stride, v_ptr, v_stride, positions_ptr, slot_mapping_ptr, T,
+                                   stream))
 
 
 def pa_decode_num_splits(pool: int, S: int, n_q_heads: int, max_blocks_per_seq: int) -> int:

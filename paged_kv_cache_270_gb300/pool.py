@@ -35,6 +35,45 @@ def _need(t: torch.Tensor, name: str, dtype=None, device=None):
         raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
+ROPE_LAYOUTS = {"half": N.PA_ROPE_HALF, "interleaved": N.PA_ROPE_INTERLEAVED}
+ROPE_SCALINGS = {"none": N.PA_ROPE_SCALE_NONE, "linear": N.PA_ROPE_SCALE_LINEAR,
+                 "ntk": N.PA_ROPE_SCALE_NTK, "bands": N.PA_ROPE_SCALE_BANDS,
+                 "yarn": N.PA_ROPE_SCALE_YARN}
+
+
+def make_rope(rot_dim: int, layout: str = "half", theta: float = 10000.0, scaling: str = "none",
+              factor: float = 1.0, original_len: float = 8192.0, low: float = 1.0,
+              high: float | None = None, gain: float | None = None, divisors=None) -> N.pa_rope:
+    """A rotary embedding for ``KVPool.rope_and_cache`` (see pa_rope_desc).
+
+    ``high`` defaults to 4 turns for "bands" and 32 for "yarn"; ``gain`` to 1, and
+    for "yarn" to 0.1 ln(factor) + 1."""
+    if high is None:
+        high = 32.0 if scaling == "yarn" else 4.0
+    if gain is None:
+        gain = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 0 else 1.0
+    return N.pa_rope_init(N.pa_rope_desc(ROPE_LAYOUTS[layout], rot_dim, ROPE_SCALINGS[scaling], theta,
+                                         factor, original_len, low, high, gain), divisors)
+
+
+def _token_rows(t: torch.Tensor, name: str, dtype, device) -> int:
+    """The token stride, in elements, of a [T, heads, head_dim] tensor whose tokens may lie
+    apart (a slice of a fused projection) but are contiguous in themselves."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, heads, head_dim]")
+    T, heads, d = t.shape
+    st, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and heads > 1):
+        raise ValueError(f"{name}: the heads and dimensions of a token must be contiguous")
+    return st if T > 1 else heads * d
+
+
 class KVPool:
     def __init__(self, n_layers: int, num_blocks: int, n_kv_heads: int, head_dim: int,
                  kv_dtype: str, k_scale: float = 1.0, v_scale: float = 1.0, device="cuda"):
@@ -132,6 +171,33 @@ class KVPool:
             raise ValueError("k and v must be [T, n_kv_heads, head_dim]")
         N.pa_reshape_and_cache(self.handle, layer, k.data_ptr(), v.data_ptr(),
                                slot_mapping.data_ptr(), T, _stream_handle(stream))
+
+    def rope_and_cache(self, rope: N.pa_rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                       positions: torch.Tensor, slot_mapping: torch.Tensor,
+                       q_out: torch.Tensor | None = None, layer: int = 0, stream=None) -> torch.Tensor:
+        """Rotate q [T, Hq, D] and k [T, Hkv, D] at `positions` (int32) and write k and v
+        into their slots; returns the rotated q (`q_out`, which may be q itself when it is
+        contiguous).  q, k and v may be slices of one fused projection."""
+        qs = _token_rows(q, "q", self.in_dtype, self.device)
+        ks = _token_rows(k, "k", self.in_dtype, self.device)
+        vs = _token_rows(v, "v", self.in_dtype, self.device)
+        _need(positions, "positions", torch.int32, self.device)
+        _need(slot_mapping, "slot_mapping", torch.int64, self.device)
+        T, Hq, D = q.shape
+        kv = (T, self.n_kv_heads, self.head_dim)
+        if D != self.head_dim or k.shape != kv or v.shape != kv:
+            raise ValueError("q must be [T, n_q_heads, head_dim], k and v [T, n_kv_heads, head_dim]")
+        if positions.numel() != T or slot_mapping.numel() != T:
+            raise ValueError("positions and slot_mapping must hold one entry per token")
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=self.device)
+        _need(q_out, "q_out", self.in_dtype, self.device)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        N.pa_rope_and_cache(self.handle, layer, rope, q.data_ptr(), qs, q_out.data_ptr(), Hq,
+                            k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(),
+                            slot_mapping.data_ptr(), T, _stream_handle(stream))
+        return q_out
 
     def copy_blocks(self, pairs: torch.Tensor, layer: int = 0, stream=None) -> None:
         _need(pairs, "pairs", torch.int32, self.device)
