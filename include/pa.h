@@ -494,6 +494,45 @@ PA_API int pa_decode_no_alloc(pa_pool* pool, int layer, void* out, int out_dtype
                               const int32_t* ctx_lens_dev, int S, int n_q_heads,
                               float softmax_scale, int num_splits, void* stream);
 
+/* ---- eviction by accumulated attention weight ("Capítulo 8 ...", section 8.2:
+ * tokens that gather little attention leave the cache, the first tokens and a
+ * window of the last ones stay) ----
+ * Running totals are fp32 rows [S][n_kv_heads][weights_stride], one entry per
+ * token of the sequence's cache in order; a row holds zeros behind the context, so a
+ * token that is appended starts from nothing.  pa_decode_weights adds to them,
+ * pa_evict_select reads them, pa_evict_compact moves them with the tokens. */
+
+/* Device scratch bytes pa_decode_weights needs for this shape: each token's
+ * scores, min(S, 4096) * n_kv_heads * max_blocks_per_seq * 16 * gs * 4 with
+ * gs = G = n_q_heads / n_kv_heads rounded up to an even number (1 stays 1),
+ * each row's softmax state, and the partial states of pa_decode's balanced
+ * schedule.  Only the parts that the contexts reach are touched. */
+PA_API int pa_decode_weights_workspace_bytes(const pa_pool* pool, int S, int n_q_heads,
+                                             int max_blocks_per_seq, size_t* bytes);
+
+/* pa_decode that also adds up how much attention each cached token got:
+ *   weights_out[s][h][t] = decay * weights_in[s][h][t] + sum over the query
+ *     heads g of kv head h of softmax_t(softmax_scale q_g . k_t),  t < ctx_lens[s]
+ * Entries from ctx_lens[s] on, of every row, are neither read nor written.
+ *   weights_in     device fp32 [S][n_kv_heads][weights_stride], or NULL for
+ *                  totals that start at zero (decay is then not used)
+ *   weights_out    the same shape; may be weights_in, must not overlap it otherwise
+ *   weights_stride at least the longest context; a longer context sets
+ *                  PA_ERR_BOUNDS, and its tokens behind the row's end get no total
+ *   decay          finite; 1 adds up, below 1 forgets
+ *   workspace      device scratch of at least pa_decode_weights_workspace_bytes;
+ *                  calls that may overlap on the GPU need one each
+ * Everything else is as for pa_decode, with its balanced schedule (any number
+ * of sequences; the contexts' lengths are read on the device).  A total takes
+ * the weights in fp32, a fixed order of additions, so equal inputs give equal
+ * bits. */
+PA_API int pa_decode_weights(pa_pool* pool, int layer, void* out, int out_dtype, const void* q,
+                             const int32_t* block_tables_dev, int max_blocks_per_seq,
+                             const int32_t* ctx_lens_dev, int S, int n_q_heads,
+                             float softmax_scale, const float* weights_in, float* weights_out,
+                             size_t weights_stride, float decay, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
 /* Chunked prefill: causal attention of a chunk of new tokens per sequence over
  * its paged history ("Optimización de KV Cache ...", sections 5 and 6.3:
  * prefill split into packets, e.g. 8,192 tokens, interleaved with decode).

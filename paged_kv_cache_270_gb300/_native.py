@@ -113,6 +113,9 @@ _SIGS = [
     ("pa_decode", [_P, _I, _P, _I, _P, _P, _I, _P, _I, _I, ctypes.c_float, _I, _P, _SZ, _P]),
     ("pa_prefill", [_P, _I, _P, _I, _P, _P, _P, _I, _P, _I, _I, _I, ctypes.c_float, _P]),
     ("pa_decode_no_alloc", [_P, _I, _P, _I, _P, _P, _I, _P, _I, _I, ctypes.c_float, _I, _P]),
+    ("pa_decode_weights_workspace_bytes", [_P, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    ("pa_decode_weights", [_P, _I, _P, _I, _P, _P, _I, _P, _I, _I, ctypes.c_float, _P, _P, _SZ,
+                           ctypes.c_float, _P, _SZ, _P]),
     ("pa_set_pipeline_wait_limit_ns", [ctypes.c_uint64]),
     ("pa_get_device_error", [_P, ctypes.POINTER(_I), _P]),
 ]
@@ -342,6 +345,25 @@ def pa_decode(pool: int, layer: int, out_ptr: int, out_dtype: int, q_ptr: int, t
     _check(lib().pa_decode(pool, layer, out_ptr, out_dtype, q_ptr, tables_ptr, max_blocks_per_seq,
                            ctx_lens_ptr, S, n_q_heads, softmax_scale, num_splits, workspace_ptr,
                            workspace_bytes, stream))
+
+
+def pa_decode_weights_workspace_bytes(pool: int, S: int, n_q_heads: int,
+                                      max_blocks_per_seq: int) -> int:
+    n = _SZ()
+    _check(lib().pa_decode_weights_workspace_bytes(pool, S, n_q_heads, max_blocks_per_seq,
+                                                   ctypes.byref(n)))
+    return n.value
+
+
+def pa_decode_weights(pool: int, layer: int, out_ptr: int, out_dtype: int, q_ptr: int,
+                      tables_ptr: int, max_blocks_per_seq: int, ctx_lens_ptr: int, S: int,
+                      n_q_heads: int, softmax_scale: float, weights_in_ptr: int,
+                      weights_out_ptr: int, weights_stride: int, decay: float, workspace_ptr: int,
+                      workspace_bytes: int, stream: int) -> None:
+    _check(lib().pa_decode_weights(pool, layer, out_ptr, out_dtype, q_ptr, tables_ptr,
+                                   max_blocks_per_seq, ctx_lens_ptr, S, n_q_heads, softmax_scale,
+                                   weights_in_ptr, weights_out_ptr, weights_stride, decay,
+                                   workspace_ptr, workspace_bytes, stream))
 
 
 def pa_prefill(pool: int, layer: int, out_ptr: int, out_dtype: int, q_ptr: int, q_start_ptr: int,

@@ -90,6 +90,18 @@ int layer_half_maps(pa_pool* pool, int layer, const CUtensorMap_st** tk, const C
 int decode_set_wait_limit(unsigned long long ns);
 int prefill_set_wait_limit(unsigned long long ns);
 int prefill_tc_set_wait_limit(unsigned long long ns);
+int weights_set_wait_limit(unsigned long long ns);
+
+// Argument checks of the decode entry points.
+int in_dtype_of(int kv_dtype);
+int check_shape(const pa_pool* pool, int S, int n_q_heads, int max_blocks);
+int check_decode_args(const pa_pool* pool, int layer, int out_dtype, int S, int n_q_heads,
+                      int max_blocks_per_seq, float softmax_scale);
+int check_decode_ptrs(const void* out, const void* q, const int32_t* tables, const int32_t* ctx);
+
+// The balanced schedule takes batches of up to this many sequences (every CTA
+// scans the context lengths, so the scan must stay short).
+constexpr int kBalancedMaxSeqs = 4096;
 
 // Chunked prefill on the tcgen05 tensor cores, for the shapes it covers
 // (head_dim 128, 1, 2, 4 or 8 query heads per KV head; FP8 or bfloat16 pools with bf16 or

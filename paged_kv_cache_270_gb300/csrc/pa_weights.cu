@@ -1,0 +1,368 @@
+// pa_weights.cu -- decode attention that also adds up the attention each cached
+// token gets ("Capítulo 8 -- Gestión de caché KV de nueva generación", section
+// 8.2: eviction by accumulated attention).
+//
+// With x the scaled scores (log2 units), M their maximum and L the sum of
+// 2^(x - M) over a row, token t's weight is sum over the group's heads of
+// 2^(x - M) / L.  M and L are known only once the whole row has been read, and
+// K must not be read twice (it is half of all traffic): the scored build of the
+// balanced decode kernel leaves every score, G floats per (kv head, token), in
+// the workspace, and the kernel below turns them into weights, rows split over
+// CTAs included.  For each (kv head, token) this costs 8 G bytes more than the
+// 2 D e bytes of K and V (25% for FP8 at D = 128, G = 8; 6% for 16 bits, G = 4),
+// where reading K again would cost D e (50%).
+#include <mutex>
+
+#include "pa_decode_core.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kFinishThreads = 256;
+constexpr int kFinishWarps = kFinishThreads / 32;
+
+// Scores kept per token: G, or an even number for the 8-byte stores.
+int score_heads(int G) { return G == 1 ? 1 : (G + 1) & ~1; }
+
+struct FinishArgs {
+  const float* w_in;  // nullptr: zeros
+  float* w_out;
+  long long w_stride;
+  float decay;
+};
+
+// One CTA per CTA of the decode kernel, over the same range of the balanced
+// schedule (see decode_bal_kernel).  For every unit (sequence, kv head) that
+// the range touches: the rows' (M, 1 / L), from the decode kernel or, where
+// the unit spans CTAs, from all its pieces; then the weights of the range's
+// tokens.  The output rows of a unit that spans n CTAs are merged by those n
+// CTAs, each a slice of the G x D values.
+template <int KV, int D, int OUT>
+__global__ void __launch_bounds__(kFinishThreads) weights_finish_kernel(const DecodeArgs a, const FinishArgs f) {
+  constexpr int kUnit = BalCfg<KV, D>::kUnitCostPages;
+  __shared__ long long s_warp_sums[kFinishWarps];
+  __shared__ long long s_off, s_cost;  // the range's first position: offset into its sequence, that sequence's start
+  __shared__ int s_seq;
+  __shared__ float2 s_ml[8];  // (M, 1 / L) of the unit's heads
+  __shared__ float s_red[kFinishWarps][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dependency_wait();
+
+  // ---- the schedule, as the decode kernel made it
+  const int per = (a.S + kFinishThreads - 1) / kFinishThreads;
+  const int s0 = min(a.S, tid * per), s1 = min(a.S, s0 + per);
+  long long mine = 0;
+  for (int s = s0; s < s1; ++s) {
+    const int np = (clamp_ctx(a.ctx[s], a.max_blocks) + 15) >> 4;
+    mine += np > 0 ? (long long)a.Hkv * (np + kUnit) : 0;
+  }
+  long long ptot;
+  const long long before = block_exclusive_scan<kFinishThreads>(mine, s_warp_sums, ptot);
+  const long long T = max((ptot + a.ctas - 1) / a.ctas, (long long)kMinPagesPerCta);
+  const long long pos_begin = (long long)blockIdx.x * T, pos_end = min(ptot, pos_begin + T);
+  if (pos_begin >= ptot) return;
+  if (before <= pos_begin && pos_begin < before + mine) {
+    long long cum = before;
+    for (int s = s0; s < s1; ++s) {
+      const int np = (clamp_ctx(a.ctx[s], a.max_blocks) + 15) >> 4;
+      const long long n = np > 0 ? (long long)a.Hkv * (np + kUnit) : 0;
+      if (pos_begin < cum + n) {
+        s_seq = s;
+        s_off = pos_begin - cum;
+        s_cost = cum;
+        break;
+      }
+      cum += n;
+    }
+  }
+  __syncthreads();
+  int seq = s_seq;
+  int ctx = clamp_ctx(a.ctx[seq], a.max_blocks);
+  int npages = (ctx + 15) >> 4;
+  int h = (int)(s_off / (npages + kUnit));
+  long long ucost = s_cost + (long long)h * (npages + kUnit);  // position of the unit's start
+
+  while (ucost < pos_end) {
+    // the unit's pages in this range
+    const long long first = ucost + kUnit;  // position of page 0
+    const int pg0 = (int)max(0LL, pos_begin - first), pg1 = (int)min((long long)npages, pos_end - first);
+    if (pg1 > pg0) {
+      const size_t row0 = (size_t)seq * a.Hq + (size_t)h * a.G;
+      const bool whole = pg0 == 0 && pg1 == npages;
+      if (whole) {
+        if (tid < a.G) s_ml[tid] = a.row_ml[row0 + tid];
+      } else {
+        // pieces: CTA c0's partial, in the slot it recorded, and the first
+        // partials of CTAs c0 + 1 .. c1
+        const int c0 = (int)(first / T), c1 = (int)((first + npages - 1) / T);
+        const int n = c1 - c0 + 1, slot0 = 2 * c0 + (a.jobs[c0].w & 1);
+        if (warp < a.G) {
+          float M = -INFINITY, L = 0.f;
+          for (int i = lane; i < n; i += 32) {
+            const size_t p = (size_t)(i == 0 ? slot0 : 2 * (c0 + i)) * a.G + warp;
+            const float m = a.ws_ml[2 * p], l = a.ws_ml[2 * p + 1];
+            const float mn = fmaxf(M, m);
+            if (mn != -INFINITY) {
+              L = L * fast_exp2(M - mn) + l * fast_exp2(m - mn);
+              M = mn;
+            }
+          }
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) {
+            const float m = __shfl_xor_sync(kFull, M, off), l = __shfl_xor_sync(kFull, L, off);
+            const float mn = fmaxf(M, m);
+            if (mn != -INFINITY) {
+              L = L * fast_exp2(M - mn) + l * fast_exp2(m - mn);
+              M = mn;
+            }
+          }
+          if (lane == 0) s_ml[warp] = make_float2(M, 1.f / L);
+        }
+        __syncthreads();
+        // this CTA's slice of the output rows, 32 values at a time; the warps
+        // take the pieces in turn and are added up in warp order
+        const int groups = a.G * D / 32, slices = min(n, groups), me = (int)blockIdx.x - c0;
+        if (me < slices) {
+          for (int gi = me * groups / slices; gi < (me + 1) * groups / slices; ++gi) {
+            const int head = gi * 32 / D, dim = gi * 32 % D + lane;
+            const float M = s_ml[head].x;
+            float O = 0.f;
+            for (int i = warp; i < n; i += kFinishWarps) {
+              const size_t p = (size_t)(i == 0 ? slot0 : 2 * (c0 + i)) * a.G + head;
+              const float m = a.ws_ml[2 * p];
+              O += m == -INFINITY ? 0.f : fast_exp2(m - M) * a.ws_o[p * D + dim];
+            }
+            s_red[warp][lane] = O;
+            __syncthreads();
+            if (warp == 0) {
+              float sum = 0.f;
+#pragma unroll
+              for (int w = 0; w < kFinishWarps; ++w) sum += s_red[w][lane];
+              store_out<OUT>(a.out, (row0 + head) * D + dim, sum * s_ml[head].y * a.v_scale);
+            }
+            __syncthreads();
+          }
+        }
+      }
+      __syncthreads();
+      // ---- the weights of tokens [16 pg0, min(ctx, 16 pg1))
+      const size_t unit = (size_t)seq * a.Hkv + h;
+      const float* sc = a.scores + unit * a.max_blocks * 16 * a.gs;
+      const float* wi = f.w_in ? f.w_in + unit * f.w_stride : nullptr;
+      float* wo = f.w_out + unit * f.w_stride;
+      int t1 = min(ctx, 16 * pg1);
+      if (t1 > f.w_stride) {
+        if (tid == 0) record_error(a.err, PA_ERR_BOUNDS);
+        t1 = (int)f.w_stride;
+      }
+      for (int t = 16 * pg0 + tid; t < t1; t += kFinishThreads) {
+        float w = wi ? f.decay * wi[t] : 0.f;
+        float p = 0.f;
+        for (int g = 0; g < a.G; ++g) p += fast_exp2(sc[(size_t)t * a.gs + g] - s_ml[g].x) * s_ml[g].y;
+        wo[t] = w + p;
+      }
+      __syncthreads();  // s_ml is free again
+    }
+    ucost += npages + kUnit;
+    if (++h == a.Hkv) {
+      h = 0;
+      do {
+        if (++seq >= a.S) return;
+        ctx = clamp_ctx(a.ctx[seq], a.max_blocks);
+      } while (ctx == 0);
+      npages = (ctx + 15) >> 4;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host side
+struct Kernels {
+  const void* decode;
+  int smem;
+  void (*finish)(const DecodeArgs, const FinishArgs);
+  cudaError_t (*launch)(const DecodeArgs&, const FinishArgs&, const CUtensorMap*, const CUtensorMap*, cudaStream_t);
+  int* occupancy;  // [128], per device; 0 = not yet configured
+};
+
+template <int KV, int D, int OUT>
+struct Build {
+  static constexpr bool kPsplit = (KV == KV_BF16) || (OUT == OUT_F32);
+  static constexpr int kMinB = std::min(Cfg<KV, D>::kMinBlocks, 4);  // the schedule puts at most four CTAs on an SM
+  static constexpr auto kDecode = &decode_bal_kernel<KV, D, OUT, kPsplit, kMinB, true>;
+  static cudaError_t launch(const DecodeArgs& a, const FinishArgs& f, const CUtensorMap* tk, const CUtensorMap* tv,
+                            cudaStream_t st) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = BalCfg<KV, D>::kLaunchSmem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kDecode, a, *tk, *tv);
+    if (e != cudaSuccess) return e;
+    cfg.blockDim = dim3(kFinishThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, weights_finish_kernel<KV, D, OUT>, a, f);
+  }
+  static Kernels get() {
+    static int occupancy[128];
+    return {reinterpret_cast<const void*>(kDecode), BalCfg<KV, D>::kLaunchSmem, &weights_finish_kernel<KV, D, OUT>,
+            &launch, occupancy};
+  }
+};
+
+template <int KV>
+Kernels pick(int head_dim, int out_dtype) {
+  constexpr int kOut16 = KV == KV_F16 ? OUT_F16 : OUT_BF16;
+  if (head_dim == 64) return out_dtype == PA_FP32 ? Build<KV, 64, OUT_F32>::get() : Build<KV, 64, kOut16>::get();
+  return out_dtype == PA_FP32 ? Build<KV, 128, OUT_F32>::get() : Build<KV, 128, kOut16>::get();
+}
+
+Kernels pick(int kv_dtype, int head_dim, int out_dtype) {
+  switch (kv_dtype) {
+    case PA_FP16:
+      return pick<KV_F16>(head_dim, out_dtype);
+    case PA_BF16:
+      return pick<KV_BF16>(head_dim, out_dtype);
+    case PA_FP8_E4M3_BLOCK:
+      return pick<KV_E4M3B>(head_dim, out_dtype);
+    default:
+      return pick<KV_E4M3>(head_dim, out_dtype);
+  }
+}
+
+// Sets the shared-memory opt-in once per device; the CTAs of a launch: one per
+// resident slot, at most four per SM.
+int configure(const Kernels& k, int* ctas) {
+  static std::mutex mu;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 128) return fail(PA_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
+  std::lock_guard<std::mutex> lock(mu);
+  if (k.occupancy[dev] == 0) {
+    int occ = 0;
+    e = cudaFuncSetAttribute(k.decode, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k.decode, kThreads, k.smem);
+    if (e != cudaSuccess) return fail(PA_ERR_CUDA, "decode kernel configuration: %s", cudaGetErrorString(e));
+    k.occupancy[dev] = std::max(occ, 1);
+  }
+  *ctas = std::min(k.occupancy[dev], 4) * sms;
+  return PA_OK;
+}
+
+// Parts of the workspace, in floats.
+struct Workspace {
+  size_t ml, jobs, rows, scores, total;
+};
+
+Workspace layout(int ctas, int S, int Hq, int Hkv, int D, int max_blocks) {
+  const size_t G = Hq / Hkv;
+  auto up = [](size_t n) { return (n + 3) / 4 * 4; };  // 16-byte parts
+  Workspace w;
+  w.ml = up(2 * (size_t)ctas * G * D);
+  w.jobs = w.ml + up(2 * (size_t)ctas * G * 2);
+  w.rows = w.jobs + 4 * (size_t)ctas;
+  w.scores = w.rows + up(2 * (size_t)S * Hq);
+  w.total = w.scores + (size_t)S * Hkv * max_blocks * 16 * score_heads((int)G);
+  return w;
+}
+
+}  // namespace
+
+int weights_set_wait_limit(unsigned long long ns) { return (int)set_pipe_wait_limit_here(ns); }
+
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" {
+
+int pa_decode_weights_workspace_bytes(const pa_pool* pool, int S, int n_q_heads, int max_blocks_per_seq,
+                                      size_t* bytes) {
+  int st = check_shape(pool, S, n_q_heads, max_blocks_per_seq);
+  if (st) return st;
+  if (!bytes) return fail(PA_ERR_INVALID, "null output");
+  const pa_pool_desc& d = pool->desc;
+  // the size does not depend on the output dtype: that of the query dtype's build
+  int ctas = 0;
+  st = configure(pick(d.kv_dtype, d.head_dim, in_dtype_of(d.kv_dtype)), &ctas);
+  if (st) return st;
+  *bytes = layout(ctas, std::min(S, kBalancedMaxSeqs), n_q_heads, d.n_kv_heads, d.head_dim, max_blocks_per_seq).total *
+           sizeof(float);
+  return PA_OK;
+}
+
+int pa_decode_weights(pa_pool* pool, int layer, void* out, int out_dtype, const void* q,
+                      const int32_t* block_tables_dev, int max_blocks_per_seq, const int32_t* ctx_lens_dev, int S,
+                      int n_q_heads, float softmax_scale, const float* weights_in, float* weights_out,
+                      size_t weights_stride, float decay, void* workspace, size_t workspace_bytes, void* stream) {
+  pa::TraceRange trace_("pa_decode_weights");
+  int st = check_decode_args(pool, layer, out_dtype, S, n_q_heads, max_blocks_per_seq, softmax_scale);
+  if (st) return st;
+  if (!std::isfinite(decay)) return fail(PA_ERR_INVALID, "decay must be finite");
+  if (weights_stride < 1 || weights_stride >= (size_t)1 << 40)
+    return fail(PA_ERR_INVALID, "weights_stride must be at least 1 and below 2^40");
+  if (S == 0) return PA_OK;
+  st = check_decode_ptrs(out, q, block_tables_dev, ctx_lens_dev);
+  if (st) return st;
+  if (!weights_out) return fail(PA_ERR_INVALID, "null weights_out");
+  if (((uintptr_t)weights_in | (uintptr_t)weights_out) & 15u)
+    return fail(PA_ERR_INVALID, "the weights must be 16-byte aligned");
+  if (!workspace || ((uintptr_t)workspace & 15u))
+    return fail(PA_ERR_INVALID, "a 16-byte aligned workspace is needed");
+  const pa_pool_desc& d = pool->desc;
+  const int Hkv = d.n_kv_heads, D = d.head_dim;
+  int ctas = 0, own_ctas = 0;
+  st = configure(pick(d.kv_dtype, D, in_dtype_of(d.kv_dtype)), &ctas);
+  if (st) return st;
+  const Kernels k = pick(d.kv_dtype, D, out_dtype);
+  st = configure(k, &own_ctas);
+  if (st) return st;
+  const Workspace ws = layout(ctas, std::min(S, kBalancedMaxSeqs), n_q_heads, Hkv, D, max_blocks_per_seq);
+  if (workspace_bytes < ws.total * sizeof(float))
+    return fail(PA_ERR_INVALID, "workspace of %zu bytes needed, %zu given", ws.total * sizeof(float), workspace_bytes);
+  unsigned int* err = device_error_word();
+  if (!err) return PA_ERR_CUDA;
+  const CUtensorMap *tk = nullptr, *tv = nullptr;
+  st = layer_maps(pool, layer, &tk, &tv);
+  if (st) return st;
+
+  DecodeArgs a = {};
+  float* base = static_cast<float*>(workspace);
+  a.ws_o = base;
+  a.ws_ml = base + ws.ml;
+  a.jobs = reinterpret_cast<int4*>(base + ws.jobs);
+  a.row_ml = reinterpret_cast<float2*>(base + ws.rows);
+  a.scores = base + ws.scores;
+  a.G = n_q_heads / Hkv;
+  a.gs = score_heads(a.G);
+  a.max_blocks = max_blocks_per_seq;
+  a.Hq = n_q_heads;
+  a.Hkv = Hkv;
+  a.num_blocks = d.num_blocks;
+  a.ctas = ctas;
+  a.qk_scale_log2 = softmax_scale * 1.4426950408889634f * (d.kv_dtype == PA_FP8_E4M3 ? d.k_scale : 1.f);
+  a.v_scale = d.kv_dtype == PA_FP8_E4M3 ? d.v_scale : 1.f;
+  a.ksc = pool->block_scaled ? layer_scales(pool, pool->k, layer) : nullptr;
+  a.vsc = pool->block_scaled ? layer_scales(pool, pool->v, layer) : nullptr;
+  a.err = err;
+  // one schedule holds at most kBalancedMaxSeqs sequences: larger batches in turn
+  for (int s = 0; s < S; s += kBalancedMaxSeqs) {
+    a.S = std::min(S - s, kBalancedMaxSeqs);
+    a.q = static_cast<const uint16_t*>(q) + (size_t)s * n_q_heads * D;
+    a.out = static_cast<uint8_t*>(out) + (size_t)s * n_q_heads * D * (out_dtype == PA_FP32 ? 4 : 2);
+    a.tables = block_tables_dev + (size_t)s * max_blocks_per_seq;
+    a.ctx = ctx_lens_dev + s;
+    const size_t at = (size_t)s * Hkv * weights_stride;
+    const FinishArgs f = {weights_in ? weights_in + at : nullptr, weights_out + at, (long long)weights_stride, decay};
+    const cudaError_t e = k.launch(a, f, tk, tv, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(PA_ERR_CUDA, "decode_weights launch: %s", cudaGetErrorString(e));
+  }
+  return PA_OK;
+}
+
+}  // extern "C"

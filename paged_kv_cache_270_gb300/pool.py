@@ -19,6 +19,9 @@ KV_DTYPES = {"fp16": N.PA_FP16, "bf16": N.PA_BF16, "fp8_e4m3": N.PA_FP8_E4M3,
 _TORCH_OUT = {N.PA_FP16: torch.float16, N.PA_BF16: torch.bfloat16, N.PA_FP32: torch.float32}
 
 
+_OUT_CODES = {v: k for k, v in _TORCH_OUT.items()}
+
+
 def _stream_handle(stream=None) -> int:
     s = torch.cuda.current_stream() if stream is None else stream
     return int(s.cuda_stream)
@@ -249,7 +252,7 @@ class KVPool:
         if out is None:
             out = torch.empty((S, Hq, D), dtype=out_dtype or q.dtype, device=self.device)
         _need(out, "out", None, self.device)
-        code = {v: k for k, v in _TORCH_OUT.items()}[out.dtype]
+        code = _OUT_CODES[out.dtype]
         if softmax_scale is None:
             softmax_scale = 1.0 / math.sqrt(D)
         ws_bytes = N.pa_decode_workspace_bytes(self.handle, S, Hq, max_blocks, num_splits)
@@ -262,6 +265,53 @@ class KVPool:
                     block_tables.data_ptr(), max_blocks, ctx_lens.data_ptr(), S, Hq,
                     float(softmax_scale), num_splits, ws_ptr, ws_bytes, _stream_handle(stream))
         return out
+
+    def weights_workspace_bytes(self, S: int, n_q_heads: int, max_blocks_per_seq: int) -> int:
+        return N.pa_decode_weights_workspace_bytes(self.handle, S, n_q_heads, max_blocks_per_seq)
+
+    def decode_weights(self, q: torch.Tensor, block_tables: torch.Tensor, ctx_lens: torch.Tensor,
+                       weights: torch.Tensor | None, weights_out: torch.Tensor | None = None,
+                       decay: float = 1.0, out: torch.Tensor | None = None,
+                       out_dtype: torch.dtype | None = None, softmax_scale: float | None = None,
+                       layer: int = 0, workspace: torch.Tensor | None = None, stream=None):
+        """``decode`` that also adds each token's attention weight to its running total:
+        `weights` fp32 [S, n_kv_heads, tokens], updated in place unless `weights_out` is
+        given (None: totals that start at zero).  Returns (out, weights_out)."""
+        _need(q, "q", self.in_dtype, self.device)
+        _need(block_tables, "block_tables", torch.int32, self.device)
+        _need(ctx_lens, "ctx_lens", torch.int32, self.device)
+        S, Hq, D = q.shape
+        if D != self.head_dim:
+            raise ValueError("q head_dim mismatch")
+        if block_tables.dim() != 2 or block_tables.shape[0] != S or ctx_lens.numel() != S:
+            raise ValueError("block_tables must be [S, max_blocks] and ctx_lens [S]")
+        max_blocks = block_tables.shape[1]
+        if weights_out is None:
+            weights_out = weights
+        _need(weights_out, "weights_out", torch.float32, self.device)
+        if weights_out.dim() != 3 or weights_out.shape[:2] != (S, self.n_kv_heads):
+            raise ValueError("weights must be [S, n_kv_heads, tokens]")
+        if weights is not None and weights is not weights_out:
+            _need(weights, "weights", torch.float32, self.device)
+            if weights.shape != weights_out.shape:
+                raise ValueError("weights and weights_out must have one shape")
+        if out is None:
+            out = torch.empty((S, Hq, D), dtype=out_dtype or q.dtype, device=self.device)
+        _need(out, "out", None, self.device)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        if softmax_scale is None:
+            softmax_scale = 1.0 / math.sqrt(D)
+        if workspace is None:
+            workspace = torch.empty(self.weights_workspace_bytes(S, Hq, max_blocks),
+                                    dtype=torch.uint8, device=self.device)
+        N.pa_decode_weights(self.handle, layer, out.data_ptr(), _OUT_CODES[out.dtype], q.data_ptr(),
+                            block_tables.data_ptr(), max_blocks, ctx_lens.data_ptr(), S, Hq,
+                            softmax_scale, weights.data_ptr() if weights is not None else 0,
+                            weights_out.data_ptr(), weights_out.shape[2], decay,
+                            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                            _stream_handle(stream))
+        return out, weights_out
 
     def prefill(self, q: torch.Tensor, q_start: torch.Tensor, block_tables: torch.Tensor,
                 ctx_lens: torch.Tensor, max_chunk: int, out: torch.Tensor | None = None,
@@ -277,7 +327,7 @@ class KVPool:
         if out is None:
             out = torch.empty((T, Hq, D), dtype=out_dtype or q.dtype, device=self.device)
         _need(out, "out", None, self.device)
-        code = {v: k for k, v in _TORCH_OUT.items()}[out.dtype]
+        code = _OUT_CODES[out.dtype]
         if softmax_scale is None:
             softmax_scale = 1.0 / math.sqrt(D)
         N.pa_prefill(self.handle, layer, out.data_ptr(), code, q.data_ptr(), q_start.data_ptr(),
