@@ -533,6 +533,55 @@ PA_API int pa_decode_weights(pa_pool* pool, int layer, void* out, int out_dtype,
                              size_t weights_stride, float decay, void* workspace,
                              size_t workspace_bytes, void* stream);
 
+/* Chooses the tokens that stay.  For each sequence s and each of its n_heads
+ * rows h of totals, with n = ctx_lens[s]:
+ *   n <= budget: all tokens, 0 .. n - 1;
+ *   else the first `sinks` tokens, the last `recent` ones, and of those between
+ *     the budget - sinks - recent with the largest totals; equal totals go to
+ *     the lower token, -0 equals 0, a NaN ranks below every number.
+ *   weights    device fp32 [S][n_heads][weights_stride]; n_heads is usually
+ *              n_kv_heads, or 1 for one choice for all heads
+ *   budget     tokens kept at most, >= 1, >= sinks + recent (both >= 0)
+ *   keep_dev   device int32 [S][n_heads][budget], out: the kept tokens in
+ *              ascending order, then -1 where fewer than budget stay
+ *   kept_lens_dev  device int32 [S], out: min(n, budget), the context length
+ *              after the eviction
+ * A context longer than weights_stride sets PA_ERR_BOUNDS (it then counts as that
+ * long).  Totals from n on are not read.  No scratch memory is needed. */
+PA_API int pa_evict_select(pa_pool* pool, const float* weights, size_t weights_stride,
+                           const int32_t* ctx_lens_dev, int S, int n_heads, int budget, int sinks,
+                           int recent, int32_t* keep_dev, int32_t* kept_lens_dev, void* stream);
+
+/* Moves the kept tokens together: token i < kept_lens[s] of sequence s's
+ * destination table gets, for each kv head h, the K and V of token
+ * keep[s][h][i] of its source table, in layer `layer` (each layer has totals and a choice
+ * of its own; the tables are shared by all).
+ *   keep_dev, kept_lens_dev  as pa_evict_select writes them, keep with
+ *              keep_heads rows per sequence: n_kv_heads, or 1 for all heads
+ *   src_tables_dev, dst_tables_dev  device int32 [S][src_max_blocks] and
+ *              [S][dst_max_blocks]: the sequences' block tables before, and
+ *              freshly allocated blocks, ceil(kept / 16) per sequence.  No
+ *              destination block may be a source block of the call, nor
+ *              appear twice (a source block may: shared prefixes stay as they are
+ *              for whoever else holds them)
+ *   weights_in, weights_out  device fp32 [S][keep_heads][stride], or both
+ *              NULL: the totals move too, weights_out[i] = weights_in[keep[i]],
+ *              and the rest of each weights_out row is zeroed; the two must
+ *              not overlap
+ * The copied bytes are the source's (16-bit and FP8 pools).
+ * PA_FP8_E4M3_BLOCK pools give each destination tile one scale: with v =
+ * fl32(decode(c) * s_src) of its kept rows, s = fl32(max |v| / 448) and codes
+ * E4M3(fl32(v / s)) (0 when s = 0).  Rows of the last page behind the kept tokens are
+ * left as they were.  A token outside its table, an id outside
+ * [0, num_blocks) or a kept_lens outside [0, min(budget, 16 *
+ * dst_max_blocks)] sets PA_ERR_BOUNDS and is skipped. */
+PA_API int pa_evict_compact(pa_pool* pool, int layer, const int32_t* keep_dev, int keep_heads,
+                            int budget, const int32_t* kept_lens_dev,
+                            const int32_t* src_tables_dev, int src_max_blocks,
+                            const int32_t* dst_tables_dev, int dst_max_blocks, int S,
+                            const float* weights_in, size_t weights_in_stride, float* weights_out,
+                            size_t weights_out_stride, void* stream);
+
 /* Chunked prefill: causal attention of a chunk of new tokens per sequence over
  * its paged history ("Optimización de KV Cache ...", sections 5 and 6.3:
  * prefill split into packets, e.g. 8,192 tokens, interleaved with decode).

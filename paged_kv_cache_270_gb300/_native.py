@@ -116,6 +116,8 @@ _SIGS = [
     ("pa_decode_weights_workspace_bytes", [_P, _I, _I, _I, ctypes.POINTER(_SZ)]),
     ("pa_decode_weights", [_P, _I, _P, _I, _P, _P, _I, _P, _I, _I, ctypes.c_float, _P, _P, _SZ,
                            ctypes.c_float, _P, _SZ, _P]),
+    ("pa_evict_select", [_P, _P, _SZ, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
+    ("pa_evict_compact", [_P, _I, _P, _I, _I, _P, _P, _I, _P, _I, _I, _P, _SZ, _P, _SZ, _P]),
     ("pa_set_pipeline_wait_limit_ns", [ctypes.c_uint64]),
     ("pa_get_device_error", [_P, ctypes.POINTER(_I), _P]),
 ]
@@ -364,6 +366,24 @@ def pa_decode_weights(pool: int, layer: int, out_ptr: int, out_dtype: int, q_ptr
                                    max_blocks_per_seq, ctx_lens_ptr, S, n_q_heads, softmax_scale,
                                    weights_in_ptr, weights_out_ptr, weights_stride, decay,
                                    workspace_ptr, workspace_bytes, stream))
+
+
+def pa_evict_select(pool: int, weights_ptr: int, weights_stride: int, ctx_lens_ptr: int, S: int,
+                    n_heads: int, budget: int, sinks: int, recent: int, keep_ptr: int,
+                    kept_lens_ptr: int, stream: int) -> None:
+    _check(lib().pa_evict_select(pool, weights_ptr, weights_stride, ctx_lens_ptr, S, n_heads, budget,
+                                 sinks, recent, keep_ptr, kept_lens_ptr, stream))
+
+
+def pa_evict_compact(pool: int, layer: int, keep_ptr: int, keep_heads: int, budget: int,
+                     kept_lens_ptr: int, src_tables_ptr: int, src_max_blocks: int,
+                     dst_tables_ptr: int, dst_max_blocks: int, S: int, weights_in_ptr: int,
+                     weights_in_stride: int, weights_out_ptr: int, weights_out_stride: int,
+                     stream: int) -> None:
+    _check(lib().pa_evict_compact(pool, layer, keep_ptr, keep_heads, budget, kept_lens_ptr,
+                                  src_tables_ptr, src_max_blocks, dst_tables_ptr, dst_max_blocks, S,
+                                  weights_in_ptr, weights_in_stride, weights_out_ptr,
+                                  weights_out_stride, stream))
 
 
 def pa_prefill(pool: int, layer: int, out_ptr: int, out_dtype: int, q_ptr: int, q_start_ptr: int,

@@ -313,6 +313,63 @@ class KVPool:
                             _stream_handle(stream))
         return out, weights_out
 
+    def evict_select(self, weights: torch.Tensor, ctx_lens: torch.Tensor, budget: int, sinks: int = 0,
+                     recent: int = 0, keep: torch.Tensor | None = None,
+                     kept_lens: torch.Tensor | None = None, stream=None):
+        """The tokens that stay when each sequence is cut to `budget`: the first `sinks`, the
+        last `recent` and the heaviest in between, by their totals `weights` [S, heads, tokens].
+        Returns (keep int32 [S, heads, budget], ascending, -1 behind; kept_lens int32 [S])."""
+        _need(weights, "weights", torch.float32, self.device)
+        _need(ctx_lens, "ctx_lens", torch.int32, self.device)
+        if weights.dim() != 3 or ctx_lens.numel() != weights.shape[0]:
+            raise ValueError("weights must be [S, heads, tokens] and ctx_lens [S]")
+        S, H, tokens = weights.shape
+        if keep is None:
+            keep = torch.empty((S, H, budget), dtype=torch.int32, device=self.device)
+        if kept_lens is None:
+            kept_lens = torch.empty(S, dtype=torch.int32, device=self.device)
+        _need(keep, "keep", torch.int32, self.device)
+        _need(kept_lens, "kept_lens", torch.int32, self.device)
+        if keep.shape != (S, H, budget) or kept_lens.numel() != S:
+            raise ValueError("keep must be [S, heads, budget] and kept_lens [S]")
+        N.pa_evict_select(self.handle, weights.data_ptr(), tokens, ctx_lens.data_ptr(), S, H, budget,
+                          sinks, recent, keep.data_ptr(), kept_lens.data_ptr(), _stream_handle(stream))
+        return keep, kept_lens
+
+    def evict_compact(self, keep: torch.Tensor, kept_lens: torch.Tensor, block_tables: torch.Tensor,
+                      dst_tables: torch.Tensor, weights: torch.Tensor | None = None,
+                      weights_out: torch.Tensor | None = None, layer: int = 0, stream=None):
+        """Copy the kept tokens of `block_tables` together into the blocks of `dst_tables`
+        (freshly allocated ones), and their totals from `weights` into `weights_out`, whose rows
+        are zeroed behind them (a new tensor of the same shape when not given).  Returns weights_out."""
+        _need(keep, "keep", torch.int32, self.device)
+        _need(kept_lens, "kept_lens", torch.int32, self.device)
+        _need(block_tables, "block_tables", torch.int32, self.device)
+        _need(dst_tables, "dst_tables", torch.int32, self.device)
+        if keep.dim() != 3:
+            raise ValueError("keep must be [S, heads, budget]")
+        S, H, budget = keep.shape
+        if (kept_lens.numel() != S or block_tables.dim() != 2 or block_tables.shape[0] != S
+                or dst_tables.dim() != 2 or dst_tables.shape[0] != S):
+            raise ValueError("kept_lens must be [S], the tables [S, blocks]")
+        w_in = w_out = in_stride = out_stride = 0
+        if weights is None and weights_out is not None:
+            raise ValueError("weights_out needs weights")
+        if weights is not None:
+            if weights_out is None:
+                weights_out = torch.empty_like(weights)
+            for t, name in ((weights, "weights"), (weights_out, "weights_out")):
+                _need(t, name, torch.float32, self.device)
+                if t.dim() != 3 or t.shape[:2] != (S, H):
+                    raise ValueError(f"{name} must be [S, heads, tokens] with keep's heads")
+            w_in, in_stride = weights.data_ptr(), weights.shape[2]
+            w_out, out_stride = weights_out.data_ptr(), weights_out.shape[2]
+        N.pa_evict_compact(self.handle, layer, keep.data_ptr(), H, budget, kept_lens.data_ptr(),
+                           block_tables.data_ptr(), block_tables.shape[1], dst_tables.data_ptr(),
+                           dst_tables.shape[1], S, w_in, in_stride, w_out, out_stride,
+                           _stream_handle(stream))
+        return weights_out
+
     def prefill(self, q: torch.Tensor, q_start: torch.Tensor, block_tables: torch.Tensor,
                 ctx_lens: torch.Tensor, max_chunk: int, out: torch.Tensor | None = None,
                 out_dtype: torch.dtype | None = None, softmax_scale: float | None = None,
