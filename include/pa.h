@@ -569,9 +569,9 @@ PA_API int pa_evict_select(pa_pool* pool, const float* weights, size_t weights_s
  *              and the rest of each weights_out row is zeroed; the two must
  *              not overlap
  * The copied bytes are the source's (16-bit and FP8 pools).
- * PA_FP8_E4M3_BLOCK pools give each destination tile one scale: with v =
- * fl32(decode(c) * s_src) of its kept rows, s = fl32(max |v| / 448) and codes
- * E4M3(fl32(v / s)) (0 when s = 0).  Rows of the last page behind the kept tokens are
+ * PA_FP8_E4M3_BLOCK pools give each destination tile one scale, s =
+ * fl32(max |fl32(decode(c) * s_src)| / 448) over its kept rows, and codes
+ * E4M3(fl32(decode(c) * fl32(s_src / s))) (0 when s = 0).  Rows of the last page behind the kept tokens are
  * left as they were.  A token outside its table, an id outside
  * [0, num_blocks) or a kept_lens outside [0, min(budget, 16 *
  * dst_max_blocks)] sets PA_ERR_BOUNDS and is skipped. */

@@ -21,14 +21,18 @@ constexpr unsigned kAll = 0xffffffffu;
 
 // ---------------------------------------------------------------- selection
 // The k-th largest of a row is found digit by digit, most significant first
-// (four 8-bit digits of an order-preserving integer key, a histogram each),
+// (11, 11 and 10 bits of an order-preserving integer key, a histogram each),
 // then one ordered pass writes what lies above it and the first of what equals
 // it.  A row is shared by a cluster of CTAs, which hold its keys in shared
 // memory (the row is read from HBM once) and add up their histograms through
 // distributed shared memory.  Counts are integers, so the result depends on no
 // order of execution.
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
+//
+// What bounds it is the instructions per key and the latency of the passes,
+// not the 4 bytes per key.  The first digit holds the sign, the exponent and two
+// bits of mantissa: wide enough that few keys share its bin with the k-th
+// one, so the later passes only compare and skip.
+constexpr int kSelBins = 2048;
 constexpr int kSelMaxKeys = 49152;  // keys a CTA keeps (192 KiB); longer shares are read again in each pass
 
 struct SelectArgs {
@@ -39,7 +43,7 @@ struct SelectArgs {
   int budget, sinks, recent;
   int32_t* keep;
   int32_t* kept;
-  int max_keys;  // keys of the CTA's dynamic shared memory
+  int max_keys;  // keys of the CTA's dynamic shared memory, a multiple of 32
   unsigned int* err;
 };
 
@@ -51,23 +55,18 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 }
 
 // Adds each lane's digit (those with `in`) to the histogram.  Totals crowd
-// into few bins (all the tokens that nothing attends to share one), and a
-// shared-memory atomic serialises on equal addresses: the lanes that agree with
-// the first remaining one are counted by a ballot, twice, before the rest add
-// one by one.
+// (all the tokens that nothing attends to share one bin), and a shared-memory
+// atomic serialises on equal addresses: the lanes that agree with the first one
+// are counted by a ballot, the rest add one by one.
 __device__ __forceinline__ void hist_add(uint32_t* hist, uint32_t digit, bool in) {
+  const unsigned all = __ballot_sync(kAll, in);
+  if (!all) return;
+  const int lead = __ffs(all) - 1;
+  const uint32_t d = __shfl_sync(kAll, digit, lead);
+  const unsigned same = __ballot_sync(kAll, in && digit == d);
   const int lane = threadIdx.x & 31;
-  unsigned left = __ballot_sync(kAll, in);
-#pragma unroll
-  for (int round = 0; round < 2; ++round) {
-    if (!left) return;
-    const int lead = __ffs(left) - 1;
-    const uint32_t d = __shfl_sync(kAll, digit, lead);
-    const unsigned same = __ballot_sync(kAll, digit == d) & left;
-    if (lane == lead) atomicAdd(&hist[d], (uint32_t)__popc(same));
-    left &= ~same;
-  }
-  if ((left >> lane) & 1u) atomicAdd(&hist[digit], 1u);
+  if (lane == lead) atomicAdd(&hist[d], (uint32_t)__popc(same));
+  else if (in && digit != d) atomicAdd(&hist[digit], 1u);
 }
 
 template <int C>
@@ -76,11 +75,14 @@ __device__ __forceinline__ void row_sync() {
   else cg::this_cluster().sync();
 }
 
-template <int C>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a) {
-  extern __shared__ uint32_t keys[];
-  __shared__ uint32_t hist[2][256];
-  __shared__ uint32_t s_scan[8];
+// C CTAs of NT threads per row.  Single CTAs take 256 threads: with short rows
+// the passes' latency counts, and six CTAs on an SM hide it better than three.
+template <int C, int NT>
+__global__ void __launch_bounds__(NT, NT == 256 ? 5 : 2) select_kernel(const SelectArgs a) {
+  constexpr int kSelThreads = NT, kSelWarps = NT / 32, BPT = kSelBins / NT;  // BPT: bins per thread
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ __align__(16) uint32_t hist[2][kSelBins];
+  __shared__ uint32_t s_scan[kSelWarps];
   __shared__ uint32_t s_digit, s_rem;
   __shared__ uint2 s_warp[kSelWarps];
   __shared__ uint2 s_cta;  // (above, equal) of this CTA's share
@@ -109,16 +111,25 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
   const int chunk = ((m + C - 1) / C + 31) / 32 * 32;
   const int begin = (int)min((long long)m, (long long)rank * chunk), cnt = min(chunk, m - begin);
   const float* src = a.w + (long long)row * a.stride + a.sinks + begin;
-  auto key_at = [&](int i) { return i < a.max_keys ? keys[i] : order_key(src[i]); };
+  // keys i .. i + 3 of the share (i a multiple of 4); those from cnt on are anything
+  auto keys4 = [&](int i) {
+    if (i < a.max_keys) return *reinterpret_cast<const uint4*>(keys + i);
+    uint4 v;
+    v.x = i < cnt ? order_key(src[i]) : 0u;
+    v.y = i + 1 < cnt ? order_key(src[i + 1]) : 0u;
+    v.z = i + 2 < cnt ? order_key(src[i + 2]) : 0u;
+    v.w = i + 3 < cnt ? order_key(src[i + 3]) : 0u;
+    return v;
+  };
 
-  for (int i = tid; i < 512; i += kSelThreads) hist[i >> 8][i & 255] = 0;
+  for (int i = tid; i < 2 * kSelBins / 4; i += kSelThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   uint32_t prefix = 0;
   uint32_t rem = k;  // still to be taken among the keys that start with the prefix
-#pragma unroll 1
-  for (int p = 0; p < 4; ++p) {
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
     uint32_t* h = hist[p & 1];
-    const int shift = 24 - 8 * p;
+    constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
     if (p == 0) {
       // eight loads in flight per thread
       for (int i0 = 0; i0 < cnt; i0 += 8 * kSelThreads) {
@@ -133,58 +144,86 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
           const int i = i0 + j * kSelThreads + tid;
           const uint32_t key = order_key(x[j]);
           if (i < cnt && i < a.max_keys) keys[i] = key;
-          if (i0 + j * kSelThreads < cnt) hist_add(h, key >> 24, i < cnt);  // (uniform per CTA)
+          if (i0 + j * kSelThreads < cnt) hist_add(h, key >> 21, i < cnt);  // (uniform per CTA)
         }
       }
     } else {
-      for (int i0 = 0; i0 < cnt; i0 += kSelThreads) {
-        const int i = i0 + tid;
-        const uint32_t key = i < cnt ? key_at(i) : 0u;
-        hist_add(h, (key >> shift) & 255u, i < cnt && (key >> (shift + 8)) == prefix);
+      for (int i0 = 0; i0 < cnt; i0 += 4 * kSelThreads) {
+        const int i = i0 + 4 * tid;
+        const uint4 v = i < cnt ? keys4(i) : make_uint4(0, 0, 0, 0);
+        const uint32_t key[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          hist_add(h, (key[j] >> kShift[p]) & ((1u << kBits[p]) - 1u),
+                   i + j < cnt && (key[j] >> (kShift[p] + kBits[p])) == prefix);
       }
     }
     row_sync<C>();  // every CTA's histogram is complete
-    // the bins of the whole row from the top down, and the one that holds the rem-th key
-    uint32_t c = 0;
-    if (tid < 256) {
-      if constexpr (C == 1) {
-        c = h[255 - tid];
-      } else {
+    // the bins of the whole row from the top down, BPT per thread, and the one
+    // that holds the rem-th key
+    uint32_t c[BPT];
 #pragma unroll
-        for (int r = 0; r < C; ++r) c += cg::this_cluster().map_shared_rank(h, r)[255 - tid];
-      }
-      uint32_t x = c;
+    for (int j = 0; j < BPT; ++j) c[j] = 0;
+    const int b0 = kSelBins - BPT - BPT * tid;  // bins b0 + BPT - 1 down to b0
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t y = __shfl_up_sync(kAll, x, off);
-        if (lane >= off) x += y;
+    for (int r = 0; r < C; ++r) {
+      const uint32_t* hr = h;
+      if constexpr (C > 1) hr = cg::this_cluster().map_shared_rank(h, r);
+#pragma unroll
+      for (int j = 0; j < BPT; j += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(hr + b0 + BPT - 4 - j);
+        c[j] += v.w;
+        c[j + 1] += v.z;
+        c[j + 2] += v.y;
+        c[j + 3] += v.x;
       }
-      if (lane == 31) s_scan[warp] = x;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      uint32_t before = x - c;
-      for (int w = 0; w < warp; ++w) before += s_scan[w];
-      if (before < rem && rem <= before + c) {
-        s_digit = 255 - tid;
-        s_rem = rem - before;
+    }
+    uint32_t mine = 0;
+#pragma unroll
+    for (int j = 0; j < BPT; ++j) mine += c[j];
+    uint32_t x = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t y = __shfl_up_sync(kAll, x, off);
+      if (lane >= off) x += y;
+    }
+    if (lane == 31) s_scan[warp] = x;
+    // the other buffer's readers passed the barrier above: clear it for the next digit
+    if (p == 1)
+      for (int i = tid; i < kSelBins / 4; i += NT) reinterpret_cast<uint4*>(hist[0])[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    uint32_t before = x - mine;
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) before += w < warp ? s_scan[w] : 0u;
+    if (before < rem && rem <= before + mine) {
+      uint32_t at = before;
+#pragma unroll
+      for (int j = 0; j < BPT; ++j) {
+        if (at < rem && rem <= at + c[j]) {
+          s_digit = b0 + BPT - 1 - j;
+          s_rem = rem - at;
+        }
+        at += c[j];
       }
-    } else {
-      // the other buffer's readers passed the barrier above: clear it for the next digit
-      hist[(p + 1) & 1][tid - 256] = 0;
     }
     __syncthreads();
-    prefix = (prefix << 8) | s_digit;
+    prefix = (prefix << kBits[p]) | s_digit;
     rem = s_rem;
   }
 
   // ---- above the threshold key, and equal to it: counts per warp, each warp
   // one stretch of the share
-  const int seg = ((cnt + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  const int seg = ((cnt + kSelWarps - 1) / kSelWarps + 127) / 128 * 128;
   const int w0 = min(cnt, warp * seg), w1 = min(cnt, w0 + seg);
   uint32_t above = 0, equal = 0;
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const uint32_t key = key_at(i);
-    above += key > prefix;
-    equal += key == prefix;
+  for (int i = w0 + 4 * lane; i < w1; i += 128) {
+    const uint4 v = keys4(i);
+    const uint32_t key[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      above += i + j < w1 && key[j] > prefix;
+      equal += i + j < w1 && key[j] == prefix;
+    }
   }
   above = __reduce_add_sync(kAll, above);
   equal = __reduce_add_sync(kAll, equal);
@@ -202,23 +241,43 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
   if constexpr (C > 1) {
     if (tid == 0) s_cta = make_uint2(ta, te);
     cg::this_cluster().sync();
-    for (int r = 0; r < rank; ++r) {
+#pragma unroll
+    for (int r = 0; r < C; ++r) {
       const uint2 v = *cg::this_cluster().map_shared_rank(&s_cta, r);
-      ga += v.x;
-      ge += v.y;
+      ga += r < rank ? v.x : 0;
+      ge += r < rank ? v.y : 0;
     }
   }
-  // ---- the taken tokens in order: all above, and the first rem of the equal ones
-  const unsigned lower = (1u << lane) - 1u;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t key = i < w1 ? key_at(i) : 0u;
-    const bool is_a = i < w1 && key > prefix, is_e = i < w1 && key == prefix;
-    const unsigned ba = __ballot_sync(kAll, is_a), be = __ballot_sync(kAll, is_e);
-    const uint32_t ea = ga + __popc(ba & lower), ee = ge + __popc(be & lower);
-    if (is_a || (is_e && ee < rem)) keep[a.sinks + ea + min(ee, rem)] = a.sinks + begin + i;
-    ga += __popc(ba);
-    ge += __popc(be);
+  // ---- the taken tokens in order: all above, and the first rem of the equal ones.
+  // A lane holds four neighbours; (above, equal) counts are scanned over the
+  // warp in one word, at most 128 each.
+  for (int i0 = w0; i0 < w1; i0 += 128) {
+    const int i = i0 + 4 * lane;
+    const uint4 v = i < w1 ? keys4(i) : make_uint4(0, 0, 0, 0);
+    const uint32_t key[4] = {v.x, v.y, v.z, v.w};
+    uint32_t f[4], own = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[j] = i + j < w1 ? (key[j] > prefix ? 1u : key[j] == prefix ? 0x10000u : 0u) : 0u;
+      own += f[j];
+    }
+    uint32_t x = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t y = __shfl_up_sync(kAll, x, off);
+      if (lane >= off) x += y;
+    }
+    const uint32_t sum = __shfl_sync(kAll, x, 31);
+    x -= own;
+    uint32_t ea = ga + (x & 0xFFFFu), ee = ge + (x >> 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (f[j] == 1u || (f[j] != 0u && ee < rem)) keep[a.sinks + ea + min(ee, rem)] = a.sinks + begin + i + j;
+      ea += f[j] & 1u;
+      ee += f[j] >> 16;
+    }
+    ga += sum & 0xFFFFu;
+    ge += sum >> 16;
   }
   if constexpr (C > 1) cg::this_cluster().sync();  // no CTA leaves while another may read its memory
 }
@@ -290,60 +349,88 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactA
     }
     if (bad) record_error(a.err, PA_ERR_BOUNDS);
     const long long dtile = ((long long)dst * a.Hkv + h) * 16;
+    if constexpr (!BLK) {
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      uint8_t* pool = which ? a.v : a.k;
-      uint4 x[PER];
-      long long from[PER];
+      for (int which = 0; which < 2; ++which) {
+        uint8_t* pool = which ? a.v : a.k;
+        uint4 x[PER];
+        long long from[PER];
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+          const int vec = j * 32 + lane;
+          from[j] = __shfl_sync(kAll, src, vec / VPR);
+          x[j] = make_uint4(0, 0, 0, 0);
+          if (from[j] >= 0) x[j] = *reinterpret_cast<const uint4*>(pool + from[j] * ROW + (vec % VPR) * 16);
+        }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+          const int vec = j * 32 + lane;
+          if (from[j] >= 0) *reinterpret_cast<uint4*>(pool + (dtile + vec / VPR) * ROW + (vec % VPR) * 16) = x[j];
+        }
+      }
+    } else {
+      // Lane r holds row r's K and V tile scales.  A tile's largest |value| is the
+      // largest of its rows' largest codes under their scales (codes order like
+      // their values), so it takes no conversion to fp32 per code; the new code
+      // is the old one's value times the row's ratio of scales.
+      float s_src[2] = {0.f, 0.f};
+      if (src >= 0) {
+        s_src[0] = a.ksc[src >> 4];
+        s_src[1] = a.vsc[src >> 4];
+      }
+      uint4 x[2][PER];
+      bool have[PER];
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         const int vec = j * 32 + lane;
-        from[j] = __shfl_sync(kAll, src, vec / VPR);
-        x[j] = make_uint4(0, 0, 0, 0);
-        if (from[j] >= 0) x[j] = *reinterpret_cast<const uint4*>(pool + from[j] * ROW + (vec % VPR) * 16);
+        const long long from = __shfl_sync(kAll, src, vec / VPR);
+        have[j] = from >= 0;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          x[which][j] = make_uint4(0, 0, 0, 0);
+          if (have[j])
+            x[which][j] = *reinterpret_cast<const uint4*>((which ? a.v : a.k) + from * ROW + (vec % VPR) * 16);
+        }
       }
-      if constexpr (BLK) {
-        // the rows' values under their tiles' scales, one scale for the new tile
-        float* sc = which ? a.vsc : a.ksc;
-        float y[PER][16];
-        uint32_t mb = 0;
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        uint32_t c[PER][8];  // the codes as binary16 pairs
+        uint32_t mb = 0;     // bits of the largest |value|
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-          const float s = from[j] >= 0 ? sc[from[j] >> 4] : 0.f;
-          const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+          const uint32_t w[4] = {x[which][j].x, x[which][j].y, x[which][j].z, x[which][j].w};
+          __half2 top = __float2half2_rn(0.f);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            uint32_t lo, hi;
-            e4m3x4_to_f16x2x2(w[q], lo, hi);
-            const float2 u0 = unpack2<false>(lo), u1 = unpack2<false>(hi);
-            y[j][4 * q] = __fmul_rn(u0.x, s);
-            y[j][4 * q + 1] = __fmul_rn(u0.y, s);
-            y[j][4 * q + 2] = __fmul_rn(u1.x, s);
-            y[j][4 * q + 3] = __fmul_rn(u1.y, s);
+            e4m3x4_to_f16x2x2(w[q], c[j][2 * q], c[j][2 * q + 1]);
+            top = __hmax2_nan(top, __habs2(*reinterpret_cast<__half2*>(&c[j][2 * q])));
+            top = __hmax2_nan(top, __habs2(*reinterpret_cast<__half2*>(&c[j][2 * q + 1])));
           }
-#pragma unroll
-          for (int q = 0; q < 16; ++q) mb = max(mb, __float_as_uint(y[j][q]) & 0x7FFFFFFFu);
+          const float2 t = __half22float2(top);
+          const float s = __shfl_sync(kAll, s_src[which], (j * 32 + lane) / VPR);
+          mb = max(mb, max(__float_as_uint(__fmul_rn(t.x, s)) & 0x7FFFFFFFu,
+                           __float_as_uint(__fmul_rn(t.y, s)) & 0x7FFFFFFFu));
         }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mb = max(mb, __shfl_xor_sync(kAll, mb, off));
+        mb = __reduce_max_sync(kAll, mb);
         const float s = __fdiv_rn(__uint_as_float(mb), 448.f);
+        // (a row of zeros may have any scale: its ratio is kept finite)
+        const float ratio = s > 0.f ? fminf(__fdiv_rn(s_src[which], s), 0x1p100f) : 0.f;
+        uint8_t* pool = which ? a.v : a.k;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
+          const int vec = j * 32 + lane;
+          const float r = __shfl_sync(kAll, ratio, vec / VPR);
           uint32_t w[8];
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            float2 f = make_float2(0.f, 0.f);
-            if (s > 0.f) f = make_float2(__fdiv_rn(y[j][2 * q], s), __fdiv_rn(y[j][2 * q + 1], s));
-            w[q] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+            const float2 u = unpack2<false>(c[j][q]);
+            w[q] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(u.x, r), __fmul_rn(u.y, r)), __NV_SATFINITE, __NV_E4M3);
           }
-          x[j] = make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
+          if (have[j])
+            *reinterpret_cast<uint4*>(pool + (dtile + vec / VPR) * ROW + (vec % VPR) * 16) =
+                make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
         }
-        if (lane == 0 && dst >= 0 && dst < a.num_blocks) sc[dtile >> 4] = s;
-      }
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        const int vec = j * 32 + lane;
-        if (from[j] >= 0) *reinterpret_cast<uint4*>(pool + (dtile + vec / VPR) * ROW + (vec % VPR) * 16) = x[j];
+        if (lane == 0 && dst >= 0 && dst < a.num_blocks) (which ? a.vsc : a.ksc)[dtile >> 4] = s;
       }
     }
   }
@@ -378,9 +465,10 @@ CompactKernel pick_compact(const pa_pool* pool) {
 
 template <int C>
 cudaError_t launch_select(const SelectArgs& a, int smem, cudaStream_t st) {
-  if (smem > 48 * 1024) {
+  constexpr int NT = C == 1 ? 256 : 512;
+  if (smem > 24 * 1024) {
     const cudaError_t e =
-        cudaFuncSetAttribute(select_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelMaxKeys * 4);
+        cudaFuncSetAttribute(select_kernel<C, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelMaxKeys * 4);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute attr[1];
@@ -389,12 +477,12 @@ cudaError_t launch_select(const SelectArgs& a, int smem, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.S * a.H * C);
-  cfg.blockDim = dim3(kSelThreads);
+  cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, select_kernel<C>, a);
+  return cudaLaunchKernelEx(&cfg, select_kernel<C, NT>, a);
 }
 
 }  // namespace
@@ -437,7 +525,7 @@ int pa_evict_select(pa_pool* pool, const float* weights, size_t weights_stride, 
   const long long tokens = a.stride;
   const int C = tokens <= 8192 ? 1 : tokens <= 32768 ? 2 : tokens <= 65536 ? 4 : 8;
   a.max_keys = (int)std::min<long long>(((tokens + C - 1) / C + 31) / 32 * 32, kSelMaxKeys);
-  const int smem = a.max_keys * 4;
+  const int smem = a.max_keys * 4;  // keys, besides the histograms' 16 KiB
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = C == 1   ? launch_select<1>(a, smem, st)
                         : C == 2 ? launch_select<2>(a, smem, st)

@@ -152,7 +152,8 @@ def _expect(pool, which, keep, kept, src, dst, layer=0):
                 if pool.block_scaled:
                     v = rows.view(torch.float8_e4m3fn).float() * sbefore[blk, h].view(-1, 1)
                     scale = v.abs().max() / torch.tensor(448.0)
-                    rows = (v / scale if scale > 0 else torch.zeros_like(v)).clamp(-448, 448)
+                    ratio = sbefore[blk, h].view(-1, 1) / scale if scale > 0 else torch.zeros(len(blk), 1)
+                    rows = (rows.view(torch.float8_e4m3fn).float() * ratio).clamp(-448, 448)
                     rows = rows.to(torch.float8_e4m3fn).view(torch.uint8)
                     scales[d, h] = scale
                 tiles[d, h, :len(toks)] = rows
