@@ -1056,8 +1056,9 @@ int decode_with_plan(pa_pool* pool, int layer, void* out, int out_dtype, const v
   for (int i = 0; i <= kGuidedSplits; ++i) a.sl.b[i] = plan.b[i];
   a.ctas = plan.ctas;
   a.scores = nullptr;
-  a.row_ml = nullptr;
-  a.gs = 0;
+  a.ranges = nullptr;
+  a.w_in = nullptr;
+  a.w_out = nullptr;
   const float log2e = 1.4426950408889634f;
   a.qk_scale_log2 = softmax_scale * log2e * (d.kv_dtype == PA_FP8_E4M3 ? d.k_scale : 1.f);
   a.v_scale = d.kv_dtype == PA_FP8_E4M3 ? d.v_scale : 1.f;

@@ -99,11 +99,23 @@ struct DecodeArgs {
   const float* ksc;     // block-scaled pools: this layer's scales [num_blocks][Hkv]
   const float* vsc;
   unsigned int* err;
-  // the scored build: every token's scores, fp32 [S][Hkv][max_blocks * 16][gs] in log2 units
-  // (gs: see score_heads), and each row's (M, 1 / L) [S][Hq] where one CTA finished it
+  // the scored build (pa_decode_weights): every token's scores, fp32
+  // [S][Hkv][max_blocks * 16][gs] in log2 units, each CTA's range of the
+  // schedule [ctas], and the running totals [S][Hkv][w_stride]
   float* scores;
-  float2* row_ml;
-  int gs;
+  struct RangeStart* ranges;
+  int gs;  // G, or the next even number (8-byte stores)
+  const float* w_in;  // nullptr: zeros
+  float* w_out;
+  long long w_stride;
+  float decay;
+};
+
+// Where a CTA's range of the balanced schedule starts: position pos_begin lies in
+// sequence seq, whose units start at position cost; positions per CTA and in all.
+struct RangeStart {
+  int seq, pad;
+  long long pos_begin, pos_end, cost, T;
 };
 
 __device__ __forceinline__ int clamp_ctx(int c, int max_blocks) { return c < 0 ? 0 : min(c, max_blocks * 16); }
@@ -176,6 +188,137 @@ template <bool SWZ>
 __device__ __forceinline__ uint32_t tile_off(uint32_t off) {
   if constexpr (SWZ) return swizzle128(off);
   else return off;
+}
+
+// Stores two floats that are read again soon: L2 is asked to keep the line.
+__device__ __forceinline__ void store_kept(float* p, float a, float b) {
+  uint64_t policy;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(policy));
+  asm volatile("st.global.L2::cache_hint.v2.f32 [%0], {%1, %2}, %3;" ::"l"(p), "f"(a), "f"(b), "l"(policy) : "memory");
+}
+
+// Turns the scores of tokens [t0, t1) of a unit (t0 a multiple of 16) into
+// weights, sum over heads of 2^(x - M) / L, and adds them to the totals.  ml:
+// (M, 1 / L) of the gs heads, (0, 0) for a padding one.  Called by NT threads.
+// With eight heads two lanes share a token (16-byte loads, 512 contiguous bytes
+// per warp instruction) and swap halves, so each lane writes one token of two
+// load rounds; with four heads a lane holds a token; other groups are loaded as
+// pairs of heads.  The score loads of a round (UNR x 64 or UNR x 128 tokens per
+// warp) are all issued before the first use: the pass is bound by their latency.
+template <int NT, int UNR>
+__device__ __forceinline__ void add_weights(const float* sc, int gs, const float2* ml, const float* wi, float* wo,
+                                            float decay, int t0, int t1) {
+  constexpr int NW = NT / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (gs == 8) {
+    float M[4], inv[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const float2 v = ml[4 * (lane & 1) + g];
+      M[g] = v.x;
+      inv[g] = v.y;
+    }
+    const float4* s4 = reinterpret_cast<const float4*>(sc);
+    for (int base = t0 + warp * 64 * UNR; base < t1; base += NW * 64 * UNR) {
+      float4 x[4 * UNR];
+      float w[2 * UNR];
+#pragma unroll
+      for (int j = 0; j < 4 * UNR; ++j) {
+        const int t = base + 16 * j + (lane >> 1);
+        x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < t1) x[j] = __ldcg(s4 + 2 * (size_t)t + (lane & 1));
+      }
+#pragma unroll
+      for (int j = 0; j < 2 * UNR; ++j) {  // even lanes write round 2j, odd ones round 2j + 1
+        const int t = base + 16 * (2 * j + (lane & 1)) + (lane >> 1);
+        w[j] = wi && t < t1 ? decay * wi[t] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 2 * UNR; ++j) {
+        float p[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float4 v = x[2 * j + r];
+          p[r] = fast_exp2(v.x - M[0]) * inv[0] + fast_exp2(v.y - M[1]) * inv[1] + fast_exp2(v.z - M[2]) * inv[2] +
+                 fast_exp2(v.w - M[3]) * inv[3];
+        }
+        const float other = __shfl_xor_sync(kFull, lane & 1 ? p[0] : p[1], 1);
+        const int t = base + 16 * (2 * j + (lane & 1)) + (lane >> 1);
+        // (the even lane's heads first, for either lane's token)
+        const float sum = lane & 1 ? other + p[1] : p[0] + other;
+        if (t < t1) wo[t] = w[j] + sum;
+      }
+    }
+  } else if (gs == 4) {
+    const float2 m0 = ml[0], m1 = ml[1], m2 = ml[2], m3 = ml[3];
+    const float4* s4 = reinterpret_cast<const float4*>(sc);
+    for (int base = t0 + warp * 128 * UNR; base < t1; base += NW * 128 * UNR) {
+      float4 x[4 * UNR];
+      float w[4 * UNR];
+#pragma unroll
+      for (int j = 0; j < 4 * UNR; ++j) {
+        const int t = base + 32 * j + lane;
+        x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < t1) x[j] = __ldcg(s4 + t);
+        w[j] = wi && t < t1 ? decay * wi[t] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 4 * UNR; ++j) {
+        const int t = base + 32 * j + lane;
+        const float p = fast_exp2(x[j].x - m0.x) * m0.y + fast_exp2(x[j].y - m1.x) * m1.y +
+                        fast_exp2(x[j].z - m2.x) * m2.y + fast_exp2(x[j].w - m3.x) * m3.y;
+        if (t < t1) wo[t] = w[j] + p;
+      }
+    }
+  } else if (gs == 1) {
+    const float2 m = ml[0];
+    for (int base = t0 + warp * 128; base < t1; base += NW * 128) {
+      float x[4], w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = base + 32 * j + lane;
+        x[j] = t < t1 ? __ldcg(sc + t) : 0.f;
+        w[j] = wi && t < t1 ? decay * wi[t] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = base + 32 * j + lane;
+        if (t < t1) wo[t] = w[j] + fast_exp2(x[j] - m.x) * m.y;
+      }
+    }
+  } else {  // two or six heads
+    for (int base = t0 + warp * 64; base < t1; base += NW * 64) {
+      float2 x[2][3];
+      float w[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int t = base + 32 * j + lane;
+#pragma unroll
+        for (int g = 0; g < 3; ++g) {
+          x[j][g] = make_float2(0.f, 0.f);
+          if (t < t1 && 2 * g < gs) x[j][g] = __ldcg(reinterpret_cast<const float2*>(sc + (size_t)t * gs) + g);
+        }
+        w[j] = wi && t < t1 ? decay * wi[t] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int t = base + 32 * j + lane;
+        float p = 0.f;
+#pragma unroll
+        for (int g = 0; g < 3; ++g)
+          if (2 * g < gs)
+            p += fast_exp2(x[j][g].x - ml[2 * g].x) * ml[2 * g].y + fast_exp2(x[j][g].y - ml[2 * g + 1].x) * ml[2 * g + 1].y;
+        if (t < t1) wo[t] = w[j] + p;
+      }
+    }
+  }
+}
+
+// The tokens of a unit's pages up to `end` that have a place in a totals row.
+__device__ __forceinline__ int totals_end(int end, const DecodeArgs& a) {
+  if (end <= a.w_stride) return end;
+  if (threadIdx.x == 0) record_error(a.err, PA_ERR_BOUNDS);
+  return (int)a.w_stride;
 }
 
 // One page of a consumer warp: S^T = K_page . Q^T for the group, the online
@@ -321,8 +464,8 @@ __device__ __forceinline__ void consume_page(const uint8_t* Ks, const uint8_t* V
           score[kg1] = x2;
         }
       } else if (2 * t < gs) {
-        *reinterpret_cast<float2*>(score + kg0 * gs + 2 * t) = make_float2(x0, x1);
-        *reinterpret_cast<float2*>(score + kg1 * gs + 2 * t) = make_float2(x2, x3);
+        store_kept(score + kg0 * gs + 2 * t, x0, x1);
+        store_kept(score + kg1 * gs + 2 * t, x2, x3);
       }
     }
     float pm0 = fmaxf(x0, x2), pm1 = fmaxf(x1, x3);
@@ -488,8 +631,12 @@ __device__ __forceinline__ void consumers_sync() {  // the four consumer warps o
 // unit (merge of their states through shared memory, then the output rows, or
 // a partial when the unit goes on in another CTA) while the ring keeps
 // filling.  A unit split across CTAs is merged by merge_jobs_kernel: the CTA
-// holding its first page records the job.  The scored build (SC) also leaves
-// every token's scores and each whole unit's (M, 1 / L) for pa_decode_weights.
+// holding its first page records the job.  The scored build (SC, for
+// pa_decode_weights) stores every token's scores as it goes.  A unit that lies
+// whole in the CTA's range gets its weights right after its last page, its scores
+// still in L2 (all such units of a CTA use one area, the first one's, so the
+// lines are written over before they need to go to HBM); the others' are
+// left for weights_finish_kernel, with the range's start.
 template <int KV, int D, int OUT, bool PSPLIT, int MINB, bool SC = false>
 __global__ void __launch_bounds__(kThreads, MINB) decode_bal_kernel(const DecodeArgs a,
                                                               const __grid_constant__ CUtensorMap tmk,
@@ -505,10 +652,12 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_bal_kernel(const Decode
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ long long s_warp_sums[kThreads / 32];
   __shared__ long long s_start_off, s_rbegin, s_rend;
+  __shared__ long long s_start_cost;  // scored build
   __shared__ int s_start_seq;
   __shared__ int s_abort;
   __shared__ int s_go;
   __shared__ int4 s_job;
+  __shared__ float2 s_unit_ml[SC ? 8 : 1];  // scored build: (M, 1 / L) of a whole unit's heads
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + C::kAlign - 1) & ~uintptr_t(C::kAlign - 1));
   uint8_t* ring = smem;
@@ -575,6 +724,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_bal_kernel(const Decode
         if (start) {
           s_start_seq = s;
           s_start_off = off;
+          if constexpr (SC) s_start_cost = cum;
           s_rbegin = r;
         } else {
           s_rend = r;
@@ -593,8 +743,12 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_bal_kernel(const Decode
   const int n_pages = (int)(s_rend - s_rbegin);  // real pages of this CTA
   if (n_pages <= 0) {  // no pages for this CTA: no partial and no merge job
     if (threadIdx.x == 0) a.jobs[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if constexpr (SC)
+      if (threadIdx.x == 0) a.ranges[blockIdx.x].seq = -1;
     return;
   }
+  if constexpr (SC)
+    if (threadIdx.x == 0) a.ranges[blockIdx.x] = RangeStart{s_start_seq, 0, pos_begin, pos_end, s_start_cost, T};
   if (threadIdx.x == 0) {
     s_abort = 0;
     s_job = make_int4(-1, 0, 0, 0);
@@ -737,6 +891,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_bal_kernel(const Decode
     float* slot = reinterpret_cast<float*>(frag);  // merge slot(s) [kMergeSlots][8][D]
     SegDesc* mine_d = desc + 1 + warp;             // this warp's copy of its unit's descriptor
     int kb = 0;
+    long long area = -1;  // scored build: the unit whose score area this CTA's whole units use
     for (int j = 0; kb < n_pages; ++j) {
       // ---- the unit: descriptor and query rows
       const bool have_q = __all_sync(kFull, wait_or_abort(q_full, j & 1, abort_flag, a.err));
@@ -788,6 +943,15 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_bal_kernel(const Decode
       // ---- the unit's pages: warp w takes those whose CTA-local index is w mod 4
       const int len = have_q ? mine_d->len : 0;
       const int pg0 = mine_d->pg0, ctx = mine_d->ctx;
+      float* score0 = nullptr;  // scored build: the scores of the unit's pages
+      if constexpr (SC) {
+        long long unit = (long long)mine_d->seq * a.Hkv + mine_d->h;
+        if (pg0 == 0 && len == mine_d->npages) {
+          if (area < 0) area = unit;
+          unit = area;
+        }
+        score0 = a.scores + (size_t)unit * a.max_blocks * 16 * a.gs;
+      }
       float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
       float o[NT][4];
 #pragma unroll
@@ -798,8 +962,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_bal_kernel(const Decode
         if (!__all_sync(kFull, wait_or_abort(&full[stage], (k / C::kStages) & 1, abort_flag, a.err))) break;
         const uint8_t* Ks = ring + stage * C::kStageBytes;
         float* score = nullptr;
-        if constexpr (SC)
-          score = a.scores + (((size_t)mine_d->seq * a.Hkv + mine_d->h) * a.max_blocks + (pg0 + k - kb)) * 16 * a.gs;
+        if constexpr (SC) score = score0 + (size_t)(pg0 + k - kb) * 16 * a.gs;
         consume_page<KV, D, PSPLIT, SC>(Ks, Ks + C::kTile, (pg0 + k - kb) * 16, ctx, qk_scale, qf, qsm,
                                         &stage_scale[stage], m0, m1, l0, l1, o, vinv, score, SC ? a.gs : 0);
         __syncwarp();
@@ -888,7 +1051,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_bal_kernel(const Decode
           const size_t row = (size_t)sd.seq * a.Hq + (size_t)sd.h * a.G + head;
           store_out<OUT>(a.out, row * D + dim, L > 0.f ? O / L * a.v_scale : 0.f);
           if constexpr (SC)
-            if (dim == 0) a.row_ml[row] = make_float2(M, 1.f / L);
+            if (dim == 0) s_unit_ml[head] = make_float2(M, 1.f / L);
         } else {
           const size_t prow = (size_t)pslot * a.G + head;
           a.ws_o[prow * D + dim] = O;
@@ -896,6 +1059,16 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_bal_kernel(const Decode
             a.ws_ml[2 * prow] = M;
             a.ws_ml[2 * prow + 1] = L;
           }
+        }
+      }
+      if constexpr (SC) {
+        if (direct) {
+          if (tid >= a.G && tid < a.gs) s_unit_ml[tid] = make_float2(0.f, 0.f);
+          consumers_sync();  // (M, 1 / L), and every warp's scores
+          const size_t row = ((size_t)sd.seq * a.Hkv + sd.h) * a.w_stride;
+          if (write)
+            add_weights<kConsumerWarps * 32, 2>(score0, a.gs, s_unit_ml, a.w_in ? a.w_in + row : nullptr, a.w_out + row,
+                                                a.decay, 0, totals_end(sd.ctx, a));
         }
       }
       if (tid == 0) s_go = !*abort_flag;  // one thread decides for all, read after the barrier

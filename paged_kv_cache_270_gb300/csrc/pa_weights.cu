@@ -6,11 +6,12 @@
 // 2^(x - M) over a row, token t's weight is sum over the group's heads of
 // 2^(x - M) / L.  M and L are known only once the whole row has been read, and
 // K must not be read twice (it is half of all traffic): the scored build of the
-// balanced decode kernel leaves every score, G floats per (kv head, token), in
-// the workspace, and the kernel below turns them into weights, rows split over
-// CTAs included.  For each (kv head, token) this costs 8 G bytes more than the
-// 2 D e bytes of K and V (25% for FP8 at D = 128, G = 8; 6% for 16 bits, G = 4),
-// where reading K again would cost D e (50%).
+// balanced decode kernel keeps every score, G floats per (kv head, token), in
+// the workspace.  Rows that one CTA streams whole are weighed by it, from scores
+// that are still in L2; rows split over CTAs by the kernel below.  For these each
+// (kv head, token) costs 8 G bytes more than the 2 D e bytes of K and V (25% for
+// FP8 at D = 128, G = 8; 6% for 16 bits, G = 4), where reading K again would
+// cost D e (50%).
 #include <mutex>
 
 #include "pa_decode_core.cuh"
@@ -24,143 +25,108 @@ constexpr int kFinishWarps = kFinishThreads / 32;
 // Scores kept per token: G, or an even number for the 8-byte stores.
 int score_heads(int G) { return G == 1 ? 1 : (G + 1) & ~1; }
 
-struct FinishArgs {
-  const float* w_in;  // nullptr: zeros
-  float* w_out;
-  long long w_stride;
-  float decay;
-};
-
-// One CTA per CTA of the decode kernel, over the same range of the balanced
-// schedule (see decode_bal_kernel).  For every unit (sequence, kv head) that
-// the range touches: the rows' (M, 1 / L), from the decode kernel or, where
-// the unit spans CTAs, from all its pieces; then the weights of the range's
+// One CTA per CTA of the decode kernel, over the same range of the schedule.
+// For every unit (sequence, kv head) of which the range holds a part: the
+// rows' (M, 1 / L) from all the unit's pieces, then the weights of the range's
 // tokens.  The output rows of a unit that spans n CTAs are merged by those n
-// CTAs, each a slice of the G x D values.
+// CTAs, each a slice of the G x D values.  (Whole units are done.)
 template <int KV, int D, int OUT>
-__global__ void __launch_bounds__(kFinishThreads) weights_finish_kernel(const DecodeArgs a, const FinishArgs f) {
+__global__ void __launch_bounds__(kFinishThreads, 4) weights_finish_kernel(const DecodeArgs a) {
   constexpr int kUnit = BalCfg<KV, D>::kUnitCostPages;
-  __shared__ long long s_warp_sums[kFinishWarps];
-  __shared__ long long s_off, s_cost;  // the range's first position: offset into its sequence, that sequence's start
-  __shared__ int s_seq;
   __shared__ float2 s_ml[8];  // (M, 1 / L) of the unit's heads
   __shared__ float s_red[kFinishWarps][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dependency_wait();
-
-  // ---- the schedule, as the decode kernel made it
-  const int per = (a.S + kFinishThreads - 1) / kFinishThreads;
-  const int s0 = min(a.S, tid * per), s1 = min(a.S, s0 + per);
-  long long mine = 0;
-  for (int s = s0; s < s1; ++s) {
-    const int np = (clamp_ctx(a.ctx[s], a.max_blocks) + 15) >> 4;
-    mine += np > 0 ? (long long)a.Hkv * (np + kUnit) : 0;
-  }
-  long long ptot;
-  const long long before = block_exclusive_scan<kFinishThreads>(mine, s_warp_sums, ptot);
-  const long long T = max((ptot + a.ctas - 1) / a.ctas, (long long)kMinPagesPerCta);
-  const long long pos_begin = (long long)blockIdx.x * T, pos_end = min(ptot, pos_begin + T);
-  if (pos_begin >= ptot) return;
-  if (before <= pos_begin && pos_begin < before + mine) {
-    long long cum = before;
-    for (int s = s0; s < s1; ++s) {
-      const int np = (clamp_ctx(a.ctx[s], a.max_blocks) + 15) >> 4;
-      const long long n = np > 0 ? (long long)a.Hkv * (np + kUnit) : 0;
-      if (pos_begin < cum + n) {
-        s_seq = s;
-        s_off = pos_begin - cum;
-        s_cost = cum;
-        break;
-      }
-      cum += n;
-    }
-  }
-  __syncthreads();
-  int seq = s_seq;
+  const RangeStart rs = a.ranges[blockIdx.x];
+  if (rs.seq < 0) return;
+  int seq = rs.seq;
   int ctx = clamp_ctx(a.ctx[seq], a.max_blocks);
   int npages = (ctx + 15) >> 4;
-  int h = (int)(s_off / (npages + kUnit));
-  long long ucost = s_cost + (long long)h * (npages + kUnit);  // position of the unit's start
+  if (npages == 0) return;  // the lengths changed under the kernel
+  int h = (int)((rs.pos_begin - rs.cost) / (npages + kUnit));
+  long long ucost = rs.cost + (long long)h * (npages + kUnit);  // position of the unit's start
 
-  while (ucost < pos_end) {
+  while (ucost < rs.pos_end && h < a.Hkv) {
     // the unit's pages in this range
     const long long first = ucost + kUnit;  // position of page 0
-    const int pg0 = (int)max(0LL, pos_begin - first), pg1 = (int)min((long long)npages, pos_end - first);
-    if (pg1 > pg0) {
+    const int pg0 = (int)max(0LL, rs.pos_begin - first), pg1 = (int)min((long long)npages, rs.pos_end - first);
+    if (pg1 > pg0 && (pg0 > 0 || pg1 < npages)) {
       const size_t row0 = (size_t)seq * a.Hq + (size_t)h * a.G;
-      const bool whole = pg0 == 0 && pg1 == npages;
-      if (whole) {
-        if (tid < a.G) s_ml[tid] = a.row_ml[row0 + tid];
-      } else {
-        // pieces: CTA c0's partial, in the slot it recorded, and the first
-        // partials of CTAs c0 + 1 .. c1
-        const int c0 = (int)(first / T), c1 = (int)((first + npages - 1) / T);
-        const int n = c1 - c0 + 1, slot0 = 2 * c0 + (a.jobs[c0].w & 1);
-        if (warp < a.G) {
-          float M = -INFINITY, L = 0.f;
-          for (int i = lane; i < n; i += 32) {
-            const size_t p = (size_t)(i == 0 ? slot0 : 2 * (c0 + i)) * a.G + warp;
-            const float m = a.ws_ml[2 * p], l = a.ws_ml[2 * p + 1];
-            const float mn = fmaxf(M, m);
-            if (mn != -INFINITY) {
-              L = L * fast_exp2(M - mn) + l * fast_exp2(m - mn);
-              M = mn;
-            }
-          }
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) {
-            const float m = __shfl_xor_sync(kFull, M, off), l = __shfl_xor_sync(kFull, L, off);
-            const float mn = fmaxf(M, m);
-            if (mn != -INFINITY) {
-              L = L * fast_exp2(M - mn) + l * fast_exp2(m - mn);
-              M = mn;
-            }
-          }
-          if (lane == 0) s_ml[warp] = make_float2(M, 1.f / L);
-        }
-        __syncthreads();
-        // this CTA's slice of the output rows, 32 values at a time; the warps
-        // take the pieces in turn and are added up in warp order
-        const int groups = a.G * D / 32, slices = min(n, groups), me = (int)blockIdx.x - c0;
-        if (me < slices) {
-          for (int gi = me * groups / slices; gi < (me + 1) * groups / slices; ++gi) {
-            const int head = gi * 32 / D, dim = gi * 32 % D + lane;
-            const float M = s_ml[head].x;
-            float O = 0.f;
-            for (int i = warp; i < n; i += kFinishWarps) {
-              const size_t p = (size_t)(i == 0 ? slot0 : 2 * (c0 + i)) * a.G + head;
-              const float m = a.ws_ml[2 * p];
-              O += m == -INFINITY ? 0.f : fast_exp2(m - M) * a.ws_o[p * D + dim];
-            }
-            s_red[warp][lane] = O;
-            __syncthreads();
-            if (warp == 0) {
-              float sum = 0.f;
-#pragma unroll
-              for (int w = 0; w < kFinishWarps; ++w) sum += s_red[w][lane];
-              store_out<OUT>(a.out, (row0 + head) * D + dim, sum * s_ml[head].y * a.v_scale);
-            }
-            __syncthreads();
+      // pieces: CTA c0's partial, in the slot it recorded, and the first
+      // partials of CTAs c0 + 1 .. c1
+      const int c0 = (int)(first / rs.T), c1 = min((int)((first + npages - 1) / rs.T), a.ctas - 1);
+      const int n = c1 - c0 + 1, slot0 = 2 * c0 + (a.jobs[c0].w & 1);
+      if (warp < a.gs) {
+        float M = -INFINITY, L = 0.f;
+        for (int i = lane; i < n && warp < a.G; i += 32) {
+          const size_t p = (size_t)(i == 0 ? slot0 : 2 * (c0 + i)) * a.G + warp;
+          const float m = a.ws_ml[2 * p], l = a.ws_ml[2 * p + 1];
+          const float mn = fmaxf(M, m);
+          if (mn != -INFINITY) {
+            L = L * fast_exp2(M - mn) + l * fast_exp2(m - mn);
+            M = mn;
           }
         }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+          const float m = __shfl_xor_sync(kFull, M, off), l = __shfl_xor_sync(kFull, L, off);
+          const float mn = fmaxf(M, m);
+          if (mn != -INFINITY) {
+            L = L * fast_exp2(M - mn) + l * fast_exp2(m - mn);
+            M = mn;
+          }
+        }
+        if (lane == 0) s_ml[warp] = warp < a.G ? make_float2(M, 1.f / L) : make_float2(0.f, 0.f);
       }
       __syncthreads();
+      // this CTA's slice of the output rows, 32 values at a time.  Few pieces: a
+      // warp per 32 values adds them all up, its loads in flight together.  Many:
+      // the warps take the pieces in turn and are added up in warp order.
+      const int groups = a.G * D / 32, slices = min(n, groups), me = (int)blockIdx.x - c0;
+      const int g0 = me * groups / slices, g1 = me < slices && me >= 0 ? (me + 1) * groups / slices : g0;
+      auto piece = [&](int i) { return (size_t)(i == 0 ? slot0 : 2 * (c0 + i)) * a.G; };
+      if (n <= kFinishWarps) {
+        for (int gi = g0 + warp; gi < g1; gi += kFinishWarps) {
+          const int head = gi * 32 / D, dim = gi * 32 % D + lane;
+          float m[kFinishWarps], o[kFinishWarps];
+#pragma unroll
+          for (int i = 0; i < kFinishWarps; ++i) {
+            m[i] = -INFINITY;
+            o[i] = 0.f;
+            if (i < n) {
+              m[i] = a.ws_ml[2 * (piece(i) + head)];
+              o[i] = a.ws_o[(piece(i) + head) * D + dim];
+            }
+          }
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < kFinishWarps; ++i) sum += m[i] == -INFINITY ? 0.f : fast_exp2(m[i] - s_ml[head].x) * o[i];
+          store_out<OUT>(a.out, (row0 + head) * D + dim, sum * s_ml[head].y * a.v_scale);
+        }
+      } else {
+        for (int gi = g0; gi < g1; ++gi) {
+          const int head = gi * 32 / D, dim = gi * 32 % D + lane;
+          float O = 0.f;
+          for (int i = warp; i < n; i += kFinishWarps) {
+            const float m = a.ws_ml[2 * (piece(i) + head)];
+            O += m == -INFINITY ? 0.f : fast_exp2(m - s_ml[head].x) * a.ws_o[(piece(i) + head) * D + dim];
+          }
+          s_red[warp][lane] = O;
+          __syncthreads();
+          if (warp == 0) {
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kFinishWarps; ++w) sum += s_red[w][lane];
+            store_out<OUT>(a.out, (row0 + head) * D + dim, sum * s_ml[head].y * a.v_scale);
+          }
+          __syncthreads();
+        }
+      }
       // ---- the weights of tokens [16 pg0, min(ctx, 16 pg1))
-      const size_t unit = (size_t)seq * a.Hkv + h;
-      const float* sc = a.scores + unit * a.max_blocks * 16 * a.gs;
-      const float* wi = f.w_in ? f.w_in + unit * f.w_stride : nullptr;
-      float* wo = f.w_out + unit * f.w_stride;
-      int t1 = min(ctx, 16 * pg1);
-      if (t1 > f.w_stride) {
-        if (tid == 0) record_error(a.err, PA_ERR_BOUNDS);
-        t1 = (int)f.w_stride;
-      }
-      for (int t = 16 * pg0 + tid; t < t1; t += kFinishThreads) {
-        float w = wi ? f.decay * wi[t] : 0.f;
-        float p = 0.f;
-        for (int g = 0; g < a.G; ++g) p += fast_exp2(sc[(size_t)t * a.gs + g] - s_ml[g].x) * s_ml[g].y;
-        wo[t] = w + p;
-      }
+      const size_t unit = (size_t)seq * a.Hkv + h, row = unit * a.w_stride;
+      add_weights<kFinishThreads, 2>(a.scores + unit * a.max_blocks * 16 * a.gs, a.gs, s_ml,
+                                     a.w_in ? a.w_in + row : nullptr, a.w_out + row, a.decay, 16 * pg0,
+                                     totals_end(min(ctx, 16 * pg1), a));
       __syncthreads();  // s_ml is free again
     }
     ucost += npages + kUnit;
@@ -179,8 +145,7 @@ __global__ void __launch_bounds__(kFinishThreads) weights_finish_kernel(const De
 struct Kernels {
   const void* decode;
   int smem;
-  void (*finish)(const DecodeArgs, const FinishArgs);
-  cudaError_t (*launch)(const DecodeArgs&, const FinishArgs&, const CUtensorMap*, const CUtensorMap*, cudaStream_t);
+  cudaError_t (*launch)(const DecodeArgs&, const CUtensorMap*, const CUtensorMap*, cudaStream_t);
   int* occupancy;  // [128], per device; 0 = not yet configured
 };
 
@@ -189,8 +154,7 @@ struct Build {
   static constexpr bool kPsplit = (KV == KV_BF16) || (OUT == OUT_F32);
   static constexpr int kMinB = std::min(Cfg<KV, D>::kMinBlocks, 4);  // the schedule puts at most four CTAs on an SM
   static constexpr auto kDecode = &decode_bal_kernel<KV, D, OUT, kPsplit, kMinB, true>;
-  static cudaError_t launch(const DecodeArgs& a, const FinishArgs& f, const CUtensorMap* tk, const CUtensorMap* tv,
-                            cudaStream_t st) {
+  static cudaError_t launch(const DecodeArgs& a, const CUtensorMap* tk, const CUtensorMap* tv, cudaStream_t st) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -205,12 +169,11 @@ struct Build {
     if (e != cudaSuccess) return e;
     cfg.blockDim = dim3(kFinishThreads);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, weights_finish_kernel<KV, D, OUT>, a, f);
+    return cudaLaunchKernelEx(&cfg, weights_finish_kernel<KV, D, OUT>, a);
   }
   static Kernels get() {
     static int occupancy[128];
-    return {reinterpret_cast<const void*>(kDecode), BalCfg<KV, D>::kLaunchSmem, &weights_finish_kernel<KV, D, OUT>,
-            &launch, occupancy};
+    return {reinterpret_cast<const void*>(kDecode), BalCfg<KV, D>::kLaunchSmem, &launch, occupancy};
   }
 };
 
@@ -256,7 +219,7 @@ int configure(const Kernels& k, int* ctas) {
 
 // Parts of the workspace, in floats.
 struct Workspace {
-  size_t ml, jobs, rows, scores, total;
+  size_t ml, jobs, ranges, scores, total;
 };
 
 Workspace layout(int ctas, int S, int Hq, int Hkv, int D, int max_blocks) {
@@ -265,8 +228,8 @@ Workspace layout(int ctas, int S, int Hq, int Hkv, int D, int max_blocks) {
   Workspace w;
   w.ml = up(2 * (size_t)ctas * G * D);
   w.jobs = w.ml + up(2 * (size_t)ctas * G * 2);
-  w.rows = w.jobs + 4 * (size_t)ctas;
-  w.scores = w.rows + up(2 * (size_t)S * Hq);
+  w.ranges = w.jobs + 4 * (size_t)ctas;
+  w.scores = w.ranges + up(sizeof(RangeStart) / 4 * (size_t)ctas);
   w.total = w.scores + (size_t)S * Hkv * max_blocks * 16 * score_heads((int)G);
   return w;
 }
@@ -336,7 +299,7 @@ int pa_decode_weights(pa_pool* pool, int layer, void* out, int out_dtype, const 
   a.ws_o = base;
   a.ws_ml = base + ws.ml;
   a.jobs = reinterpret_cast<int4*>(base + ws.jobs);
-  a.row_ml = reinterpret_cast<float2*>(base + ws.rows);
+  a.ranges = reinterpret_cast<RangeStart*>(base + ws.ranges);
   a.scores = base + ws.scores;
   a.G = n_q_heads / Hkv;
   a.gs = score_heads(a.G);
@@ -350,6 +313,8 @@ int pa_decode_weights(pa_pool* pool, int layer, void* out, int out_dtype, const 
   a.ksc = pool->block_scaled ? layer_scales(pool, pool->k, layer) : nullptr;
   a.vsc = pool->block_scaled ? layer_scales(pool, pool->v, layer) : nullptr;
   a.err = err;
+  a.w_stride = (long long)weights_stride;
+  a.decay = decay;
   // one schedule holds at most kBalancedMaxSeqs sequences: larger batches in turn
   for (int s = 0; s < S; s += kBalancedMaxSeqs) {
     a.S = std::min(S - s, kBalancedMaxSeqs);
@@ -358,8 +323,9 @@ int pa_decode_weights(pa_pool* pool, int layer, void* out, int out_dtype, const 
     a.tables = block_tables_dev + (size_t)s * max_blocks_per_seq;
     a.ctx = ctx_lens_dev + s;
     const size_t at = (size_t)s * Hkv * weights_stride;
-    const FinishArgs f = {weights_in ? weights_in + at : nullptr, weights_out + at, (long long)weights_stride, decay};
-    const cudaError_t e = k.launch(a, f, tk, tv, static_cast<cudaStream_t>(stream));
+    a.w_in = weights_in ? weights_in + at : nullptr;
+    a.w_out = weights_out + at;
+    const cudaError_t e = k.launch(a, tk, tv, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "decode_weights launch: %s", cudaGetErrorString(e));
   }
   return PA_OK;
