@@ -190,11 +190,25 @@ __device__ __forceinline__ uint32_t tile_off(uint32_t off) {
   else return off;
 }
 
+// The largest first + i * step below end, i >= 0 (below first if there is none).
+__device__ __forceinline__ int last_round(int first, int end, int step) {
+  return end > first ? first + (end - 1 - first) / step * step : first - step;
+}
+
 // Stores two floats that are read again soon: L2 is asked to keep the line.
 __device__ __forceinline__ void store_kept(float* p, float a, float b) {
   uint64_t policy;
   asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(policy));
   asm volatile("st.global.L2::cache_hint.v2.f32 [%0], {%1, %2}, %3;" ::"l"(p), "f"(a), "f"(b), "l"(policy) : "memory");
+}
+
+// Drops a warp's round of scores from L2 once its lanes have used them: bytes
+// [0, bytes) at p (128-byte aligned; whole lines only, one per lane at a time)
+// need no write-back to HBM, for nothing reads them again.
+__device__ __forceinline__ void drop_lines(const float* p, int bytes) {
+  __syncwarp();
+  for (int at = 128 * (threadIdx.x & 31); at + 128 <= bytes; at += 32 * 128)
+    asm volatile("discard.global.L2 [%0], 128;" ::"l"(reinterpret_cast<const uint8_t*>(p) + at) : "memory");
 }
 
 // Turns the scores of tokens [t0, t1) of a unit (t0 a multiple of 16) into
@@ -219,7 +233,8 @@ __device__ __forceinline__ void add_weights(const float* sc, int gs, const float
       inv[g] = v.y;
     }
     const float4* s4 = reinterpret_cast<const float4*>(sc);
-    for (int base = t0 + warp * 64 * UNR; base < t1; base += NW * 64 * UNR) {
+    // from the last round back: the scores written last are the likeliest to be in L2
+    for (int base = last_round(t0 + warp * 64 * UNR, t1, NW * 64 * UNR); base >= t0; base -= NW * 64 * UNR) {
       float4 x[4 * UNR];
       float w[2 * UNR];
 #pragma unroll
@@ -248,11 +263,12 @@ __device__ __forceinline__ void add_weights(const float* sc, int gs, const float
         const float sum = lane & 1 ? other + p[1] : p[0] + other;
         if (t < t1) wo[t] = w[j] + sum;
       }
+      drop_lines(sc + (size_t)base * 8, min(64 * UNR, (t1 - base + 15) & ~15) * 32);
     }
   } else if (gs == 4) {
     const float2 m0 = ml[0], m1 = ml[1], m2 = ml[2], m3 = ml[3];
     const float4* s4 = reinterpret_cast<const float4*>(sc);
-    for (int base = t0 + warp * 128 * UNR; base < t1; base += NW * 128 * UNR) {
+    for (int base = last_round(t0 + warp * 128 * UNR, t1, NW * 128 * UNR); base >= t0; base -= NW * 128 * UNR) {
       float4 x[4 * UNR];
       float w[4 * UNR];
 #pragma unroll
@@ -269,6 +285,7 @@ __device__ __forceinline__ void add_weights(const float* sc, int gs, const float
                         fast_exp2(x[j].z - m2.x) * m2.y + fast_exp2(x[j].w - m3.x) * m3.y;
         if (t < t1) wo[t] = w[j] + p;
       }
+      drop_lines(sc + (size_t)base * 4, min(128 * UNR, (t1 - base + 15) & ~15) * 16);
     }
   } else if (gs == 1) {
     const float2 m = ml[0];

@@ -107,9 +107,20 @@ __global__ void __launch_bounds__(kFinishThreads, 4) weights_finish_kernel(const
         for (int gi = g0; gi < g1; ++gi) {
           const int head = gi * 32 / D, dim = gi * 32 % D + lane;
           float O = 0.f;
-          for (int i = warp; i < n; i += kFinishWarps) {
-            const float m = a.ws_ml[2 * (piece(i) + head)];
-            O += m == -INFINITY ? 0.f : fast_exp2(m - s_ml[head].x) * a.ws_o[(piece(i) + head) * D + dim];
+          for (int i0 = warp; i0 < n; i0 += 4 * kFinishWarps) {
+            float m[4], o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int i = i0 + j * kFinishWarps;
+              m[j] = -INFINITY;
+              o[j] = 0.f;
+              if (i < n) {
+                m[j] = a.ws_ml[2 * (piece(i) + head)];
+                o[j] = a.ws_o[(piece(i) + head) * D + dim];
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) O += m[j] == -INFINITY ? 0.f : fast_exp2(m[j] - s_ml[head].x) * o[j];
           }
           s_red[warp][lane] = O;
           __syncthreads();
@@ -229,7 +240,7 @@ Workspace layout(int ctas, int S, int Hq, int Hkv, int D, int max_blocks) {
   w.ml = up(2 * (size_t)ctas * G * D);
   w.jobs = w.ml + up(2 * (size_t)ctas * G * 2);
   w.ranges = w.jobs + 4 * (size_t)ctas;
-  w.scores = w.ranges + up(sizeof(RangeStart) / 4 * (size_t)ctas);
+  w.scores = w.ranges + up(sizeof(RangeStart) / 4 * (size_t)ctas) + 28;  // room to start on a 128-byte line
   w.total = w.scores + (size_t)S * Hkv * max_blocks * 16 * score_heads((int)G);
   return w;
 }
@@ -300,7 +311,7 @@ int pa_decode_weights(pa_pool* pool, int layer, void* out, int out_dtype, const 
   a.ws_ml = base + ws.ml;
   a.jobs = reinterpret_cast<int4*>(base + ws.jobs);
   a.ranges = reinterpret_cast<RangeStart*>(base + ws.ranges);
-  a.scores = base + ws.scores;
+  a.scores = reinterpret_cast<float*>(reinterpret_cast<uintptr_t>(base + ws.scores) & ~(uintptr_t)127);
   a.G = n_q_heads / Hkv;
   a.gs = score_heads(a.G);
   a.max_blocks = max_blocks_per_seq;
