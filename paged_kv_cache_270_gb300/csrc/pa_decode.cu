@@ -1059,6 +1059,7 @@ int decode_with_plan(pa_pool* pool, int layer, void* out, int out_dtype, const v
   a.ranges = nullptr;
   a.w_in = nullptr;
   a.w_out = nullptr;
+  a.whole = 0;
   const float log2e = 1.4426950408889634f;
   a.qk_scale_log2 = softmax_scale * log2e * (d.kv_dtype == PA_FP8_E4M3 ? d.k_scale : 1.f);
   a.v_scale = d.kv_dtype == PA_FP8_E4M3 ? d.v_scale : 1.f;

@@ -104,7 +104,8 @@ struct DecodeArgs {
   // schedule [ctas], and the running totals [S][Hkv][w_stride]
   float* scores;
   struct RangeStart* ranges;
-  int gs;  // G, or the next even number (8-byte stores)
+  int gs;     // G, or the next even number (8-byte stores)
+  int whole;  // a CTA takes whole units (every unit costs 1), so none is left over
   const float* w_in;  // nullptr: zeros
   float* w_out;
   long long w_stride;
@@ -703,6 +704,8 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_bal_kernel(const Decode
   // cost; the real pages of position x are R(x) = Hkv * (pages before s) +
   // h * n + max(0, v - kUnit) for x in unit h of s at offset v.
   constexpr int kUnit = B::kUnitCostPages;
+  const bool whole = SC && a.whole;
+  auto span = [&](int np) { return whole ? 1 : np + kUnit; };  // a unit's cost
   const int per = (a.S + kThreads - 1) / kThreads;
   const int s0 = min(a.S, (int)threadIdx.x * per), s1 = min(a.S, s0 + per);
   long long mine = 0, mine_pg = 0;
@@ -714,14 +717,14 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_bal_kernel(const Decode
     }
     const int np = (c + 15) >> 4;
     mine_pg += np;
-    mine += np > 0 ? (long long)a.Hkv * (np + kUnit) : 0;
+    mine += np > 0 ? (long long)a.Hkv * span(np) : 0;
   }
   long long total, total_pg;
   const long long before = block_exclusive_scan<kThreads>(mine, s_warp_sums, total);
   __syncthreads();  // the scan's partial sums are read before the second scan writes them
   const long long before_pg = block_exclusive_scan<kThreads>(mine_pg, s_warp_sums, total_pg);
   const long long ptot = total;  // in cost
-  const long long T = max((ptot + a.ctas - 1) / a.ctas, (long long)kMinPagesPerCta);
+  const long long T = max((ptot + a.ctas - 1) / a.ctas, whole ? 1LL : (long long)kMinPagesPerCta);
   const long long pos_begin = (long long)blockIdx.x * T;
   const long long pos_end = min(ptot, pos_begin + T);
   // Sequences without context get a zero output row, written by CTA s mod ctas.
@@ -734,9 +737,9 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_bal_kernel(const Decode
     long long cum = before, cum_pg = before_pg * a.Hkv;
     for (int s = s0; s < s1; ++s) {
       const long long np = (clamp_ctx(a.ctx[s], a.max_blocks) + 15) >> 4;
-      const long long n = np > 0 ? a.Hkv * (np + kUnit) : 0;
+      const long long n = np > 0 ? (long long)a.Hkv * span((int)np) : 0;
       if (x < cum + n) {
-        const long long off = x - cum, hh = off / (np + kUnit), v = off - hh * (np + kUnit);
+        const long long off = x - cum, hh = off / span((int)np), v = off - hh * span((int)np);
         const long long r = cum_pg + hh * np + max(0LL, v - kUnit);
         if (start) {
           s_start_seq = s;
@@ -789,8 +792,8 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_bal_kernel(const Decode
     int seq = s_start_seq;
     int ctx = clamp_ctx(a.ctx[seq], a.max_blocks);
     int npages = (ctx + 15) >> 4;
-    int h = (int)(s_start_off / (npages + kUnit));
-    const int v0 = (int)(s_start_off - (long long)h * (npages + kUnit));
+    int h = (int)(s_start_off / span(npages));
+    const int v0 = (int)(s_start_off - (long long)h * span(npages));
     int pg0 = max(0, v0 - kUnit);
     long long ucost = pos_begin - v0;  // cost position of the current unit's start
     int left = n_pages;                // real pages still to stream
@@ -872,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_bal_kernel(const Decode
       left -= len;
       if (left <= 0) break;
       // the next unit, from its first page
-      ucost += npages + kUnit;
+      ucost += span(npages);
       pg0 = 0;
       if (++h == a.Hkv) {
         h = 0;

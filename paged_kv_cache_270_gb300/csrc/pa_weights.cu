@@ -19,6 +19,14 @@
 namespace pa {
 namespace {
 
+// When a CTA takes whole units (one kernel) in the place of equal ranges (two):
+// the pages of the busiest CTA are at most kWholeMost, and at most kWholeExtra
+// more than an equal share, if every context is as long as its table.  Measured
+// both ways (us, one kernel against two): 8 units of 7 pages 7.2 / 12.3, of 16
+// 9.2 / 10.7, of 32 13.0 / 10.6; 256 units of 32 pages (14 extra) 19.8 / 22.6, of
+// 64 (28) 32.3 / 31.8; 512 of 64 (10) 33.9 / 45.0, of 128 (20) 57.1 / 63.3 and
+// 46.4 / 45.1 with most contexts half as long; 800 of 32 (22) 39.5 / 41.6.
+constexpr int kWholeMost = 128, kWholeExtra = 20;
 constexpr int kFinishThreads = 256;
 constexpr int kFinishWarps = kFinishThreads / 32;
 
@@ -177,7 +185,7 @@ struct Build {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kDecode, a, *tk, *tv);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || a.whole) return e;
     cfg.blockDim = dim3(kFinishThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, weights_finish_kernel<KV, D, OUT>, a);
@@ -326,6 +334,9 @@ int pa_decode_weights(pa_pool* pool, int layer, void* out, int out_dtype, const 
   a.err = err;
   a.w_stride = (long long)weights_stride;
   a.decay = decay;
+  const long long units = (long long)std::min(S, kBalancedMaxSeqs) * Hkv;
+  const long long most = (units + ctas - 1) / ctas * max_blocks_per_seq, share = units * max_blocks_per_seq / ctas;
+  a.whole = most <= kWholeMost && most - share <= kWholeExtra;
   // one schedule holds at most kBalancedMaxSeqs sequences: larger batches in turn
   for (int s = 0; s < S; s += kBalancedMaxSeqs) {
     a.S = std::min(S - s, kBalancedMaxSeqs);

@@ -23,8 +23,16 @@ _OUT_CODES = {v: k for k, v in _TORCH_OUT.items()}
 
 
 def _stream_handle(stream=None) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return int(s.cuda_stream)
+    if stream is None:  # the current device's current stream, without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return int(stream.cuda_stream)
+
+
+def _all_need(device, *tensors) -> None:
+    """_need of several (tensor, name, dtype), quick where all is well."""
+    for t, name, dtype in tensors:
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.is_contiguous()):
+            _need(t, name, dtype, device)
 
 
 def _need(t: torch.Tensor, name: str, dtype=None, device=None):
@@ -62,11 +70,11 @@ def make_rope(rot_dim: int, layout: str = "half", theta: float = 10000.0, scalin
 def _token_rows(t: torch.Tensor, name: str, dtype, device) -> int:
     """The token stride, in elements, of a [T, heads, head_dim] tensor whose tokens may lie
     apart (a slice of a fused projection) but are contiguous in themselves."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [T, heads, head_dim]")
@@ -164,6 +172,15 @@ class KVPool:
         return buf[off:off + n].view(torch.float32).view(self.num_blocks, self.n_kv_heads)
 
     # --------------------------------------------------------- device calls
+    def _launch(self, call, args, stream) -> None:
+        """call(*args, stream) with the pool's device current: the library launches there,
+        and without a stream given it is that device's current one."""
+        if torch._C._cuda_getDevice() == self.device.index:
+            call(*args, _stream_handle(stream))
+        else:
+            with torch.cuda.device(self.device):
+                call(*args, _stream_handle(stream))
+
     def reshape_and_cache(self, k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
                           layer: int = 0, stream=None) -> None:
         _need(k, "k", self.in_dtype, self.device)
@@ -184,8 +201,7 @@ class KVPool:
         qs = _token_rows(q, "q", self.in_dtype, self.device)
         ks = _token_rows(k, "k", self.in_dtype, self.device)
         vs = _token_rows(v, "v", self.in_dtype, self.device)
-        _need(positions, "positions", torch.int32, self.device)
-        _need(slot_mapping, "slot_mapping", torch.int64, self.device)
+        _all_need(self.device, (positions, "positions", torch.int32), (slot_mapping, "slot_mapping", torch.int64))
         T, Hq, D = q.shape
         kv = (T, self.n_kv_heads, self.head_dim)
         if D != self.head_dim or k.shape != kv or v.shape != kv:
@@ -194,12 +210,13 @@ class KVPool:
             raise ValueError("positions and slot_mapping must hold one entry per token")
         if q_out is None:
             q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=self.device)
-        _need(q_out, "q_out", self.in_dtype, self.device)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-        N.pa_rope_and_cache(self.handle, layer, rope, q.data_ptr(), qs, q_out.data_ptr(), Hq,
-                            k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(),
-                            slot_mapping.data_ptr(), T, _stream_handle(stream))
+        else:
+            _need(q_out, "q_out", self.in_dtype, self.device)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+        self._launch(N.pa_rope_and_cache,
+                     (self.handle, layer, rope, q.data_ptr(), qs, q_out.data_ptr(), Hq, k.data_ptr(), ks,
+                      v.data_ptr(), vs, positions.data_ptr(), slot_mapping.data_ptr(), T), stream)
         return q_out
 
     def copy_blocks(self, pairs: torch.Tensor, layer: int = 0, stream=None) -> None:
@@ -267,7 +284,8 @@ class KVPool:
         return out
 
     def weights_workspace_bytes(self, S: int, n_q_heads: int, max_blocks_per_seq: int) -> int:
-        return N.pa_decode_weights_workspace_bytes(self.handle, S, n_q_heads, max_blocks_per_seq)
+        with torch.cuda.device(self.device):
+            return N.pa_decode_weights_workspace_bytes(self.handle, S, n_q_heads, max_blocks_per_seq)
 
     def decode_weights(self, q: torch.Tensor, block_tables: torch.Tensor, ctx_lens: torch.Tensor,
                        weights: torch.Tensor | None, weights_out: torch.Tensor | None = None,
@@ -277,40 +295,40 @@ class KVPool:
         """``decode`` that also adds each token's attention weight to its running total:
         `weights` fp32 [S, n_kv_heads, tokens], updated in place unless `weights_out` is
         given (None: totals that start at zero).  Returns (out, weights_out)."""
-        _need(q, "q", self.in_dtype, self.device)
-        _need(block_tables, "block_tables", torch.int32, self.device)
-        _need(ctx_lens, "ctx_lens", torch.int32, self.device)
+        dev = self.device
+        if weights_out is None:
+            weights_out = weights
+        _all_need(dev, (q, "q", self.in_dtype), (block_tables, "block_tables", torch.int32),
+                  (ctx_lens, "ctx_lens", torch.int32), (weights_out, "weights_out", torch.float32))
         S, Hq, D = q.shape
         if D != self.head_dim:
             raise ValueError("q head_dim mismatch")
         if block_tables.dim() != 2 or block_tables.shape[0] != S or ctx_lens.numel() != S:
             raise ValueError("block_tables must be [S, max_blocks] and ctx_lens [S]")
         max_blocks = block_tables.shape[1]
-        if weights_out is None:
-            weights_out = weights
-        _need(weights_out, "weights_out", torch.float32, self.device)
         if weights_out.dim() != 3 or weights_out.shape[:2] != (S, self.n_kv_heads):
             raise ValueError("weights must be [S, n_kv_heads, tokens]")
         if weights is not None and weights is not weights_out:
-            _need(weights, "weights", torch.float32, self.device)
+            _need(weights, "weights", torch.float32, dev)
             if weights.shape != weights_out.shape:
                 raise ValueError("weights and weights_out must have one shape")
         if out is None:
-            out = torch.empty((S, Hq, D), dtype=out_dtype or q.dtype, device=self.device)
-        _need(out, "out", None, self.device)
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
+            out = torch.empty((S, Hq, D), dtype=out_dtype or q.dtype, device=dev)
+        else:
+            _need(out, "out", None, dev)
+            if out.shape != q.shape:
+                raise ValueError("out must have q's shape")
         if softmax_scale is None:
             softmax_scale = 1.0 / math.sqrt(D)
         if workspace is None:
             workspace = torch.empty(self.weights_workspace_bytes(S, Hq, max_blocks),
-                                    dtype=torch.uint8, device=self.device)
-        N.pa_decode_weights(self.handle, layer, out.data_ptr(), _OUT_CODES[out.dtype], q.data_ptr(),
-                            block_tables.data_ptr(), max_blocks, ctx_lens.data_ptr(), S, Hq,
-                            softmax_scale, weights.data_ptr() if weights is not None else 0,
-                            weights_out.data_ptr(), weights_out.shape[2], decay,
-                            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                            _stream_handle(stream))
+                                    dtype=torch.uint8, device=dev)
+        self._launch(N.pa_decode_weights,
+                     (self.handle, layer, out.data_ptr(), _OUT_CODES[out.dtype], q.data_ptr(),
+                      block_tables.data_ptr(), max_blocks, ctx_lens.data_ptr(), S, Hq, softmax_scale,
+                      weights.data_ptr() if weights is not None else 0, weights_out.data_ptr(),
+                      weights_out.shape[2], decay, workspace.data_ptr(),
+                      workspace.numel() * workspace.element_size()), stream)
         return out, weights_out
 
     def evict_select(self, weights: torch.Tensor, ctx_lens: torch.Tensor, budget: int, sinks: int = 0,
@@ -319,21 +337,21 @@ class KVPool:
         """The tokens that stay when each sequence is cut to `budget`: the first `sinks`, the
         last `recent` and the heaviest in between, by their totals `weights` [S, heads, tokens].
         Returns (keep int32 [S, heads, budget], ascending, -1 behind; kept_lens int32 [S])."""
-        _need(weights, "weights", torch.float32, self.device)
-        _need(ctx_lens, "ctx_lens", torch.int32, self.device)
+        dev = self.device
+        _all_need(dev, (weights, "weights", torch.float32), (ctx_lens, "ctx_lens", torch.int32))
         if weights.dim() != 3 or ctx_lens.numel() != weights.shape[0]:
             raise ValueError("weights must be [S, heads, tokens] and ctx_lens [S]")
         S, H, tokens = weights.shape
         if keep is None:
-            keep = torch.empty((S, H, budget), dtype=torch.int32, device=self.device)
+            keep = torch.empty((S, H, budget), dtype=torch.int32, device=dev)
         if kept_lens is None:
-            kept_lens = torch.empty(S, dtype=torch.int32, device=self.device)
-        _need(keep, "keep", torch.int32, self.device)
-        _need(kept_lens, "kept_lens", torch.int32, self.device)
+            kept_lens = torch.empty(S, dtype=torch.int32, device=dev)
+        _all_need(dev, (keep, "keep", torch.int32), (kept_lens, "kept_lens", torch.int32))
         if keep.shape != (S, H, budget) or kept_lens.numel() != S:
             raise ValueError("keep must be [S, heads, budget] and kept_lens [S]")
-        N.pa_evict_select(self.handle, weights.data_ptr(), tokens, ctx_lens.data_ptr(), S, H, budget,
-                          sinks, recent, keep.data_ptr(), kept_lens.data_ptr(), _stream_handle(stream))
+        self._launch(N.pa_evict_select,
+                     (self.handle, weights.data_ptr(), tokens, ctx_lens.data_ptr(), S, H, budget, sinks,
+                      recent, keep.data_ptr(), kept_lens.data_ptr()), stream)
         return keep, kept_lens
 
     def evict_compact(self, keep: torch.Tensor, kept_lens: torch.Tensor, block_tables: torch.Tensor,
@@ -342,10 +360,8 @@ class KVPool:
         """Copy the kept tokens of `block_tables` together into the blocks of `dst_tables`
         (freshly allocated ones), and their totals from `weights` into `weights_out`, whose rows
         are zeroed behind them (a new tensor of the same shape when not given).  Returns weights_out."""
-        _need(keep, "keep", torch.int32, self.device)
-        _need(kept_lens, "kept_lens", torch.int32, self.device)
-        _need(block_tables, "block_tables", torch.int32, self.device)
-        _need(dst_tables, "dst_tables", torch.int32, self.device)
+        _all_need(self.device, (keep, "keep", torch.int32), (kept_lens, "kept_lens", torch.int32),
+                  (block_tables, "block_tables", torch.int32), (dst_tables, "dst_tables", torch.int32))
         if keep.dim() != 3:
             raise ValueError("keep must be [S, heads, budget]")
         S, H, budget = keep.shape
@@ -358,16 +374,16 @@ class KVPool:
         if weights is not None:
             if weights_out is None:
                 weights_out = torch.empty_like(weights)
+            _all_need(self.device, (weights, "weights", torch.float32), (weights_out, "weights_out", torch.float32))
             for t, name in ((weights, "weights"), (weights_out, "weights_out")):
-                _need(t, name, torch.float32, self.device)
                 if t.dim() != 3 or t.shape[:2] != (S, H):
                     raise ValueError(f"{name} must be [S, heads, tokens] with keep's heads")
             w_in, in_stride = weights.data_ptr(), weights.shape[2]
             w_out, out_stride = weights_out.data_ptr(), weights_out.shape[2]
-        N.pa_evict_compact(self.handle, layer, keep.data_ptr(), H, budget, kept_lens.data_ptr(),
-                           block_tables.data_ptr(), block_tables.shape[1], dst_tables.data_ptr(),
-                           dst_tables.shape[1], S, w_in, in_stride, w_out, out_stride,
-                           _stream_handle(stream))
+        self._launch(N.pa_evict_compact,
+                     (self.handle, layer, keep.data_ptr(), H, budget, kept_lens.data_ptr(),
+                      block_tables.data_ptr(), block_tables.shape[1], dst_tables.data_ptr(),
+                      dst_tables.shape[1], S, w_in, in_stride, w_out, out_stride), stream)
         return weights_out
 
     def prefill(self, q: torch.Tensor, q_start: torch.Tensor, block_tables: torch.Tensor,
