@@ -9,9 +9,9 @@
 // signed fraction of half a turn are the argument of sincospi.
 //
 // The work is a copy with some arithmetic in it, bound by HBM: 16-byte loads
-// and stores, each thread owning both halves of eight pairs, and the
-// sin / cos of a token computed once per CTA, in shared memory, for all
-// its heads.
+// and stores, each thread owning both halves of eight pairs.  A warp makes its
+// token's table of sin / cos in shared memory, for all the heads it takes, while its
+// first loads are in flight; no warp waits for another.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -27,7 +27,13 @@ namespace {
 // vector), or HALF with any even rot_dim (partners read one by one).
 enum RopeLayout { ROPE_HALF = 0, ROPE_INTER = 1, ROPE_HALF_ODD = 2 };
 
-constexpr int kRopeMaxTokens = 8;  // tokens per CTA when the heads are few
+constexpr int kRopeWarps = 8;  // per CTA
+// A token gets one warp, or up to eight while the call has fewer than this many
+// warps: each warp makes its own table, so more warps a token cost instructions,
+// fewer leave SMs idle.  64 tokens of 32 / 8 heads (bf16): 6.1 us with one warp a
+// token, 3.5 with eight; 1024 of 64 / 8 (FP8): 17.3 with one, 12.6 with two, 13.8
+// with eight; 8192: 56 us with one or two (5.7 TB/s), 83 with eight.
+constexpr int kRopeFewWarps = 2048;
 
 struct RopeArgs {
   const uint16_t* q;
@@ -38,7 +44,8 @@ struct RopeArgs {
   const int32_t* pos;
   const int64_t* slots;
   int T, Hq, Hkv;
-  int tokens_per_cta;
+  int warps_per_token;     // 1, 2, 4 or 8
+  unsigned q_ctas, parts;  // block-scaled pools
   long long num_slots;
   uint8_t* kpool;
   uint8_t* vpool;
@@ -94,8 +101,8 @@ struct UnitIn {
   uint16_t partner[LAY == ROPE_HALF_ODD ? 16 : 1];
 };
 
-template <int LAY>
-__device__ __forceinline__ void load_unit(const uint16_t* row, int u, int rot, bool turns, UnitIn<LAY>& in) {
+template <int LAY, bool FULL>
+__device__ __forceinline__ void load_unit(const uint16_t* row, int u, int rot, UnitIn<LAY>& in) {
   int v0, v1;
   unit_vecs<LAY>(u, rot, v0, v1);
   in.x0 = *reinterpret_cast<const uint4*>(row + 8 * v0);
@@ -105,15 +112,14 @@ __device__ __forceinline__ void load_unit(const uint16_t* row, int u, int rot, b
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const int e = 16 * u + j;
-      in.partner[j] = turns && e < rot ? row[e < half ? e + half : e - half] : 0;
+      in.partner[j] = e < rot ? row[e < half ? e + half : e - half] : 0;
     }
   }
 }
 
-// The unit's 16 values after the rotation (turns) or as they are.
-template <bool BF, int D, int LAY>
-__device__ __forceinline__ void turn_unit(const UnitIn<LAY>& in, int u, int rot, bool turns, const float2* cs,
-                                          float (&y)[16]) {
+// The unit's 16 values as they are.
+template <bool BF, int LAY>
+__device__ __forceinline__ void plain_unit(const UnitIn<LAY>& in, float (&y)[16]) {
   uint32_t w0[4], w1[4];
   words(in.x0, w0);
   words(in.x1, w1);
@@ -125,9 +131,14 @@ __device__ __forceinline__ void turn_unit(const UnitIn<LAY>& in, int u, int rot,
     y[8 + 2 * j] = b.x;
     y[8 + 2 * j + 1] = b.y;
   }
-  if (!turns) return;
+}
+
+// The unit's 16 values after the rotation.  FULL: all of the row turns.
+template <bool BF, int D, int LAY, bool FULL>
+__device__ __forceinline__ void turn_unit(const UnitIn<LAY>& in, int u, int rot, const float2* cs, float (&y)[16]) {
+  plain_unit<BF, LAY>(in, y);
   if constexpr (LAY == ROPE_HALF) {
-    if (u >= (rot >> 4)) return;
+    if (!FULL && u >= (rot >> 4)) return;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float4 t = reinterpret_cast<const float4*>(cs)[j * (D / 16) + u];
@@ -142,11 +153,11 @@ __device__ __forceinline__ void turn_unit(const UnitIn<LAY>& in, int u, int rot,
     for (int j = 0; j < 4; ++j) {
       const float4 t = reinterpret_cast<const float4*>(cs)[j * (D / 16) + u];
       const float a0 = y[4 * j], b0 = y[4 * j + 1], a1 = y[4 * j + 2], b1 = y[4 * j + 3];
-      if (16 * u + 4 * j < rot) {
+      if (FULL || 16 * u + 4 * j < rot) {
         y[4 * j] = a0 * t.x - b0 * t.y;
         y[4 * j + 1] = b0 * t.x + a0 * t.y;
       }
-      if (16 * u + 4 * j + 2 < rot) {
+      if (FULL || 16 * u + 4 * j + 2 < rot) {
         y[4 * j + 2] = a1 * t.z - b1 * t.w;
         y[4 * j + 3] = b1 * t.z + a1 * t.w;
       }
@@ -183,144 +194,197 @@ __device__ __forceinline__ uint2 codes8(const float* y, float s) {
   return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
 }
 
-// Rows [0, rows) of `ntok` tokens from t0 on: row r < Hq is query head r, then
-// the key and the value heads.  A CTA takes its items (token, row, unit)
-// IPT at a time per thread, every load of a batch issued before the first use.
-template <bool BF, bool FP8, int D, int LAY>
-__device__ __forceinline__ void rope_rows(const RopeArgs& a, int t0, int ntok, int rows, float2 (*cs)[D / 2]) {
+// Items [lt, items) of one token's heads, `nt` apart: item i is unit i % UNITS of
+// head i / UNITS, IPT of them at a time, every load of a batch issued before the
+// first use.  `first` runs behind the first batch's loads (the token's table);
+// put(h, v0, v1, in, y) stores the turned unit.
+template <bool BF, int D, int LAY, bool FULL, typename First, typename Put>
+__device__ __forceinline__ void turn_heads(const uint16_t* src, int items, int rot, int lt, int nt, const float2* cs,
+                                           First first, Put put) {
   constexpr int UNITS = D / 16, IPT = LAY == ROPE_HALF_ODD ? 1 : 2;
-  const int tid = threadIdx.x, nt = blockDim.x;
-  const int rot = a.rope.rot_dim;
-  const int per_token = rows * UNITS, total = ntok * per_token;
-  for (int base = 0; base < total; base += nt * IPT) {
+  for (int base = lt; base < items || base == lt; base += nt * IPT) {
     UnitIn<LAY> in[IPT];
-    int tok[IPT], row[IPT], unit[IPT];
 #pragma unroll
-    for (int k = 0; k < IPT; ++k) {
-      const int item = base + k * nt + tid;
-      row[k] = -1;
-      if (item < total) {
-        tok[k] = item / per_token;
-        const int r = item - tok[k] * per_token;
-        row[k] = r / UNITS;
-        unit[k] = r % UNITS;
-        const long long t = t0 + tok[k];
-        const uint16_t* src = row[k] < a.Hq            ? a.q + t * a.qs + (long long)row[k] * D
-                              : row[k] < a.Hq + a.Hkv ? a.k + t * a.ks + (long long)(row[k] - a.Hq) * D
-                                                      : a.v + t * a.vs + (long long)(row[k] - a.Hq - a.Hkv) * D;
-        load_unit<LAY>(src, unit[k], rot, row[k] < a.Hq + a.Hkv, in[k]);
-      }
+    for (int j = 0; j < IPT; ++j) {
+      const int i = base + j * nt;
+      if (i < items) load_unit<LAY, FULL>(src + (i / UNITS) * D, i % UNITS, FULL ? D : rot, in[j]);
     }
-    if (base == 0) {  // the tokens' tables, while the first loads are in flight
-      for (int i = tid; i < ntok * (rot >> 1); i += nt) {
-        const int tk = i / (rot >> 1), p = i - tk * (rot >> 1);
-        cs[tk][cs_index<D, LAY>(p)] = turn(a.rope, p, a.pos[t0 + tk]);
-      }
-      __syncthreads();
-    }
-    // A row's units sit in one warp: with q_out == q its partners are read
-    // (above) before any lane writes the row.
+    if (base == lt) first();
+    // The table is complete; and with q_out == q a row's partners, which its own
+    // warp reads (above), are read before any lane writes the row.
     __syncwarp();
 #pragma unroll
-    for (int k = 0; k < IPT; ++k) {
-      if (row[k] < 0) continue;
-      int v0, v1;
-      unit_vecs<LAY>(unit[k], rot, v0, v1);
-      const long long t = t0 + tok[k];
-      const bool is_v = row[k] >= a.Hq + a.Hkv;
-      float y[16];
-      turn_unit<BF, D, LAY>(in[k], unit[k], rot, !is_v, cs[tok[k]], y);
-      if (row[k] < a.Hq) {
-        uint16_t* dst = a.q_out + (t * a.Hq + row[k]) * D;
-        *reinterpret_cast<uint4*>(dst + 8 * v0) = pack8<BF>(y);
-        *reinterpret_cast<uint4*>(dst + 8 * v1) = pack8<BF>(y + 8);
-        continue;
-      }
-      const int64_t slot = a.slots[t];
-      if (slot < 0) continue;
-      if (slot >= a.num_slots) {
-        record_error(a.err, PA_ERR_BOUNDS);
-        continue;
-      }
-      const int h = row[k] - a.Hq - (is_v ? a.Hkv : 0);
-      const long long e = (((slot >> 4) * a.Hkv + h) * 16 + (slot & 15)) * (long long)D;
-      uint8_t* pool = is_v ? a.vpool : a.kpool;
-      if constexpr (FP8) {
-        const float s = is_v ? a.v_scale : a.k_scale;
-        *reinterpret_cast<uint2*>(pool + e + 8 * v0) = codes8(y, s);
-        *reinterpret_cast<uint2*>(pool + e + 8 * v1) = codes8(y + 8, s);
-      } else {
-        *reinterpret_cast<uint4*>(pool + 2 * (e + 8 * v0)) = is_v ? in[k].x0 : pack8<BF>(y);
-        *reinterpret_cast<uint4*>(pool + 2 * (e + 8 * v1)) = is_v ? in[k].x1 : pack8<BF>(y + 8);
+    for (int j = 0; j < IPT; ++j) {
+      const int i = base + j * nt;
+      if (i < items) {
+        int v0, v1;
+        unit_vecs<LAY>(i % UNITS, FULL ? D : rot, v0, v1);
+        float y[16];
+        turn_unit<BF, D, LAY, FULL>(in[j], i % UNITS, FULL ? D : rot, cs, y);
+        put(i / UNITS, v0, v1, y);
       }
     }
   }
 }
 
-template <bool BF, bool FP8, int D, int LAY>
-__global__ void __launch_bounds__(320) rope_cache_kernel(const __grid_constant__ RopeArgs a) {
-  __shared__ __align__(16) float2 cs[kRopeMaxTokens][D / 2];
-  grid_dependents_launch();  // a decode behind this kernel waits for its writes itself
-  const int t0 = blockIdx.x * a.tokens_per_cta;
-  rope_rows<BF, FP8, D, LAY>(a, t0, min(a.tokens_per_cta, a.T - t0), a.Hq + 2 * a.Hkv, cs);
+// One token by `nt` threads (whole warps) of which this is `lt`: its query heads,
+// then (KV) its key and value heads into their slot.  cs: this warp's table.
+template <bool BF, bool FP8, bool KV, int D, int LAY, bool FULL>
+__device__ __forceinline__ void rope_token(const RopeArgs& a, int t, int lt, int nt, float2* cs) {
+  constexpr int UNITS = D / 16;
+  const int rot = FULL ? D : a.rope.rot_dim;
+  uint16_t* q_out = a.q_out + (long long)t * a.Hq * D;
+  turn_heads<BF, D, LAY, FULL>(
+      a.q + t * a.qs, a.Hq * UNITS, rot, lt, nt, cs,
+      [&] {
+        const int p = a.pos[t];
+        for (int i = lt & 31; i < (rot >> 1); i += 32) cs[cs_index<D, LAY>(i)] = turn(a.rope, i, p);
+      },
+      [&](int h, int v0, int v1, const float* y) {
+        *reinterpret_cast<uint4*>(q_out + h * D + 8 * v0) = pack8<BF>(y);
+        *reinterpret_cast<uint4*>(q_out + h * D + 8 * v1) = pack8<BF>(y + 8);
+      });
+  if constexpr (KV) {
+    const int64_t slot = a.slots[t];
+    if (slot >= a.num_slots && lt == 0) record_error(a.err, PA_ERR_BOUNDS);
+    if (slot < 0 || slot >= a.num_slots) return;
+    // element (h, offset, d) of the slot's block
+    const long long e0 = ((slot >> 4) * a.Hkv * 16 + (slot & 15)) * (long long)D;
+    constexpr int EB = FP8 ? 1 : 2;
+    uint8_t* kp = a.kpool + EB * e0;
+    uint8_t* vp = a.vpool + EB * e0;
+    turn_heads<BF, D, LAY, FULL>(
+        a.k + t * a.ks, a.Hkv * UNITS, rot, lt, nt, cs, [] {},
+        [&](int h, int v0, int v1, const float* y) {
+          uint8_t* dst = kp + (long long)h * (16 * D * EB);
+          if constexpr (FP8) {
+            *reinterpret_cast<uint2*>(dst + 8 * v0) = codes8(y, a.k_scale);
+            *reinterpret_cast<uint2*>(dst + 8 * v1) = codes8(y + 8, a.k_scale);
+          } else {
+            *reinterpret_cast<uint4*>(dst + 16 * v0) = pack8<BF>(y);
+            *reinterpret_cast<uint4*>(dst + 16 * v1) = pack8<BF>(y + 8);
+          }
+        });
+    // values: whole vectors, unchanged or encoded
+    const uint16_t* v = a.v + t * a.vs;
+    for (int i = lt; i < a.Hkv * (D / 8); i += nt) {
+      const uint4 x = *reinterpret_cast<const uint4*>(v + 8 * i);
+      uint8_t* dst = vp + (long long)(i / (D / 8)) * (16 * D * EB) + (i % (D / 8)) * (8 * EB);
+      if constexpr (FP8) {
+        uint32_t w[4];
+        words(x, w);
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 u = unpack2<BF>(w[j]);
+          y[2 * j] = u.x;
+          y[2 * j + 1] = u.y;
+        }
+        *reinterpret_cast<uint2*>(dst) = codes8(y, a.v_scale);
+      } else {
+        *reinterpret_cast<uint4*>(dst) = x;
+      }
+    }
+  }
 }
 
-// Block-scaled pools: CTA (t, 0) turns token t's queries; CTA (t, y > 0) takes,
-// if t starts a run (see reshape_block_scaled_kernel), eight (K or V, head)
-// tiles of the run, one per warp.  A run's rows of one tile, at most 16 x D
-// values, stay in the warp's registers between the maximum and the encoding.
+// FULL: every dimension turns (ROPE_HALF and ROPE_INTER).
+template <bool BF, bool FP8, int D, int LAY, bool FULL>
+__global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_cache_kernel(const __grid_constant__ RopeArgs a) {
+  __shared__ __align__(16) float2 cs[kRopeWarps][D / 2];
+  grid_dependents_launch();  // a decode behind this kernel waits for its writes itself
+  const int warp = threadIdx.x >> 5, wpt = a.warps_per_token, tok = warp / wpt;
+  const int t = blockIdx.x * (kRopeWarps / wpt) + tok;
+  if (t < a.T)
+    rope_token<BF, FP8, true, D, LAY, FULL>(a, t, threadIdx.x - tok * wpt * 32, wpt * 32, cs[warp]);
+}
+
+// Block-scaled pools.  The first a.q_ctas CTAs turn queries as above.  Then come, for
+// each token, a.parts CTAs: K and V of eight heads each; those of a token that
+// starts a run (see reshape_block_scaled_kernel) take the run, a warp per (K or V, head)
+// tile.  A run's rows of one tile, at most 16 x D values, stay in the warp's
+// registers as they were loaded; they are turned twice, for the maximum and for
+// the encoding, which costs less than the registers of the fp32 values would
+// (four CTAs on an SM in the place of two).
 template <int D, int LAY>
-__global__ void __launch_bounds__(256) rope_cache_block_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_cache_block_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ __align__(16) float2 cs[16][D / 2];
   grid_dependents_launch();
-  const int t = blockIdx.x;
-  if (blockIdx.y == 0) {
-    rope_rows<true, true, D, LAY>(a, t, 1, a.Hq, cs);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x < a.q_ctas) {
+    const int wpt = a.warps_per_token, tok = warp / wpt;
+    const int t = blockIdx.x * (kRopeWarps / wpt) + tok;
+    if (t < a.T)
+      rope_token<true, true, false, D, LAY, false>(a, t, threadIdx.x - tok * wpt * 32, wpt * 32, cs[warp]);
     return;
   }
-  const int64_t slot = a.slots[t];
+  const unsigned r = blockIdx.x - a.q_ctas;
+  const int t = r / a.parts, part = r % a.parts;
+  // lane i reads the slot of token t - 1 + i: the run's length is one ballot away
+  const long long ti = (long long)t - 1 + lane;
+  const int64_t sl = lane <= 16 && ti >= 0 && ti < a.T ? a.slots[ti] : -2;
+  const int64_t slot = __shfl_sync(0xffffffffu, sl, 1), prev = __shfl_sync(0xffffffffu, sl, 0);
   if (slot < 0) return;
   if (slot >= a.num_slots) {
-    if (threadIdx.x == 0 && blockIdx.y == 1) record_error(a.err, PA_ERR_BOUNDS);
+    if (threadIdx.x == 0 && part == 0) record_error(a.err, PA_ERR_BOUNDS);
     return;
   }
   const int off0 = (int)(slot & 15);
-  if (t > 0 && off0 != 0 && a.slots[t - 1] == slot - 1) return;  // not the first token of its run
-  int n = 1;
-  while (n < 16 - off0 && t + n < a.T && a.slots[t + n] == slot + n) ++n;
+  if (off0 != 0 && prev == slot - 1) return;  // not the first token of its run
+  const unsigned follows = __ballot_sync(0xffffffffu, sl == slot + lane - 1) >> 1;  // bit i: token t + i
+  const int n = min(16 - off0, __ffs(~follows) - 1);
+  const bool is_v = part & 1;
+  const int h = (part >> 1) * kRopeWarps + warp;
+  const bool live = h < a.Hkv;
   const int rot = a.rope.rot_dim;
-  for (int i = threadIdx.x; i < n * (rot >> 1); i += blockDim.x) {
-    const int tk = i / (rot >> 1), p = i - tk * (rot >> 1);
-    cs[tk][cs_index<D, LAY>(p)] = turn(a.rope, p, a.pos[t + tk]);
-  }
-  __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int unit_id = (blockIdx.y - 1) * 8 + warp;
-  if (unit_id >= 2 * a.Hkv) return;
-  const bool is_v = unit_id >= a.Hkv;
-  const int h = unit_id - (is_v ? a.Hkv : 0);
-  const uint16_t* src = (is_v ? a.v : a.k) + (long long)h * D;
+  const uint16_t* src = (is_v ? a.v : a.k) + (long long)(live ? h : 0) * D;
   const long long stride = is_v ? a.vs : a.ks;
-  const size_t sidx = (size_t)(slot >> 4) * a.Hkv + h;
+  const size_t sidx = (size_t)(slot >> 4) * a.Hkv + (live ? h : 0);
   float* scp = (is_v ? a.vsc : a.ksc) + sidx;
-  const float s_old = off0 > 0 ? *scp : 0.f;
   constexpr int UNITS = D / 16, ROWS = 32 / UNITS, ITERS = 16 / ROWS;
   const int u = lane % UNITS, r0 = lane / UNITS;
-  float y[ITERS][16];
-  uint32_t mb = 0;  // largest |y|: without the sign bit, magnitudes order like their bits (a NaN above all)
+  int v0, v1;
+  unit_vecs<LAY>(u, rot, v0, v1);
+  uint4 x[ITERS][2];
+  auto row_at = [&](int i) { return src + (t + i * ROWS + r0) * stride; };
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
-    const int r = i * ROWS + r0;
-    if (r < n) {
-      UnitIn<LAY> in;
-      load_unit<LAY>(src + (t + r) * stride, u, rot, !is_v, in);
-      turn_unit<true, D, LAY>(in, u, rot, !is_v, cs[r], y[i]);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) mb = max(mb, __float_as_uint(y[i][j]) & 0x7FFFFFFFu);
+    x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+    if (i * ROWS + r0 < n) {
+      x[i][0] = *reinterpret_cast<const uint4*>(row_at(i) + 8 * v0);
+      x[i][1] = *reinterpret_cast<const uint4*>(row_at(i) + 8 * v1);
     }
   }
+  const float s_old = off0 > 0 ? *scp : 0.f;
+  if (!is_v) {  // the run's tables, while the rows are in flight
+    for (int i = threadIdx.x; i < n * (rot >> 1); i += blockDim.x) {
+      const int tk = i / (rot >> 1), p = i - tk * (rot >> 1);
+      cs[tk][cs_index<D, LAY>(p)] = turn(a.rope, p, a.pos[t + tk]);
+    }
+    __syncthreads();
+  }
+  if (!live) return;
+  auto values = [&](int i, float (&y)[16]) {
+    UnitIn<LAY> in;
+    in.x0 = x[i][0];
+    in.x1 = x[i][1];
+    if (is_v) {
+      plain_unit<true, LAY>(in, y);
+    } else {
+      if constexpr (LAY == ROPE_HALF_ODD) load_unit<LAY, false>(row_at(i), u, rot, in);
+      turn_unit<true, D, LAY, false>(in, u, rot, cs[i * ROWS + r0], y);
+    }
+  };
+  uint32_t mb = 0;  // largest |y|: without the sign bit, magnitudes order like their bits (a NaN above all)
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+  for (int i = 0; i < ITERS; ++i)
+    if (i * ROWS + r0 < n) {
+      float y[16];
+      values(i, y);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) mb = max(mb, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+    }
+  mb = __reduce_max_sync(0xffffffffu, mb);
   const float s_run = __fdiv_rn(__uint_as_float(mb), 448.f);
   const bool grow = off0 == 0 || s_run > s_old;
   const float s = grow ? s_run : s_old;
@@ -343,16 +407,14 @@ __global__ void __launch_bounds__(256) rope_cache_block_kernel(const __grid_cons
     }
   }
 #pragma unroll
-  for (int i = 0; i < ITERS; ++i) {
-    const int r = i * ROWS + r0;
-    if (r < n) {
-      int v0, v1;
-      unit_vecs<LAY>(u, rot, v0, v1);
-      uint8_t* dst = tile + (size_t)(off0 + r) * D;
-      *reinterpret_cast<uint2*>(dst + 8 * v0) = codes8(y[i], s);
-      *reinterpret_cast<uint2*>(dst + 8 * v1) = codes8(y[i] + 8, s);
+  for (int i = 0; i < ITERS; ++i)
+    if (i * ROWS + r0 < n) {
+      float y[16];
+      values(i, y);
+      uint8_t* dst = tile + (size_t)(off0 + i * ROWS + r0) * D;
+      *reinterpret_cast<uint2*>(dst + 8 * v0) = codes8(y, s);
+      *reinterpret_cast<uint2*>(dst + 8 * v1) = codes8(y + 8, s);
     }
-  }
   if (lane == 0) *scp = s;
 }
 
@@ -360,20 +422,21 @@ __global__ void __launch_bounds__(256) rope_cache_block_kernel(const __grid_cons
 typedef void (*RopeKernel)(RopeArgs);
 
 template <bool BF, bool FP8, int D>
-RopeKernel pick_lay(int lay) {
-  return lay == ROPE_HALF    ? rope_cache_kernel<BF, FP8, D, ROPE_HALF>
-         : lay == ROPE_INTER ? rope_cache_kernel<BF, FP8, D, ROPE_INTER>
-                             : rope_cache_kernel<BF, FP8, D, ROPE_HALF_ODD>;
+RopeKernel pick_lay(int lay, bool full) {
+  if (lay == ROPE_HALF_ODD) return rope_cache_kernel<BF, FP8, D, ROPE_HALF_ODD, false>;
+  if (lay == ROPE_HALF)
+    return full ? rope_cache_kernel<BF, FP8, D, ROPE_HALF, true> : rope_cache_kernel<BF, FP8, D, ROPE_HALF, false>;
+  return full ? rope_cache_kernel<BF, FP8, D, ROPE_INTER, true> : rope_cache_kernel<BF, FP8, D, ROPE_INTER, false>;
 }
 
 template <int D>
-RopeKernel pick_kernel(int kv_dtype, int lay) {
+RopeKernel pick_kernel(int kv_dtype, int lay, bool full) {
   if (kv_dtype == PA_FP8_E4M3_BLOCK)
     return lay == ROPE_HALF    ? rope_cache_block_kernel<D, ROPE_HALF>
            : lay == ROPE_INTER ? rope_cache_block_kernel<D, ROPE_INTER>
                                : rope_cache_block_kernel<D, ROPE_HALF_ODD>;
-  if (kv_dtype == PA_FP8_E4M3) return pick_lay<true, true, D>(lay);
-  return kv_dtype == PA_BF16 ? pick_lay<true, false, D>(lay) : pick_lay<false, false, D>(lay);
+  if (kv_dtype == PA_FP8_E4M3) return pick_lay<true, true, D>(lay, full);
+  return kv_dtype == PA_BF16 ? pick_lay<true, false, D>(lay, full) : pick_lay<false, false, D>(lay, full);
 }
 
 int check_stride(const char* name, size_t stride, int heads, int head_dim) {
@@ -497,24 +560,16 @@ int pa_rope_and_cache(pa_pool* pool, int layer, const pa_rope* rope, const void*
   a.err = err;
   a.rope = *rope;
   const int lay = rope->layout == PA_ROPE_INTERLEAVED ? ROPE_INTER : rope->rot_dim % 16 == 0 ? ROPE_HALF : ROPE_HALF_ODD;
-  const RopeKernel kern = d.head_dim == 64 ? pick_kernel<64>(d.kv_dtype, lay) : pick_kernel<128>(d.kv_dtype, lay);
-  dim3 grid;
-  int threads = 256;
-  if (pool->block_scaled) {
-    const int tiles = (2 * d.n_kv_heads + 7) / 8;
-    if (tiles > 65534) return fail(PA_ERR_UNSUPPORTED, "too many kv heads for one call");
-    a.tokens_per_cta = 1;
-    grid = dim3(T, 1 + tiles);
-  } else {
-    // A CTA takes whole tokens, about 256 items at least; a token of more than
-    // 320 items is taken in even rounds.
-    const int items = (n_q_heads + 2 * d.n_kv_heads) * (d.head_dim / 16);
-    a.tokens_per_cta = items >= 256 ? 1 : std::min(kRopeMaxTokens, 256 / items);
-    const int all = items * a.tokens_per_cta, rounds = (all + 319) / 320;
-    threads = (all + rounds * 32 - 1) / (rounds * 32) * 32;
-    grid = dim3((T - 1) / a.tokens_per_cta + 1);
-  }
-  kern<<<grid, threads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  const bool full = rope->rot_dim == d.head_dim;
+  const RopeKernel kern =
+      d.head_dim == 64 ? pick_kernel<64>(d.kv_dtype, lay, full) : pick_kernel<128>(d.kv_dtype, lay, full);
+  a.warps_per_token = 1;
+  while (a.warps_per_token < kRopeWarps && (long long)T * a.warps_per_token < kRopeFewWarps) a.warps_per_token *= 2;
+  a.q_ctas = (unsigned)((T - 1) / (kRopeWarps / a.warps_per_token) + 1);
+  a.parts = 2u * (unsigned)((d.n_kv_heads + kRopeWarps - 1) / kRopeWarps);
+  const long long ctas = a.q_ctas + (pool->block_scaled ? (long long)T * a.parts : 0);
+  if (ctas > 0x7FFFFFFF) return fail(PA_ERR_UNSUPPORTED, "too many tokens and kv heads for one call");
+  kern<<<(unsigned)ctas, kRopeWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, "rope_and_cache launch: %s", cudaGetErrorString(e));
   return PA_OK;
