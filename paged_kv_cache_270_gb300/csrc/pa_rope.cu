@@ -45,7 +45,7 @@ struct RopeArgs {
   const int64_t* slots;
   int T, Hq, Hkv;
   int warps_per_token;     // 1, 2, 4 or 8
-  unsigned q_ctas, parts;  // block-scaled pools
+  unsigned parts;          // block-scaled pools
   long long num_slots;
   uint8_t* kpool;
   uint8_t* vpool;
@@ -299,10 +299,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_cache_kernel(const __
     rope_token<BF, FP8, true, D, LAY, FULL>(a, t, threadIdx.x - tok * wpt * 32, wpt * 32, cs[warp]);
 }
 
-// Block-scaled pools.  The first a.q_ctas CTAs turn queries as above.  Then come, for
-// each token, a.parts CTAs: K and V of eight heads each; those of a token that
-// starts a run (see reshape_block_scaled_kernel) take the run, a warp per (K or V, head)
-// tile.  A run's rows of one tile, at most 16 x D values, stay in the warp's
+// Block-scaled pools.  For each token come a.parts CTAs, K and V of eight heads
+// each; those of a token that starts a run (see reshape_block_scaled_kernel) take the run, a warp per (K or V, head)
+// tile, the others return at once.  The CTAs behind them turn queries as above: the
+// runs are the longer chains, so they start first.  A run's rows of one tile, at most 16 x D values, stay in the warp's
 // registers as they were loaded; they are turned twice, for the maximum and for
 // the encoding, which costs less than the registers of the fp32 values would
 // (four CTAs on an SM in the place of two).
@@ -311,14 +311,14 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_cache_block_kernel(co
   __shared__ __align__(16) float2 cs[16][D / 2];
   grid_dependents_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x < a.q_ctas) {
+  const unsigned r = blockIdx.x, kv_ctas = (unsigned)a.T * a.parts;
+  if (r >= kv_ctas) {
     const int wpt = a.warps_per_token, tok = warp / wpt;
-    const int t = blockIdx.x * (kRopeWarps / wpt) + tok;
+    const int t = (r - kv_ctas) * (kRopeWarps / wpt) + tok;
     if (t < a.T)
       rope_token<true, true, false, D, LAY, false>(a, t, threadIdx.x - tok * wpt * 32, wpt * 32, cs[warp]);
     return;
   }
-  const unsigned r = blockIdx.x - a.q_ctas;
   const int t = r / a.parts, part = r % a.parts;
   // lane i reads the slot of token t - 1 + i: the run's length is one ballot away
   const long long ti = (long long)t - 1 + lane;
@@ -565,9 +565,9 @@ int pa_rope_and_cache(pa_pool* pool, int layer, const pa_rope* rope, const void*
       d.head_dim == 64 ? pick_kernel<64>(d.kv_dtype, lay, full) : pick_kernel<128>(d.kv_dtype, lay, full);
   a.warps_per_token = 1;
   while (a.warps_per_token < kRopeWarps && (long long)T * a.warps_per_token < kRopeFewWarps) a.warps_per_token *= 2;
-  a.q_ctas = (unsigned)((T - 1) / (kRopeWarps / a.warps_per_token) + 1);
+  const unsigned q_ctas = (unsigned)((T - 1) / (kRopeWarps / a.warps_per_token) + 1);
   a.parts = 2u * (unsigned)((d.n_kv_heads + kRopeWarps - 1) / kRopeWarps);
-  const long long ctas = a.q_ctas + (pool->block_scaled ? (long long)T * a.parts : 0);
+  const long long ctas = q_ctas + (pool->block_scaled ? (long long)T * a.parts : 0);
   if (ctas > 0x7FFFFFFF) return fail(PA_ERR_UNSUPPORTED, "too many tokens and kv heads for one call");
   kern<<<(unsigned)ctas, kRopeWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
   const cudaError_t e = cudaGetLastError();
