@@ -28,12 +28,19 @@ constexpr unsigned kAll = 0xffffffffu;
 // distributed shared memory.  Counts are integers, so the result depends on no
 // order of execution.
 //
-// What bounds it is the instructions per key and the latency of the passes,
-// not the 4 bytes per key.  The first digit holds the sign, the exponent and two
-// bits of mantissa: wide enough that few keys share its bin with the k-th
-// one, so the later passes only compare and skip.
+// What bounds it is instructions per key and the latency of the passes, not the
+// 4 bytes per key.  So keys go four at a time; the first digit holds the sign,
+// the exponent and two bits of mantissa, wide enough that few keys share its bin
+// with the k-th one; every key of the share has a value (the tokens that stay
+// anyway above all others, places behind the context below all), so no pass
+// tests where a key lies; and the bin search reads 64 sums of 32 bins from each
+// CTA, then 32 bins.
 constexpr int kSelBins = 2048;
 constexpr int kSelMaxKeys = 49152;  // keys a CTA keeps (192 KiB); longer shares are read again in each pass
+constexpr uint32_t kKeyNone = 0u;            // behind the context
+constexpr uint32_t kKeyNaN = 1u;             // below every number
+constexpr uint32_t kKeyZero = 0x80000000u;
+constexpr uint32_t kKeyStays = 0xFFFFFFFFu;  // first and last tokens
 
 struct SelectArgs {
   const float* w;
@@ -43,30 +50,16 @@ struct SelectArgs {
   int budget, sinks, recent;
   int32_t* keep;
   int32_t* kept;
-  int max_keys;  // keys of the CTA's dynamic shared memory, a multiple of 32
+  int max_keys;  // keys of the CTA's dynamic shared memory, a multiple of 128
+  int vec;       // rows are 16-byte aligned
   unsigned int* err;
 };
 
-// Larger floats have larger keys; -0 counts as 0, NaN comes below every number.
+// Larger floats have larger keys; -0 counts as 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
-  if (x != x) return 0u;
   const uint32_t b = __float_as_uint(x + 0.f);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-
-// Adds each lane's digit (those with `in`) to the histogram.  Totals crowd
-// (all the tokens that nothing attends to share one bin), and a shared-memory
-// atomic serialises on equal addresses: the lanes that agree with the first one
-// are counted by a ballot, the rest add one by one.
-__device__ __forceinline__ void hist_add(uint32_t* hist, uint32_t digit, bool in) {
-  const unsigned all = __ballot_sync(kAll, in);
-  if (!all) return;
-  const int lead = __ffs(all) - 1;
-  const uint32_t d = __shfl_sync(kAll, digit, lead);
-  const unsigned same = __ballot_sync(kAll, in && digit == d);
-  const int lane = threadIdx.x & 31;
-  if (lane == lead) atomicAdd(&hist[d], (uint32_t)__popc(same));
-  else if (in && digit != d) atomicAdd(&hist[digit], 1u);
+  const uint32_t k = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  return x == x ? k : kKeyNaN;
 }
 
 template <int C>
@@ -75,17 +68,34 @@ __device__ __forceinline__ void row_sync() {
   else cg::this_cluster().sync();
 }
 
-// C CTAs of NT threads per row.  Single CTAs take 256 threads: with short rows
-// the passes' latency counts, and six CTAs on an SM hide it better than three.
+// p in CTA r of the row's cluster.
+template <int C, typename T>
+__device__ __forceinline__ const T* of_rank(T* p, int r) {
+  if constexpr (C == 1) return p;
+  else return cg::this_cluster().map_shared_rank(p, r);
+}
+
+// Inclusive sum over the lanes from the highest down.
+__device__ __forceinline__ uint32_t scan_down(uint32_t x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t y = __shfl_down_sync(kAll, x, off);
+    if (lane + off < 32) x += y;
+  }
+  return x;
+}
+
+// C CTAs of NT threads per row.
 template <int C, int NT>
 __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 2) select_kernel(const SelectArgs a) {
-  constexpr int kSelThreads = NT, kSelWarps = NT / 32, BPT = kSelBins / NT;  // BPT: bins per thread
+  constexpr int NW = NT / 32;
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ __align__(16) uint32_t hist[2][kSelBins];
-  __shared__ uint32_t s_scan[kSelWarps];
+  __shared__ __align__(16) uint32_t sums[2][64];  // of 32 bins each
   __shared__ uint32_t s_digit, s_rem;
-  __shared__ uint2 s_warp[kSelWarps];
-  __shared__ uint2 s_cta;  // (above, equal) of this CTA's share
+  __shared__ uint2 s_warp[NW];
+  __shared__ uint2 s_cta, s_before;  // (above, equal): of this CTA's share, of the shares before it
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / C, rank = blockIdx.x % C;
   const int seq = row / a.H;
@@ -98,192 +108,221 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 2) select_kernel(const Sel
   int32_t* keep = a.keep + (long long)row * a.budget;
   if (tid == 0 && rank == 0 && row == seq * a.H) a.kept[seq] = min(n, a.budget);
   if (n <= a.budget) {  // everything stays (the same for all CTAs of the row)
-    for (int i = rank * kSelThreads + tid; i < a.budget; i += C * kSelThreads) keep[i] = i < n ? i : -1;
+    for (int i = rank * NT + tid; i < a.budget; i += C * NT) keep[i] = i < n ? i : -1;
     return;
   }
-  for (int i = rank * kSelThreads + tid; i < a.sinks + a.recent; i += C * kSelThreads)
-    keep[i < a.sinks ? i : a.budget - a.recent + (i - a.sinks)] = i < a.sinks ? i : n - a.recent + (i - a.sinks);
-  const int k = a.budget - a.sinks - a.recent;
-  if (k == 0) return;
 
-  // this CTA's share of the m tokens between the first and the last ones
-  const int m = n - a.sinks - a.recent;
-  const int chunk = ((m + C - 1) / C + 31) / 32 * 32;
-  const int begin = (int)min((long long)m, (long long)rank * chunk), cnt = min(chunk, m - begin);
-  const float* src = a.w + (long long)row * a.stride + a.sinks + begin;
-  // keys i .. i + 3 of the share (i a multiple of 4); those from cnt on are anything
-  auto keys4 = [&](int i) {
-    if (i < a.max_keys) return *reinterpret_cast<const uint4*>(keys + i);
-    uint4 v;
-    v.x = i < cnt ? order_key(src[i]) : 0u;
-    v.y = i + 1 < cnt ? order_key(src[i + 1]) : 0u;
-    v.z = i + 2 < cnt ? order_key(src[i + 2]) : 0u;
-    v.w = i + 3 < cnt ? order_key(src[i + 3]) : 0u;
-    return v;
+  // this CTA's share of the row: tokens [begin, begin + cnt), in groups of four
+  const int chunk = ((n + C - 1) / C + 127) / 128 * 128;
+  const int begin = (int)min((long long)n, (long long)rank * chunk), cnt = min(chunk, n - begin);
+  const int groups = (cnt + 3) / 4;
+  const int tail = n - a.recent - begin, head = a.sinks - begin;  // in the share: i < head or i >= tail stays
+  const float* src = a.w + (long long)row * a.stride + begin;
+  auto load_keys = [&](int i) {  // keys of tokens i .. i + 3 of the share
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.vec) {
+      x = *reinterpret_cast<const float4*>(src + i);  // (the row's stride reaches past its last group)
+    } else {
+      x.x = src[i];
+      if (i + 1 < cnt) x.y = src[i + 1];
+      if (i + 2 < cnt) x.z = src[i + 2];
+      if (i + 3 < cnt) x.w = src[i + 3];
+    }
+    uint4 k = make_uint4(order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w));
+    if (i < head || i + 3 >= tail) {  // (tail <= cnt - recent: the share's end is behind it)
+      uint32_t* e[4] = {&k.x, &k.y, &k.z, &k.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (i + j < head || i + j >= tail) *e[j] = kKeyStays;
+        if (i + j >= cnt) *e[j] = kKeyNone;
+      }
+    }
+    return k;
   };
+  auto keys4 = [&](int i) { return i < a.max_keys ? *reinterpret_cast<const uint4*>(keys + i) : load_keys(i); };
 
-  for (int i = tid; i < 2 * kSelBins / 4; i += kSelThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < 2 * kSelBins / 4; i += NT) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   uint32_t prefix = 0;
-  uint32_t rem = k;  // still to be taken among the keys that start with the prefix
+  uint32_t rem = a.budget - a.sinks - a.recent;  // still to be taken among the keys that start with the prefix
+  const bool search = rem > 0;                   // (else what stays anyway fills the budget)
 #pragma unroll
   for (int p = 0; p < 3; ++p) {
     uint32_t* h = hist[p & 1];
     constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
+    // Shared-memory atomics serialise on equal addresses, and one value is met by the
+    // thousand: the zero of tokens that nothing attended to.  Each thread counts its
+    // own; the rest spread over the bins.
+    uint32_t zeros = 0;
+    auto add = [&](uint32_t key) {
+      const bool in = p == 0 ? key - 1u < kKeyStays - 1u : (key >> (kShift[p] + kBits[p])) == prefix;
+      if (in && key != kKeyZero) atomicAdd(&h[(key >> kShift[p]) & ((1u << kBits[p]) - 1u)], 1u);
+      zeros += key == kKeyZero;
+    };
     if (p == 0) {
-      // eight loads in flight per thread
-      for (int i0 = 0; i0 < cnt; i0 += 8 * kSelThreads) {
-        float x[8];
+      constexpr int LD = NT == 256 ? 2 : 4;  // loads in flight per thread
+      for (int g0 = tid; g0 < groups; g0 += LD * NT) {
+        uint4 v[LD];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int i = i0 + j * kSelThreads + tid;
-          x[j] = i < cnt ? src[i] : 0.f;
-        }
+        for (int j = 0; j < LD; ++j)
+          if (g0 + j * NT < groups) v[j] = load_keys(4 * (g0 + j * NT));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int i = i0 + j * kSelThreads + tid;
-          const uint32_t key = order_key(x[j]);
-          if (i < cnt && i < a.max_keys) keys[i] = key;
-          if (i0 + j * kSelThreads < cnt) hist_add(h, key >> 21, i < cnt);  // (uniform per CTA)
-        }
+        for (int j = 0; j < LD; ++j)
+          if (g0 + j * NT < groups) {
+            const int i = 4 * (g0 + j * NT);
+            if (i < a.max_keys) *reinterpret_cast<uint4*>(keys + i) = v[j];
+            add(v[j].x);
+            add(v[j].y);
+            add(v[j].z);
+            add(v[j].w);
+          }
       }
-    } else {
-      for (int i0 = 0; i0 < cnt; i0 += 4 * kSelThreads) {
-        const int i = i0 + 4 * tid;
-        const uint4 v = i < cnt ? keys4(i) : make_uint4(0, 0, 0, 0);
-        const uint32_t key[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          hist_add(h, (key[j] >> kShift[p]) & ((1u << kBits[p]) - 1u),
-                   i + j < cnt && (key[j] >> (kShift[p] + kBits[p])) == prefix);
+    } else if (search) {
+      for (int g = tid; g < groups; g += NT) {
+        const uint4 v = keys4(4 * g);
+        add(v.x);
+        add(v.y);
+        add(v.z);
+        add(v.w);
       }
+    }
+    if (!search) continue;
+    if (p == 0 || (kKeyZero >> (kShift[p] + kBits[p])) == prefix) {
+      zeros = __reduce_add_sync(kAll, zeros);
+      if (lane == 0 && zeros) atomicAdd(&h[(kKeyZero >> kShift[p]) & ((1u << kBits[p]) - 1u)], zeros);
+    }
+    __syncthreads();
+    for (int b = 4 * tid; b < kSelBins; b += 4 * NT) {
+      const uint4 v = *reinterpret_cast<const uint4*>(h + b);
+      uint32_t x = v.x + v.y + v.z + v.w;
+#pragma unroll
+      for (int off = 1; off < 8; off <<= 1) x += __shfl_xor_sync(kAll, x, off);
+      if ((lane & 7) == 0) sums[p & 1][b / 32] = x;
     }
     row_sync<C>();  // every CTA's histogram is complete
-    // the bins of the whole row from the top down, BPT per thread, and the one
-    // that holds the rem-th key
-    uint32_t c[BPT];
+    if (warp == 0) {
+      uint2 c = make_uint2(0, 0);  // sums 2 lane, 2 lane + 1 of the whole row
 #pragma unroll
-    for (int j = 0; j < BPT; ++j) c[j] = 0;
-    const int b0 = kSelBins - BPT - BPT * tid;  // bins b0 + BPT - 1 down to b0
-#pragma unroll
-    for (int r = 0; r < C; ++r) {
-      const uint32_t* hr = h;
-      if constexpr (C > 1) hr = cg::this_cluster().map_shared_rank(h, r);
-#pragma unroll
-      for (int j = 0; j < BPT; j += 4) {
-        const uint4 v = *reinterpret_cast<const uint4*>(hr + b0 + BPT - 4 - j);
-        c[j] += v.w;
-        c[j + 1] += v.z;
-        c[j + 2] += v.y;
-        c[j + 3] += v.x;
+      for (int r = 0; r < C; ++r) {
+        const uint2 v = *reinterpret_cast<const uint2*>(of_rank<C>(sums[p & 1], r) + 2 * lane);
+        c.x += v.x;
+        c.y += v.y;
       }
-    }
-    uint32_t mine = 0;
+      uint32_t upto = scan_down(c.x + c.y), above = upto - c.x - c.y;
+      // the sum that holds the rem-th key from above, and what lies above it
+      const bool hi = above < rem && rem <= above + c.y, lo = above + c.y < rem && rem <= upto;
+      const unsigned who = __ballot_sync(kAll, hi || lo);
+      const int from = __ffs(who) - 1;
+      const int bin32 = __shfl_sync(kAll, 2 * lane + (hi ? 1 : 0), from);
+      const uint32_t left = rem - __shfl_sync(kAll, above + (hi ? 0 : c.y), from);
+      uint32_t f = 0;
 #pragma unroll
-    for (int j = 0; j < BPT; ++j) mine += c[j];
-    uint32_t x = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t y = __shfl_up_sync(kAll, x, off);
-      if (lane >= off) x += y;
-    }
-    if (lane == 31) s_scan[warp] = x;
-    // the other buffer's readers passed the barrier above: clear it for the next digit
-    if (p == 1)
-      for (int i = tid; i < kSelBins / 4; i += NT) reinterpret_cast<uint4*>(hist[0])[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    uint32_t before = x - mine;
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) before += w < warp ? s_scan[w] : 0u;
-    if (before < rem && rem <= before + mine) {
-      uint32_t at = before;
-#pragma unroll
-      for (int j = 0; j < BPT; ++j) {
-        if (at < rem && rem <= at + c[j]) {
-          s_digit = b0 + BPT - 1 - j;
-          s_rem = rem - at;
-        }
-        at += c[j];
+      for (int r = 0; r < C; ++r) f += of_rank<C>(h, r)[32 * bin32 + lane];
+      upto = scan_down(f);
+      above = upto - f;
+      if (above < left && left <= upto) {
+        s_digit = 32 * bin32 + lane;
+        s_rem = left - above;
       }
+    } else if (p == 1) {
+      // the first buffer's readers passed the barrier above: clear it for the last digit
+      for (int i = tid - 32; i < kSelBins / 4; i += NT - 32) reinterpret_cast<uint4*>(hist[0])[i] = make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
     prefix = (prefix << kBits[p]) | s_digit;
     rem = s_rem;
   }
+  if (!search) {  // nothing but what stays anyway
+    prefix = kKeyStays;
+    rem = 1u << 31;
+    __syncthreads();  // (the keys)
+  }
 
-  // ---- above the threshold key, and equal to it: counts per warp, each warp
-  // one stretch of the share
-  const int seg = ((cnt + kSelWarps - 1) / kSelWarps + 127) / 128 * 128;
-  const int w0 = min(cnt, warp * seg), w1 = min(cnt, w0 + seg);
+  // ---- above the threshold key, and equal to it: counts per warp, each warp one
+  // stretch of the share
+  const int seg = ((groups + NW - 1) / NW + 31) / 32 * 32;
+  const int w0 = min(groups, warp * seg), w1 = min(groups, w0 + seg);
   uint32_t above = 0, equal = 0;
-  for (int i = w0 + 4 * lane; i < w1; i += 128) {
-    const uint4 v = keys4(i);
-    const uint32_t key[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      above += i + j < w1 && key[j] > prefix;
-      equal += i + j < w1 && key[j] == prefix;
-    }
+  for (int g = w0 + lane; g < w1; g += 32) {
+    const uint4 v = keys4(4 * g);
+    above += (v.x > prefix) + (v.y > prefix) + (v.z > prefix) + (v.w > prefix);
+    equal += (v.x == prefix) + (v.y == prefix) + (v.z == prefix) + (v.w == prefix);
   }
   above = __reduce_add_sync(kAll, above);
   equal = __reduce_add_sync(kAll, equal);
   if (lane == 0) s_warp[warp] = make_uint2(above, equal);
   __syncthreads();
-  uint32_t ga = 0, ge = 0, ta = 0, te = 0;  // before this warp in the CTA; of the CTA
+  uint32_t ga = 0, ge = 0;  // before this warp's stretch
+  {
+    uint32_t ta = 0, te = 0;
 #pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) {
-    const uint2 v = s_warp[w];
-    ga += w < warp ? v.x : 0;
-    ge += w < warp ? v.y : 0;
-    ta += v.x;
-    te += v.y;
-  }
-  if constexpr (C > 1) {
-    if (tid == 0) s_cta = make_uint2(ta, te);
-    cg::this_cluster().sync();
-#pragma unroll
-    for (int r = 0; r < C; ++r) {
-      const uint2 v = *cg::this_cluster().map_shared_rank(&s_cta, r);
-      ga += r < rank ? v.x : 0;
-      ge += r < rank ? v.y : 0;
+    for (int w = 0; w < NW; ++w) {
+      const uint2 v = s_warp[w];
+      ga += w < warp ? v.x : 0;
+      ge += w < warp ? v.y : 0;
+      ta += v.x;
+      te += v.y;
+    }
+    if constexpr (C > 1) {
+      if (tid == 0) s_cta = make_uint2(ta, te);
+      cg::this_cluster().sync();
+      if (warp == 0) {
+        uint2 v = make_uint2(0, 0);
+        if (lane < rank) v = *of_rank<C>(&s_cta, lane);
+        v.x = __reduce_add_sync(kAll, v.x);
+        v.y = __reduce_add_sync(kAll, v.y);
+        if (lane == 0) s_before = v;
+      }
+      __syncthreads();
+      ga += s_before.x;
+      ge += s_before.y;
+      cg::this_cluster().barrier_arrive();  // this CTA reads no other's memory any more
     }
   }
   // ---- the taken tokens in order: all above, and the first rem of the equal ones.
-  // A lane holds four neighbours; (above, equal) counts are scanned over the
-  // warp in one word, at most 128 each.
-  for (int i0 = w0; i0 < w1; i0 += 128) {
-    const int i = i0 + 4 * lane;
-    const uint4 v = i < w1 ? keys4(i) : make_uint4(0, 0, 0, 0);
-    const uint32_t key[4] = {v.x, v.y, v.z, v.w};
-    uint32_t f[4], own = 0;
+  // A warp whose equal keys are all taken, or none, compares once per key.
+  const bool mixed = ge < rem && ge + equal > rem;
+  const uint32_t least = ge < rem ? prefix : prefix + 1u;  // (prefix + 1: only where some key lies above)
+  const bool none = ge >= rem && prefix == kKeyStays;
+  uint32_t at = ga + min(ge, rem);
+  for (int g0 = w0; g0 < w1 && !none; g0 += 32) {
+    const int g = g0 + lane;
+    const uint4 v = g < w1 ? keys4(4 * g) : make_uint4(0, 0, 0, 0);
+    uint32_t t[4];
+    t[0] = v.x >= least;
+    t[1] = v.y >= least;
+    t[2] = v.z >= least;
+    t[3] = v.w >= least;
+    if (mixed) {  // (few warps: the one where the equal ones run out)
+      const uint32_t e = (v.x == prefix) + (v.y == prefix) + (v.z == prefix) + (v.w == prefix);
+      const uint32_t up = e + (scan_down(e) - e);  // this lane and those behind it
+      uint32_t rank_e = ge + __shfl_sync(kAll, up, 0) - up;  // equal ones before this lane
+      ge += __shfl_sync(kAll, up, 0);
+      const uint32_t key[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[j] = i + j < w1 ? (key[j] > prefix ? 1u : key[j] == prefix ? 0x10000u : 0u) : 0u;
-      own += f[j];
+      for (int j = 0; j < 4; ++j)
+        if (key[j] == prefix) t[j] = rank_e++ < rem;
     }
+    const uint32_t own = t[0] + t[1] + t[2] + t[3];
     uint32_t x = own;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const uint32_t y = __shfl_up_sync(kAll, x, off);
       if (lane >= off) x += y;
     }
-    const uint32_t sum = __shfl_sync(kAll, x, 31);
-    x -= own;
-    uint32_t ea = ga + (x & 0xFFFFu), ee = ge + (x >> 16);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (f[j] == 1u || (f[j] != 0u && ee < rem)) keep[a.sinks + ea + min(ee, rem)] = a.sinks + begin + i + j;
-      ea += f[j] & 1u;
-      ee += f[j] >> 16;
-    }
-    ga += sum & 0xFFFFu;
-    ge += sum >> 16;
+    int32_t* out = keep + at + (x - own);
+    at += __shfl_sync(kAll, x, 31);
+    const int tok = begin + 4 * g;
+    if (t[0]) *out++ = tok;
+    if (t[1]) *out++ = tok + 1;
+    if (t[2]) *out++ = tok + 2;
+    if (t[3]) *out = tok + 3;
   }
-  if constexpr (C > 1) cg::this_cluster().sync();  // no CTA leaves while another may read its memory
+  if constexpr (C > 1) cg::this_cluster().barrier_wait();  // no CTA leaves while another may read its memory
 }
 
 // ---------------------------------------------------------------- compaction
-// One warp per destination tile (sequence, kv head, page): 16 rows, gathered
+// One warp per destination page of a (sequence, kv head): 16 rows, gathered
 // from wherever they lie.  Lanes 0-15 resolve the rows' addresses; the rows
 // then move as 16-byte vectors, all loads of a batch in flight before the
 // first store.
@@ -304,7 +343,8 @@ struct CompactArgs {
   long long w_in_stride;
   float* w_out;
   long long w_out_stride;
-  int warps_per_row;  // >= the destination pages of a row
+  unsigned ctas_per_row;
+  int pages_per_row;  // >= the destination pages of a row
   unsigned int* err;
 };
 
@@ -317,12 +357,11 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactA
   constexpr int PER = 16 * VPR / 32;  // vectors of a tile per lane
   grid_dependents_launch();
   const int lane = threadIdx.x & 31;
-  const long long unit = (long long)blockIdx.x * (kCompactThreads / 32) + (threadIdx.x >> 5);
-  const int page = (int)(unit % a.warps_per_row);
-  const long long row = unit / a.warps_per_row;
-  const int h = (int)(row % a.Hkv);
-  if (row / a.Hkv >= a.S) return;
-  const int seq = (int)(row / a.Hkv);
+  const unsigned row = blockIdx.x / a.ctas_per_row;
+  const int unit = (int)(blockIdx.x - row * a.ctas_per_row) * (kCompactThreads / 32) + (int)(threadIdx.x >> 5);
+  const int page = BLK ? unit >> 1 : unit, which_blk = BLK ? unit & 1 : 0;
+  if (page >= a.pages_per_row) return;
+  const int seq = (int)(row / (unsigned)a.Hkv), h = (int)(row - (unsigned)seq * a.Hkv);
   int kept = a.kept[seq];
   if (kept < 0 || kept > a.budget || kept > 16ll * a.dst_blocks) {
     if (lane == 0 && page == 0) record_error(a.err, PA_ERR_BOUNDS);
@@ -369,73 +408,64 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactA
         }
       }
     } else {
-      // Lane r holds row r's K and V tile scales.  A tile's largest |value| is the
-      // largest of its rows' largest codes under their scales (codes order like
-      // their values), so it takes no conversion to fp32 per code; the new code
-      // is the old one's value times the row's ratio of scales.
-      float s_src[2] = {0.f, 0.f};
-      if (src >= 0) {
-        s_src[0] = a.ksc[src >> 4];
-        s_src[1] = a.vsc[src >> 4];
-      }
-      uint4 x[2][PER];
+      // A warp for the K tile, one for the V tile.  Lane r holds row r's tile scale.
+      // The new tile's largest |value| is the largest of its rows' largest codes under
+      // their scales (codes order like their values), so it takes no conversion
+      // to fp32 per code; the new code is the old one's value times the row's
+      // ratio of scales.
+      uint8_t* pool = which_blk ? a.v : a.k;
+      float* scales = which_blk ? a.vsc : a.ksc;
+      const float s_src = src >= 0 ? scales[src >> 4] : 0.f;
+      uint4 x[PER];
       bool have[PER];
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         const int vec = j * 32 + lane;
         const long long from = __shfl_sync(kAll, src, vec / VPR);
         have[j] = from >= 0;
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-          x[which][j] = make_uint4(0, 0, 0, 0);
-          if (have[j])
-            x[which][j] = *reinterpret_cast<const uint4*>((which ? a.v : a.k) + from * ROW + (vec % VPR) * 16);
-        }
+        x[j] = make_uint4(0, 0, 0, 0);
+        if (have[j]) x[j] = *reinterpret_cast<const uint4*>(pool + from * ROW + (vec % VPR) * 16);
       }
+      uint32_t c[PER][8];  // the codes as binary16 pairs
+      uint32_t mb = 0;     // bits of the largest |value|
 #pragma unroll
-      for (int which = 0; which < 2; ++which) {
-        uint32_t c[PER][8];  // the codes as binary16 pairs
-        uint32_t mb = 0;     // bits of the largest |value|
+      for (int j = 0; j < PER; ++j) {
+        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+        __half2 top = __float2half2_rn(0.f);
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          const uint32_t w[4] = {x[which][j].x, x[which][j].y, x[which][j].z, x[which][j].w};
-          __half2 top = __float2half2_rn(0.f);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            e4m3x4_to_f16x2x2(w[q], c[j][2 * q], c[j][2 * q + 1]);
-            top = __hmax2_nan(top, __habs2(*reinterpret_cast<__half2*>(&c[j][2 * q])));
-            top = __hmax2_nan(top, __habs2(*reinterpret_cast<__half2*>(&c[j][2 * q + 1])));
-          }
-          const float2 t = __half22float2(top);
-          const float s = __shfl_sync(kAll, s_src[which], (j * 32 + lane) / VPR);
-          mb = max(mb, max(__float_as_uint(__fmul_rn(t.x, s)) & 0x7FFFFFFFu,
-                           __float_as_uint(__fmul_rn(t.y, s)) & 0x7FFFFFFFu));
+        for (int q = 0; q < 4; ++q) {
+          e4m3x4_to_f16x2x2(w[q], c[j][2 * q], c[j][2 * q + 1]);
+          top = __hmax2_nan(top, __habs2(*reinterpret_cast<__half2*>(&c[j][2 * q])));
+          top = __hmax2_nan(top, __habs2(*reinterpret_cast<__half2*>(&c[j][2 * q + 1])));
         }
-        mb = __reduce_max_sync(kAll, mb);
-        const float s = __fdiv_rn(__uint_as_float(mb), 448.f);
-        // (a row of zeros may have any scale: its ratio is kept finite)
-        const float ratio = s > 0.f ? fminf(__fdiv_rn(s_src[which], s), 0x1p100f) : 0.f;
-        uint8_t* pool = which ? a.v : a.k;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          const int vec = j * 32 + lane;
-          const float r = __shfl_sync(kAll, ratio, vec / VPR);
-          uint32_t w[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float2 u = unpack2<false>(c[j][q]);
-            w[q] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(u.x, r), __fmul_rn(u.y, r)), __NV_SATFINITE, __NV_E4M3);
-          }
-          if (have[j])
-            *reinterpret_cast<uint4*>(pool + (dtile + vec / VPR) * ROW + (vec % VPR) * 16) =
-                make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
-        }
-        if (lane == 0 && dst >= 0 && dst < a.num_blocks) (which ? a.vsc : a.ksc)[dtile >> 4] = s;
+        const float2 t = __half22float2(top);
+        const float s = __shfl_sync(kAll, s_src, (j * 32 + lane) / VPR);
+        mb = max(mb, max(__float_as_uint(__fmul_rn(t.x, s)) & 0x7FFFFFFFu,
+                         __float_as_uint(__fmul_rn(t.y, s)) & 0x7FFFFFFFu));
       }
+      mb = __reduce_max_sync(kAll, mb);
+      const float s = __fdiv_rn(__uint_as_float(mb), 448.f);
+      // (a row of zeros may have any scale: its ratio is kept finite)
+      const float ratio = s > 0.f ? fminf(__fdiv_rn(s_src, s), 0x1p100f) : 0.f;
+      uint8_t* out = pool + dtile * ROW + lane * 16;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const float r = __shfl_sync(kAll, ratio, (j * 32 + lane) / VPR);
+        uint32_t w[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float2 u = unpack2<false>(c[j][q]);
+          w[q] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(u.x, r), __fmul_rn(u.y, r)), __NV_SATFINITE, __NV_E4M3);
+        }
+        if (have[j])
+          *reinterpret_cast<uint4*>(out + j * 512) =
+              make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
+      }
+      if (lane == 0 && dst >= 0 && dst < a.num_blocks) scales[dtile >> 4] = s;
     }
   }
   // ---- totals: of the page's tokens, and this warp's part of the zeros behind them
-  if (a.w_in && kh == h) {
+  if (a.w_in && kh == h && which_blk == 0) {
     const long long wrow = (long long)seq * a.keep_heads + kh;
     float* wo = a.w_out + wrow * a.w_out_stride;
     if (live && i < a.w_out_stride) {
@@ -448,7 +478,7 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactA
     }
     const long long zeros = a.w_out_stride - kept;
     if (zeros > 0) {
-      const long long each = (zeros + a.warps_per_row - 1) / a.warps_per_row;
+      const long long each = (zeros + a.pages_per_row - 1) / a.pages_per_row;
       const long long z0 = kept + each * page, z1 = min(a.w_out_stride, z0 + each);
       for (long long z = z0 + lane; z < z1; z += 32) wo[z] = 0.f;
     }
@@ -524,7 +554,8 @@ int pa_evict_select(pa_pool* pool, const float* weights, size_t weights_stride, 
   // 16384 keys (64 KiB, three CTAs per SM), up to the portable cluster of eight.
   const long long tokens = a.stride;
   const int C = tokens <= 8192 ? 1 : tokens <= 32768 ? 2 : tokens <= 65536 ? 4 : 8;
-  a.max_keys = (int)std::min<long long>(((tokens + C - 1) / C + 31) / 32 * 32, kSelMaxKeys);
+  a.max_keys = (int)std::min<long long>(((tokens + C - 1) / C + 127) / 128 * 128, kSelMaxKeys);
+  a.vec = weights_stride % 4 == 0;
   const int smem = a.max_keys * 4;  // keys, besides the histograms' 16 KiB
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = C == 1   ? launch_select<1>(a, smem, st)
@@ -558,11 +589,11 @@ int pa_evict_compact(pa_pool* pool, int layer, const int32_t* keep_dev, int keep
     return fail(PA_ERR_INVALID, "the destination table must name other blocks than the source table");
   if (((uintptr_t)weights_in | (uintptr_t)weights_out) & 15u)
     return fail(PA_ERR_INVALID, "the weights must be 16-byte aligned");
-  // a row's warps: one per destination page, and enough that none zeroes more than 1024 totals
+  // a row's pages: the destination's, and enough that no warp zeroes more than 1024 totals
   long long per_row = (std::min<long long>(budget, 16ll * dst_max_blocks) + 15) / 16;
   if (weights_in) per_row = std::max<long long>(per_row, ((long long)weights_out_stride + 1023) / 1024);
-  const long long warps = (long long)S * d.n_kv_heads * per_row;
-  const long long ctas = (warps + kCompactThreads / 32 - 1) / (kCompactThreads / 32);
+  const long long ctas_per_row = (per_row * (pool->block_scaled ? 2 : 1) + kCompactThreads / 32 - 1) / (kCompactThreads / 32);
+  const long long ctas = (long long)S * d.n_kv_heads * ctas_per_row;
   if (per_row > 0x7FFFFFFF || ctas > 0x7FFFFFFF) return fail(PA_ERR_UNSUPPORTED, "too many pages for one call");
   unsigned int* err = device_error_word();
   if (!err) return PA_ERR_CUDA;
@@ -586,7 +617,8 @@ int pa_evict_compact(pa_pool* pool, int layer, const int32_t* keep_dev, int keep
   a.w_in_stride = (long long)weights_in_stride;
   a.w_out = weights_out;
   a.w_out_stride = (long long)weights_out_stride;
-  a.warps_per_row = (int)per_row;
+  a.ctas_per_row = (unsigned)ctas_per_row;
+  a.pages_per_row = (int)per_row;
   a.err = err;
   pick_compact(pool)<<<(unsigned)ctas, kCompactThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
   const cudaError_t e = cudaGetLastError();
