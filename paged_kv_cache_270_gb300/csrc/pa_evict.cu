@@ -352,7 +352,7 @@ constexpr int kCompactThreads = 256;
 
 // ROW: bytes of one token row of a tile (64, 128 or 256).
 template <int ROW, bool BLK>
-__global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactArgs a) {
+__global__ void __launch_bounds__(kCompactThreads, BLK ? 4 : 5) compact_kernel(const CompactArgs a) {
   constexpr int VPR = ROW / 16;       // vectors per row
   constexpr int PER = 16 * VPR / 32;  // vectors of a tile per lane
   grid_dependents_launch();
@@ -387,24 +387,48 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactA
       }
     }
     if (bad) record_error(a.err, PA_ERR_BOUNDS);
+  }
+  // Totals of the page's tokens (loaded here, stored at the end) and this warp's part
+  // of the zeros behind them.
+  const bool totals = a.w_in && kh == h && which_blk == 0;
+  float* wo = nullptr;
+  float w = 0.f;
+  if (totals) {
+    const long long wrow = (long long)seq * a.keep_heads + kh;
+    wo = a.w_out + wrow * a.w_out_stride;
+    if (live) {
+      if (tok >= 0 && tok < a.w_in_stride) w = a.w_in[wrow * a.w_in_stride + tok];
+      if (tok < 0 || tok >= a.w_in_stride || i >= a.w_out_stride) record_error(a.err, PA_ERR_BOUNDS);
+    }
+    const long long zeros = a.w_out_stride - kept;
+    if (zeros > 0) {
+      const long long each = (zeros + a.pages_per_row - 1) / a.pages_per_row;
+      const long long z0 = kept + each * page, z1 = min(a.w_out_stride, z0 + each);
+      for (long long z = z0 + lane; z < z1; z += 32) wo[z] = 0.f;
+    }
+  }
+  if (16 * page < kept) {
     const long long dtile = ((long long)dst * a.Hkv + h) * 16;
     if constexpr (!BLK) {
+      // The 2 PER vectors of a lane, K's then V's, in batches of at most eight (128 bytes
+      // a lane in flight; larger batches cost resident warps more than they gain).
+      constexpr int BATCH = 2 * PER < 8 ? 2 * PER : 8;
 #pragma unroll
-      for (int which = 0; which < 2; ++which) {
-        uint8_t* pool = which ? a.v : a.k;
-        uint4 x[PER];
-        long long from[PER];
+      for (int m0 = 0; m0 < 2 * PER; m0 += BATCH) {
+        uint4 x[BATCH];
+        bool have[BATCH];
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          const int vec = j * 32 + lane;
-          from[j] = __shfl_sync(kAll, src, vec / VPR);
-          x[j] = make_uint4(0, 0, 0, 0);
-          if (from[j] >= 0) x[j] = *reinterpret_cast<const uint4*>(pool + from[j] * ROW + (vec % VPR) * 16);
+        for (int b = 0; b < BATCH; ++b) {
+          const int j = (m0 + b) % PER, vec = j * 32 + lane;
+          const long long from = __shfl_sync(kAll, src, vec / VPR);
+          have[b] = from >= 0;
+          x[b] = make_uint4(0, 0, 0, 0);
+          if (have[b]) x[b] = *reinterpret_cast<const uint4*>((m0 + b < PER ? a.k : a.v) + from * ROW + (vec % VPR) * 16);
         }
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          const int vec = j * 32 + lane;
-          if (from[j] >= 0) *reinterpret_cast<uint4*>(pool + (dtile + vec / VPR) * ROW + (vec % VPR) * 16) = x[j];
+        for (int b = 0; b < BATCH; ++b) {
+          const int j = (m0 + b) % PER;
+          if (have[b]) *reinterpret_cast<uint4*>((m0 + b < PER ? a.k : a.v) + dtile * ROW + lane * 16 + j * 512) = x[b];
         }
       }
     } else {
@@ -464,25 +488,7 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactA
       if (lane == 0 && dst >= 0 && dst < a.num_blocks) scales[dtile >> 4] = s;
     }
   }
-  // ---- totals: of the page's tokens, and this warp's part of the zeros behind them
-  if (a.w_in && kh == h && which_blk == 0) {
-    const long long wrow = (long long)seq * a.keep_heads + kh;
-    float* wo = a.w_out + wrow * a.w_out_stride;
-    if (live && i < a.w_out_stride) {
-      float w = 0.f;
-      if (tok >= 0 && tok < a.w_in_stride) w = a.w_in[wrow * a.w_in_stride + tok];
-      else record_error(a.err, PA_ERR_BOUNDS);
-      wo[i] = w;
-    } else if (live) {
-      record_error(a.err, PA_ERR_BOUNDS);
-    }
-    const long long zeros = a.w_out_stride - kept;
-    if (zeros > 0) {
-      const long long each = (zeros + a.pages_per_row - 1) / a.pages_per_row;
-      const long long z0 = kept + each * page, z1 = min(a.w_out_stride, z0 + each);
-      for (long long z = z0 + lane; z < z1; z += 32) wo[z] = 0.f;
-    }
-  }
+  if (totals && live && i < a.w_out_stride) wo[i] = w;
 }
 
 typedef void (*CompactKernel)(CompactArgs);
