@@ -310,7 +310,11 @@ int pa_decode_weights(pa_pool* pool, int layer, void* out, int out_dtype, const 
   unsigned int* err = device_error_word();
   if (!err) return PA_ERR_CUDA;
   const CUtensorMap *tk = nullptr, *tv = nullptr;
-  st = layer_maps(pool, layer, &tk, &tv);
+  try {
+    st = layer_maps(pool, layer, &tk, &tv);
+  } catch (...) {  // (the pool's first use of a layer allocates its map on the host)
+    return fail(PA_ERR_NO_MEMORY, "host allocation failed");
+  }
   if (st) return st;
 
   DecodeArgs a = {};

@@ -181,6 +181,14 @@ class KVPool:
             with torch.cuda.device(self.device):
                 call(*args, _stream_handle(stream))
 
+    def _new(self, shape, dtype, stream) -> torch.Tensor:
+        """A tensor for the call's stream to write: allocated in that stream's order, so neither
+        its memory's last use nor its next one overlaps the call."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
     def reshape_and_cache(self, k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
                           layer: int = 0, stream=None) -> None:
         _need(k, "k", self.in_dtype, self.device)
@@ -209,7 +217,7 @@ class KVPool:
         if positions.numel() != T or slot_mapping.numel() != T:
             raise ValueError("positions and slot_mapping must hold one entry per token")
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=self.device)
+            q_out = self._new((T, Hq, D), q.dtype, stream)
         else:
             _need(q_out, "q_out", self.in_dtype, self.device)
             if q_out.shape != q.shape:
@@ -313,7 +321,7 @@ class KVPool:
             if weights.shape != weights_out.shape:
                 raise ValueError("weights and weights_out must have one shape")
         if out is None:
-            out = torch.empty((S, Hq, D), dtype=out_dtype or q.dtype, device=dev)
+            out = self._new((S, Hq, D), out_dtype or q.dtype, stream)
         else:
             _need(out, "out", None, dev)
             if out.shape != q.shape:
@@ -321,8 +329,7 @@ class KVPool:
         if softmax_scale is None:
             softmax_scale = 1.0 / math.sqrt(D)
         if workspace is None:
-            workspace = torch.empty(self.weights_workspace_bytes(S, Hq, max_blocks),
-                                    dtype=torch.uint8, device=dev)
+            workspace = self._new(self.weights_workspace_bytes(S, Hq, max_blocks), torch.uint8, stream)
         self._launch(N.pa_decode_weights,
                      (self.handle, layer, out.data_ptr(), _OUT_CODES[out.dtype], q.data_ptr(),
                       block_tables.data_ptr(), max_blocks, ctx_lens.data_ptr(), S, Hq, softmax_scale,
@@ -343,9 +350,9 @@ class KVPool:
             raise ValueError("weights must be [S, heads, tokens] and ctx_lens [S]")
         S, H, tokens = weights.shape
         if keep is None:
-            keep = torch.empty((S, H, budget), dtype=torch.int32, device=dev)
+            keep = self._new((S, H, budget), torch.int32, stream)
         if kept_lens is None:
-            kept_lens = torch.empty(S, dtype=torch.int32, device=dev)
+            kept_lens = self._new(S, torch.int32, stream)
         _all_need(dev, (keep, "keep", torch.int32), (kept_lens, "kept_lens", torch.int32))
         if keep.shape != (S, H, budget) or kept_lens.numel() != S:
             raise ValueError("keep must be [S, heads, budget] and kept_lens [S]")
@@ -373,7 +380,7 @@ class KVPool:
             raise ValueError("weights_out needs weights")
         if weights is not None:
             if weights_out is None:
-                weights_out = torch.empty_like(weights)
+                weights_out = self._new(weights.shape, torch.float32, stream)
             _all_need(self.device, (weights, "weights", torch.float32), (weights_out, "weights_out", torch.float32))
             for t, name in ((weights, "weights"), (weights_out, "weights_out")):
                 if t.dim() != 3 or t.shape[:2] != (S, H):
