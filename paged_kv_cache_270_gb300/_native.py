@@ -132,6 +132,8 @@ def library_path() -> str:
 def lib():
     """The loaded library.  Raises if it has not been built (no fallback)."""
     global _lib
+    if _lib is not None:  # (set once, under the lock)
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

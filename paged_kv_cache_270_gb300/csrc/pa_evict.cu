@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "pa_device.cuh"
 
@@ -502,10 +503,13 @@ CompactKernel pick_compact(const pa_pool* pool) {
 template <int C>
 cudaError_t launch_select(const SelectArgs& a, int smem, cudaStream_t st) {
   constexpr int NT = C == 1 ? 256 : 512;
-  if (smem > 24 * 1024) {
+  static std::atomic<bool> opted[128];  // per device: more than 48 KiB of shared memory
+  int dev = 0;
+  if (smem > 24 * 1024 && (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128 || !opted[dev])) {
     const cudaError_t e =
         cudaFuncSetAttribute(select_kernel<C, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelMaxKeys * 4);
     if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 128) opted[dev] = true;
   }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

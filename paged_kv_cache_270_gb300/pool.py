@@ -71,14 +71,11 @@ def _token_rows(t: torch.Tensor, name: str, dtype, device) -> int:
     """The token stride, in elements, of a [T, heads, head_dim] tensor whose tokens may lie
     apart (a slice of a fused projection) but are contiguous in themselves."""
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a tensor")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dim() != 3:
+        _need(t[0:0] if isinstance(t, torch.Tensor) else t, name, dtype, device)
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{name} must be [T, heads, head_dim]")
-    T, heads, d = t.shape
+    T, heads, d = shape
     st, sh, sd = t.stride()
     if (sd != 1 and d > 1) or (sh != d and heads > 1):
         raise ValueError(f"{name}: the heads and dimensions of a token must be contiguous")
