@@ -1087,7 +1087,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_bal_kernel(const Decode
           consumers_sync();  // (M, 1 / L), and every warp's scores
           const size_t row = ((size_t)sd.seq * a.Hkv + sd.h) * a.w_stride;
           if (write)
-            add_weights<kConsumerWarps * 32, 2>(score0, a.gs, s_unit_ml, a.w_in ? a.w_in + row : nullptr, a.w_out + row,
+            add_weights<kConsumerWarps * 32, C::kFp8 ? 2 : 1>(score0, a.gs, s_unit_ml, a.w_in ? a.w_in + row : nullptr, a.w_out + row,
                                                 a.decay, 0, totals_end(sd.ctx, a));
         }
       }
