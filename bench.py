@@ -93,12 +93,12 @@ DESCRIPTION = {
 # measured.
 NCU_TRAFFIC = {
     # hash of the decode source with comments and blank lines removed (see _source_sha)
-    "source_sha256": "1fffa0627ca9a67c2af353fbfdac22678835d4f261f9384f609d9a64fae42a63",
+    "source_sha256": "7cd4fd5c241a58e580d4709bfc92e95ee1e5107adb05735098d6b0ec1f55c6e2",
     # dram__bytes_read.sum + dram__bytes_write.sum of one decode launch
-    "bytes_per_launch": {"llama3_70b_fp8_a": 1073987328 + 3501568,
-                         "llama3_70b_fp8_b": 2151997952 + 4874240,
-                         "llama3_70b_fp8_block_a": 1076081664 + 2970112,
-                         "llama3_70b_fp8_block_b": 2156272128 + 4859136},
+    "bytes_per_launch": {"llama3_70b_fp8_a": 1073979904 + 3283456,
+                         "llama3_70b_fp8_b": 2152001536 + 4656384,
+                         "llama3_70b_fp8_block_a": 1076186624 + 2825728,
+                         "llama3_70b_fp8_block_b": 2156264960 + 4898304},
 }
 
 # --------------------------------------------------------------------- workers
@@ -202,12 +202,15 @@ def _p10_p90(xs):
 
 
 def _source_sha():
-    """sha256 of the decode kernel's code: pa_decode.cu and pa_device.cuh with
-    // comments, trailing blanks and empty lines removed, so that editing a
-    comment keeps the recorded traffic valid and any code change voids it."""
+    """sha256 of the decode kernels' code: pa_decode.cu, pa_device.cuh and
+    pa_decode_core.cuh with // comments, trailing blanks and empty lines removed, so
+    that editing a comment keeps the recorded traffic valid and any code change voids it."""
     h = hashlib.sha256()
-    for f in ("pa_decode.cu", "pa_device.cuh"):
-        with open(os.path.join(ROOT, "paged_kv_cache_270_gb300", "csrc", f)) as fh:
+    for f in ("pa_decode.cu", "pa_device.cuh", "pa_decode_core.cuh"):
+        path = os.path.join(ROOT, "paged_kv_cache_270_gb300", "csrc", f)
+        if not os.path.exists(path):
+            continue
+        with open(path) as fh:
             lines = (re.sub(r"//.*$", "", ln).rstrip() for ln in fh.read().splitlines())
             h.update(("\n".join(ln for ln in lines if ln.strip()) + "\n").encode())
     return h.hexdigest()
