@@ -232,25 +232,32 @@ def test_bad_lengths_are_reported():
 
 
 def test_timeout_leaves_the_context_usable():
-    """Waits that run out are reported; the next call is right.  (64 sequences of 1024
-    tokens: with the GPU this busy, waits outlast the hardware's own brief first test.)"""
-    w = W.make("llama3_70b_fp8_b", scale_down=4)
-    w.compute_fp8_scales()
-    pool = new_pool(w, 0)
-    fill_both(w, pool, None)
-    q = bits_to_torch(w.q_bits(), "bf16")
-    t, c = torch.from_numpy(w.block_tables).cuda(), torch.from_numpy(w.ctx_lens).cuda()
-    zeros = torch.zeros(w.S, w.n_kv_heads, int(w.ctx_lens.max()), device="cuda")
-    want, tot = pool.decode_weights(q, t, c, None, weights_out=zeros.clone())
+    """Waits that run out are reported; the next call is right.  A wait outlasts the
+    hardware's own brief first test only now and then, so the GPU is kept busy (256
+    sequences of 4096 tokens) and the call repeated until one does."""
+    from paged_kv_cache_270_gb300.pool import KVPool
+    S, n = 256, 4096
+    pool = KVPool(1, S * n // 16, 8, 128, "fp8_e4m3", 0.01, 0.01)
+    pool.k_cache.random_(0, 120)
+    pool.v_cache.random_(0, 120)
+    q = torch.randn(S, 64, 128, device="cuda").to(torch.bfloat16)
+    t = torch.randperm(S * n // 16, device="cuda").to(torch.int32).view(S, -1)
+    c = torch.full((S,), n, dtype=torch.int32, device="cuda")
+    tot = torch.zeros(S, 8, n, device="cuda")
+    want, first = pool.decode_weights(q, t, c, None, weights_out=tot.clone())
     torch.cuda.synchronize()
+    assert pool.device_error() == N.PA_OK
+    seen = []
     try:
         N.pa_set_pipeline_wait_limit_ns(1)
-        pool.decode_weights(q, t, c, None, weights_out=zeros.clone())
-        assert pool.device_error() == N.PA_ERR_TIMEOUT
+        while len(seen) < 200 and N.PA_ERR_TIMEOUT not in seen:
+            pool.decode_weights(q, t, c, None, weights_out=tot)
+            seen.append(pool.device_error())
     finally:
         torch.cuda.synchronize()
         N.pa_set_pipeline_wait_limit_ns(0)
-    out, again = pool.decode_weights(q, t, c, None, weights_out=zeros.clone())
+    assert set(seen) <= {N.PA_OK, N.PA_ERR_TIMEOUT} and seen[-1] == N.PA_ERR_TIMEOUT
+    out, again = pool.decode_weights(q, t, c, None, weights_out=tot)
     assert pool.device_error() == N.PA_OK
-    assert torch.equal(out, want) and torch.equal(again, tot)
+    assert torch.equal(out, want) and torch.equal(again, first)
     pool.close()
