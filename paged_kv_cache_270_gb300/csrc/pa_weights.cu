@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kFinishThreads, 4) weights_finish_kernel(const
           float sum = 0.f;
 #pragma unroll
           for (int i = 0; i < kFinishWarps; ++i) sum += m[i] == -INFINITY ? 0.f : fast_exp2(m[i] - s_ml[head].x) * o[i];
-          store_out<OUT>(a.out, (row0 + head) * D + dim, sum * s_ml[head].y * a.v_scale);
+          store_out<OUT>(a.out, (row0 + head) * D + dim, s_ml[head].y > 0.f ? sum * s_ml[head].y * a.v_scale : 0.f);
         }
       } else {
         for (int gi = g0; gi < g1; ++gi) {
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kFinishThreads, 4) weights_finish_kernel(const
             float sum = 0.f;
 #pragma unroll
             for (int w = 0; w < kFinishWarps; ++w) sum += s_red[w][lane];
-            store_out<OUT>(a.out, (row0 + head) * D + dim, sum * s_ml[head].y * a.v_scale);
+            store_out<OUT>(a.out, (row0 + head) * D + dim, s_ml[head].y > 0.f ? sum * s_ml[head].y * a.v_scale : 0.f);
           }
           __syncthreads();
         }

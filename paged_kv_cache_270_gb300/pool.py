@@ -347,11 +347,11 @@ class KVPool:
             raise ValueError("weights must be [S, heads, tokens] and ctx_lens [S]")
         S, H, tokens = weights.shape
         if keep is None:
-            keep = self._new((S, H, budget), torch.int32, stream)
+            keep = self._new((S, H, max(budget, 0)), torch.int32, stream)
         if kept_lens is None:
             kept_lens = self._new(S, torch.int32, stream)
         _all_need(dev, (keep, "keep", torch.int32), (kept_lens, "kept_lens", torch.int32))
-        if keep.shape != (S, H, budget) or kept_lens.numel() != S:
+        if keep.shape != (S, H, max(budget, 0)) or kept_lens.numel() != S:
             raise ValueError("keep must be [S, heads, budget] and kept_lens [S]")
         self._launch(N.pa_evict_select,
                      (self.handle, weights.data_ptr(), tokens, ctx_lens.data_ptr(), S, H, budget, sinks,

@@ -116,6 +116,9 @@ def test_select_bounds_and_wrapper():
             pool.evict_select(a["weights"], a["ctx"], 4, keep=a["keep"])
     with pytest.raises(N.PAError):
         pool.evict_select(w, c, 4, sinks=3, recent=2)
+    for budget in (0, -1):
+        with pytest.raises(N.PAError):
+            pool.evict_select(w, c, budget)
     pool.close()
 
 

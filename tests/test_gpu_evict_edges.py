@@ -170,6 +170,24 @@ def test_infinities_and_nan():
     pool.close()
 
 
+def test_a_nan_key_in_a_row_of_many_ctas():
+    """A row that many CTAs share ends as pa_decode's does: zeros out, NaN weights, and the
+    other rows untouched."""
+    pool = _pool("bf16", 2, 128, 900)
+    pool.k_cache.view(torch.bfloat16).normal_()
+    pool.v_cache.view(torch.bfloat16).normal_()
+    t = torch.randperm(900, device="cuda")[:800].to(torch.int32).view(1, 800)
+    ctx = torch.tensor([12800], dtype=torch.int32, device="cuda")
+    q = torch.randn(1, 16, 128, device="cuda").to(torch.bfloat16)
+    clean, w0 = pool.decode_weights(q, t, ctx, None, weights_out=torch.zeros(1, 2, 12800, device="cuda"))
+    pool.layer_view("k").view(torch.bfloat16)[int(t[0, 333]), 1, 7] = math.nan
+    out, w1 = pool.decode_weights(q, t, ctx, None, weights_out=torch.zeros(1, 2, 12800, device="cuda"))
+    want = pool.decode(q, t, ctx)
+    assert torch.equal(out[:, :8], clean[:, :8]) and torch.equal(w1[:, 0], w0[:, 0])
+    assert bool((want[:, 8:] == 0).all()) and bool((out[:, 8:] == 0).all()) and bool(w1[:, 1].isnan().all())
+    pool.close()
+
+
 def test_two_graphs_share_a_workspace():
     """Nothing in the workspace outlives a call: two captured decodes with one workspace,
     replayed in turn, keep giving their own results."""
