@@ -35,7 +35,9 @@ constexpr unsigned kAll = 0xffffffffu;
 // with the k-th one; every key of the share has a value (the tokens that stay
 // anyway above all others, places behind the context below all), so no pass
 // tests where a key lies; and the bin search reads 64 sums of 32 bins from each
-// CTA, then 32 bins.
+// CTA, then 32 bins.  32 rows of 131072 tokens: 21 us (their 17 MB would take 2.5
+// at a copy's rate), with eight-bit digits and one key at a time 46; 512 rows of up to
+// 4096: 9.7 us.
 constexpr int kSelBins = 2048;
 constexpr int kSelMaxKeys = 49152;  // keys a CTA keeps (192 KiB); longer shares are read again in each pass
 constexpr uint32_t kKeyNone = 0u;            // behind the context
@@ -326,7 +328,9 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 2) select_kernel(const Sel
 // One warp per destination page of a (sequence, kv head): 16 rows, gathered
 // from wherever they lie.  Lanes 0-15 resolve the rows' addresses; the rows
 // then move as 16-byte vectors, all loads of a batch in flight before the
-// first store.
+// first store.  Bound by HBM where rows are copied: 4 x 32768 of 131072 tokens,
+// bf16 166 us (6.5 TB/s), FP8 86 us (6.3).  With a scale per tile 117 us: the
+// conversions between the loads and the stores; 296 with a division per code.
 struct CompactArgs {
   const int32_t* keep;
   int keep_heads, budget;
