@@ -327,6 +327,8 @@ class KVPool:
             softmax_scale = 1.0 / math.sqrt(D)
         if workspace is None:
             workspace = self._new(self.weights_workspace_bytes(S, Hq, max_blocks), torch.uint8, stream)
+        else:
+            _need(workspace, "workspace", None, dev)
         self._launch(N.pa_decode_weights,
                      (self.handle, layer, out.data_ptr(), _OUT_CODES[out.dtype], q.data_ptr(),
                       block_tables.data_ptr(), max_blocks, ctx_lens.data_ptr(), S, Hq, softmax_scale,

@@ -44,6 +44,17 @@ def test_no_sequences(pool):
     _call(pool, S=0, q=0, out=0, w_out=0, ws=0)
 
 
+@pytest.mark.parametrize("ws", [torch.empty(1 << 20, dtype=torch.uint8, device="meta"),
+                                torch.empty(1, dtype=torch.uint8).expand(1 << 20), b"bytes"])
+def test_a_workspace_of_another_device_or_with_repeated_memory(ws):
+    from paged_kv_cache_270_gb300.pool import KVPool
+    p = KVPool(1, 8, 2, 64, "fp16", device="cpu")
+    with pytest.raises((TypeError, ValueError), match="workspace"):
+        p.decode_weights(torch.zeros(1, 4, 64, dtype=torch.float16), torch.zeros(1, 4, dtype=torch.int32),
+                         torch.zeros(1, dtype=torch.int32), torch.zeros(1, 2, 64), workspace=ws)
+    p.close()
+
+
 def test_workspace_refusals(pool):
     for args, code in (((-1, 4, 4), INV), ((3, 5, 4), INV), ((3, 18, 4), UNS), ((3, 4, 0), INV)):
         with pytest.raises(N.PAError) as e:
