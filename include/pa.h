@@ -522,9 +522,10 @@ PA_API int pa_decode_weights_workspace_bytes(const pa_pool* pool, int S, int n_q
  *   workspace      device scratch of at least pa_decode_weights_workspace_bytes;
  *                  calls that may overlap on the GPU need one each
  * Everything else is as for pa_decode, with its balanced schedule (any number
- * of sequences; the contexts' lengths are read on the device).  A total takes
- * the weights in fp32, a fixed order of additions, so equal inputs give equal
- * bits. */
+ * of sequences; the contexts' lengths are read on the device), except that the
+ * weights keep their precision in the product with V for 16-bit outputs too, whose
+ * error is that of the fp32 output and one rounding.  A total takes the weights in
+ * fp32, a fixed order of additions, so equal inputs give equal bits. */
 PA_API int pa_decode_weights(pa_pool* pool, int layer, void* out, int out_dtype, const void* q,
                              const int32_t* block_tables_dev, int max_blocks_per_seq,
                              const int32_t* ctx_lens_dev, int S, int n_q_heads,

@@ -181,7 +181,12 @@ struct Kernels {
 
 template <int KV, int D, int OUT>
 struct Build {
-  static constexpr bool kPsplit = (KV == KV_BF16) || (OUT == OUT_F32);
+  // The weights keep their precision in the product with V, also for 16-bit outputs (a
+  // second product with what rounding them to 16 bits drops).  With one product the
+  // bf16 output of FP8 pages is off from a value rounded once by 7e-4 of its norm, with
+  // two by 1e-4.  The second one costs 256 x 4096 tokens of FP8 390 -> 395 us, with a
+  // scale per tile 406 -> 414, 4 x 131072 nothing that shows (208).
+  static constexpr bool kPsplit = true;
   static constexpr int kMinB = std::min(Cfg<KV, D>::kMinBlocks, 4);  // the schedule puts at most four CTAs on an SM
   static constexpr auto kDecode = &decode_bal_kernel<KV, D, OUT, kPsplit, kMinB, true>;
   static cudaError_t launch(const DecodeArgs& a, const CUtensorMap* tk, const CUtensorMap* tv, cudaStream_t st) {
