@@ -201,25 +201,28 @@ __device__ __forceinline__ uint2 codes8(const float* y, float s) {
 // Items [lt, items) of one token's heads, `nt` apart: item i is unit i % UNITS of
 // head i / UNITS, IPT of them at a time, every load of a batch issued before the
 // first use.  `first` runs behind the first batch's loads (the token's table);
-// put(h, v0, v1, in, y) stores the turned unit.
+// put(h, v0, v1, in, y) stores the turned unit.  The rounds are counted per warp,
+// not per lane: in a last round with fewer than 32 items the lanes without one
+// take part in the warp's barrier all the same.
 template <bool BF, int D, int LAY, bool FULL, typename First, typename Put>
 __device__ __forceinline__ void turn_heads(const uint16_t* src, int items, int rot, int lt, int nt, const float2* cs,
                                            First first, Put put) {
   constexpr int UNITS = D / 16, IPT = LAY == ROPE_HALF_ODD ? 1 : 2;
-  for (int base = lt; base < items || base == lt; base += nt * IPT) {
+  const int lane = lt & 31, warp0 = lt - lane;
+  for (int base = warp0; base < items || base == warp0; base += nt * IPT) {
     UnitIn<LAY> in[IPT];
 #pragma unroll
     for (int j = 0; j < IPT; ++j) {
-      const int i = base + j * nt;
+      const int i = base + lane + j * nt;
       if (i < items) load_unit<LAY, FULL>(src + (i / UNITS) * D, i % UNITS, FULL ? D : rot, in[j]);
     }
-    if (base == lt) first();
+    if (base == warp0) first();
     // The table is complete; and with q_out == q a row's partners, which its own
     // warp reads (above), are read before any lane writes the row.
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < IPT; ++j) {
-      const int i = base + j * nt;
+      const int i = base + lane + j * nt;
       if (i < items) {
         int v0, v1;
         unit_vecs<LAY>(i % UNITS, FULL ? D : rot, v0, v1);
