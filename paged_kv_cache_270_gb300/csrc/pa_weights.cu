@@ -53,6 +53,7 @@ template <int KV, int D, int OUT>
 __global__ void __launch_bounds__(kFinishThreads, 4) weights_finish_kernel(const DecodeArgs a) {
   constexpr int kUnit = BalCfg<KV, D>::kUnitCostPages;
   __shared__ float2 s_ml[8];  // (M, 1 / L) of the unit's heads
+  __shared__ float s_inv[8];  // 1 / L for the output rows: 0 where no score was finite
   __shared__ float s_red[kFinishWarps][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dependency_wait();
@@ -95,7 +96,10 @@ __global__ void __launch_bounds__(kFinishThreads, 4) weights_finish_kernel(const
             M = mn;
           }
         }
-        if (lane == 0) s_ml[warp] = warp < a.G ? make_float2(M, 1.f / L) : make_float2(0.f, 0.f);
+        if (lane == 0) {
+          s_ml[warp] = warp < a.G ? make_float2(M, 1.f / L) : make_float2(0.f, 0.f);
+          s_inv[warp] = L > 0.f ? 1.f / L : 0.f;
+        }
       }
       __syncthreads();
       // this CTA's slice of the output rows, 32 values at a time.  Few pieces: a
@@ -120,7 +124,7 @@ __global__ void __launch_bounds__(kFinishThreads, 4) weights_finish_kernel(const
           float sum = 0.f;
 #pragma unroll
           for (int i = 0; i < kFinishWarps; ++i) sum += m[i] == -INFINITY ? 0.f : fast_exp2(m[i] - s_ml[head].x) * o[i];
-          store_out<OUT>(a.out, (row0 + head) * D + dim, s_ml[head].y > 0.f ? sum * s_ml[head].y * a.v_scale : 0.f);
+          store_out<OUT>(a.out, (row0 + head) * D + dim, s_inv[head] > 0.f ? sum * s_inv[head] * a.v_scale : 0.f);
         }
       } else {
         for (int gi = g0; gi < g1; ++gi) {
@@ -147,7 +151,7 @@ __global__ void __launch_bounds__(kFinishThreads, 4) weights_finish_kernel(const
             float sum = 0.f;
 #pragma unroll
             for (int w = 0; w < kFinishWarps; ++w) sum += s_red[w][lane];
-            store_out<OUT>(a.out, (row0 + head) * D + dim, s_ml[head].y > 0.f ? sum * s_ml[head].y * a.v_scale : 0.f);
+            store_out<OUT>(a.out, (row0 + head) * D + dim, s_inv[head] > 0.f ? sum * s_inv[head] * a.v_scale : 0.f);
           }
           __syncthreads();
         }
