@@ -214,7 +214,8 @@ __device__ __forceinline__ void drop_lines(const float* p, int bytes) {
 
 // Turns the scores of tokens [t0, t1) of a unit (t0 a multiple of 16) into
 // weights, sum over heads of 2^(x - M) / L, and adds them to the totals.  ml:
-// (M, 1 / L) of the gs heads, (0, 0) for a padding one.  Called by NT threads.
+// (M, 1 / L) of the gs heads, (0, 0) for a padding one, whose scores are 0.  Called
+// by NT threads.
 // With eight heads two lanes share a token (16-byte loads, 512 contiguous bytes
 // per warp instruction) and swap halves, so each lane writes one token of two
 // load rounds; with four heads a lane holds a token; other groups are loaded as
@@ -343,13 +344,15 @@ __device__ __forceinline__ int totals_end(int end, const DecodeArgs& a) {
 // softmax update of (m, l) and the rescale of O, then O^T += V_page^T . P^T.
 // Ks, Vs: the page's K and V tiles in shared memory; tok0: its first token;
 // sc: its (K, V) tile scales (block-scaled pools).  SC: the page's scores are
-// also stored, at score [16 tokens][gs heads] (behind the context: -inf).
+// also stored, at score [16 tokens][gs heads] (behind the context: -inf), of the
+// group's `heads`; the place of a head that an odd group lacks gets 0, whatever the
+// key (its product with the absent query is NaN where the key is infinite).
 template <int KV, int D, bool PSPLIT, bool SC = false>
 __device__ __forceinline__ void consume_page(const uint8_t* Ks, const uint8_t* Vs, int tok0, int ctx,
                                              float qk_scale, const uint32_t (&qf)[D / 8],
                                              const uint2* qsm, const float2* sc, float& m0, float& m1,
                                              float& l0, float& l1, float (&o)[D / 16][4], float& vinv,
-                                             float* score = nullptr, int gs = 0) {
+                                             float* score = nullptr, int gs = 0, int heads = 0) {
   using C = Cfg<KV, D>;
   constexpr bool BF = C::kMmaBf16;
   constexpr bool SWZ = C::kSwizzle;
@@ -482,8 +485,9 @@ __device__ __forceinline__ void consume_page(const uint8_t* Ks, const uint8_t* V
           score[kg1] = x2;
         }
       } else if (2 * t < gs) {
-        store_kept(score + kg0 * gs + 2 * t, x0, x1);
-        store_kept(score + kg1 * gs + 2 * t, x2, x3);
+        const bool pair = 2 * t + 1 < heads;
+        store_kept(score + kg0 * gs + 2 * t, x0, pair ? x1 : 0.f);
+        store_kept(score + kg1 * gs + 2 * t, x2, pair ? x3 : 0.f);
       }
     }
     float pm0 = fmaxf(x0, x2), pm1 = fmaxf(x1, x3);
@@ -984,7 +988,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_bal_kernel(const Decode
         float* score = nullptr;
         if constexpr (SC) score = score0 + (size_t)(pg0 + k - kb) * 16 * a.gs;
         consume_page<KV, D, PSPLIT, SC>(Ks, Ks + C::kTile, (pg0 + k - kb) * 16, ctx, qk_scale, qf, qsm,
-                                        &stage_scale[stage], m0, m1, l0, l1, o, vinv, score, SC ? a.gs : 0);
+                                        &stage_scale[stage], m0, m1, l0, l1, o, vinv, score, SC ? a.gs : 0, SC ? a.G : 0);
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
       }

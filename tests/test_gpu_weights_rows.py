@@ -1,5 +1,5 @@
-"""Rows of pa_decode_weights without a finite score, whether one CTA holds the row whole or
-several share it."""
+"""Rows of pa_decode_weights without a finite score, and keys of infinite size, whether one
+CTA holds the row whole or several share it."""
 import math
 
 import pytest
@@ -34,5 +34,26 @@ def test_a_row_without_a_finite_score_ends_in_zeros(kv, n):
     others = [h for h in range(16) if h != 3]
     assert torch.equal(out[:, others], clean[:, others])
     assert bool(w1[0, 0].isnan().all()) and torch.equal(w1[0, 1], w0[0, 1])
+    assert pool.device_error() == N.PA_OK
+    pool.close()
+
+
+@pytest.mark.parametrize("kv", ["fp16", "bf16"])
+@pytest.mark.parametrize("G", [3, 5, 7])
+@pytest.mark.parametrize("n", [40, 12800])
+def test_a_key_of_infinite_size_in_an_odd_group(kv, G, n):
+    """A key whose scores are all -inf weighs nothing: its total stays, and so does every
+    other number finite, in a group of any size (an odd one keeps a place for one head more)."""
+    pool, t, c, _, _ = _filled(kv, 2, 64, [n], seed=G)
+    q = torch.randn(1, 2 * G, 64, device="cuda").abs().add(0.1).to(pool.in_dtype)
+    at = n - 7
+    pool.layer_view("k").view(pool.in_dtype)[int(t[0, at // 16]), 1, at % 16, 5] = -math.inf
+    start = torch.rand(1, 2, n, device="cuda")
+    out, w = pool.decode_weights(q, t, c, start, weights_out=torch.zeros_like(start), out_dtype=torch.float32)
+    assert bool((w[0, 1, at] == start[0, 1, at])), w[0, 1, at]
+    assert bool(w.isfinite().all()) and bool(out.isfinite().all())
+    # the weights of a row add up to its heads: n additions and as many roundings as in the kernels' sum
+    added = (w.double() - start.double()).sum(-1)
+    assert float((added - G).abs().max()) <= G * (16 + n) * 2.0 ** -23 + n * 2.0 ** -24 * 2
     assert pool.device_error() == N.PA_OK
     pool.close()
