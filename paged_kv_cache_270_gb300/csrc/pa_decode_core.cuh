@@ -1043,7 +1043,8 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_bal_kernel(const Decode
       const SegDesc sd = *mine_d;
       const bool direct = sd.pg0 == 0 && sd.len == sd.npages;
       const int pslot = 2 * blockIdx.x + (j == 0 ? 0 : 1);
-      const bool write = have_q && !*abort_flag;
+      bool write = have_q && !*abort_flag;
+      if constexpr (SC) write = __all_sync(kFull, write);  // one decision per warp: add_weights shuffles
       if (write && !direct && sd.pg0 == 0 && threadIdx.x == 0) s_job = make_int4(sd.seq, sd.h, sd.last_cta, pslot);
       const int tid = threadIdx.x;  // 0 .. 127
       for (int idx = tid; idx < a.G * D && write; idx += kConsumerWarps * 32) {
