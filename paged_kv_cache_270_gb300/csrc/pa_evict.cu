@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 2) select_kernel(const Sel
   int32_t* keep = a.keep + (long long)row * a.budget;
   if (tid == 0 && rank == 0 && row == seq * a.H) a.kept[seq] = min(n, a.budget);
   if (n <= a.budget) {  // everything stays (the same for all CTAs of the row)
-    for (int i = rank * NT + tid; i < a.budget; i += C * NT) keep[i] = i < n ? i : -1;
+    for (long long i = rank * NT + tid; i < a.budget; i += C * NT) keep[i] = i < n ? (int)i : -1;
     return;
   }
 
