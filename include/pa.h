@@ -308,7 +308,7 @@ PA_API int pa_reshape_and_cache(pa_pool* pool, int layer, const void* k, const v
 /* the same blend with g falling linearly in i, from 1 at the pair that turns
  * `high` times (its index rounded down, at least 0) to 0 at the one that turns
  * `low` times (rounded up, at most rot_dim - 1); a model so scaled usually
- * takes gain = 0.1 ln(factor) + 1 */
+ * takes gain = 0.1 ln(factor) + 1, and 1 for a factor of at most 1 */
 #define PA_ROPE_SCALE_YARN 4
 
 /* Description of a rotary embedding.

@@ -58,11 +58,11 @@ def make_rope(rot_dim: int, layout: str = "half", theta: float = 10000.0, scalin
     """A rotary embedding for ``KVPool.rope_and_cache`` (see pa_rope_desc).
 
     ``high`` defaults to 4 turns for "bands" and 32 for "yarn"; ``gain`` to 1, and
-    for "yarn" to 0.1 ln(factor) + 1."""
+    for "yarn" with a factor above 1 to 0.1 ln(factor) + 1."""
     if high is None:
         high = 32.0 if scaling == "yarn" else 4.0
     if gain is None:
-        gain = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 0 else 1.0
+        gain = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 1 else 1.0
     return N.pa_rope_init(N.pa_rope_desc(ROPE_LAYOUTS[layout], rot_dim, ROPE_SCALINGS[scaling], theta,
                                          factor, original_len, low, high, gain), divisors)
 
