@@ -505,7 +505,9 @@ PA_API int pa_decode_no_alloc(pa_pool* pool, int layer, void* out, int out_dtype
 /* Device scratch bytes pa_decode_weights needs for this shape: each token's
  * scores, min(S, 4096) * n_kv_heads * max_blocks_per_seq * 16 * gs * 4 with
  * gs = G = n_q_heads / n_kv_heads rounded up to an even number (1 stays 1),
- * and the partial states and bookkeeping of pa_decode's balanced schedule.  Only the parts that the contexts reach are touched. */
+ * and the partial states and bookkeeping of pa_decode's balanced schedule.  Only the parts
+ * that the contexts reach are touched.  PA_ERR_UNSUPPORTED for tables of more than
+ * 2^27 - 256 blocks, whose tokens are not counted in 32 bits, here and in pa_decode_weights. */
 PA_API int pa_decode_weights_workspace_bytes(const pa_pool* pool, int S, int n_q_heads,
                                              int max_blocks_per_seq, size_t* bytes);
 

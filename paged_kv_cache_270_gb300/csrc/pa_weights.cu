@@ -273,6 +273,14 @@ Workspace layout(int ctas, int S, int Hq, int Hkv, int D, int max_blocks) {
   return w;
 }
 
+// Tokens are indexed in 32 bits, up to 4096 past the last one of a row (a round of
+// the weighing).
+int check_width(int max_blocks) {
+  if (max_blocks > (1 << 27) - 256)
+    return fail(PA_ERR_UNSUPPORTED, "tables of at most 2^27 - 256 blocks (got %d)", max_blocks);
+  return PA_OK;
+}
+
 }  // namespace
 
 int weights_set_wait_limit(unsigned long long ns) { return (int)set_pipe_wait_limit_here(ns); }
@@ -287,6 +295,7 @@ int pa_decode_weights_workspace_bytes(const pa_pool* pool, int S, int n_q_heads,
                                       size_t* bytes) {
   int st = check_shape(pool, S, n_q_heads, max_blocks_per_seq);
   if (st) return st;
+  if ((st = check_width(max_blocks_per_seq))) return st;
   if (!bytes) return fail(PA_ERR_INVALID, "null output");
   const pa_pool_desc& d = pool->desc;
   // the size does not depend on the output dtype: that of the query dtype's build
@@ -305,6 +314,7 @@ int pa_decode_weights(pa_pool* pool, int layer, void* out, int out_dtype, const 
   pa::TraceRange trace_("pa_decode_weights");
   int st = check_decode_args(pool, layer, out_dtype, S, n_q_heads, max_blocks_per_seq, softmax_scale);
   if (st) return st;
+  if ((st = check_width(max_blocks_per_seq))) return st;
   if (!std::isfinite(decay)) return fail(PA_ERR_INVALID, "decay must be finite");
   if (weights_stride < 1 || weights_stride >= (size_t)1 << 40)
     return fail(PA_ERR_INVALID, "weights_stride must be at least 1 and below 2^40");
