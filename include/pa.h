@@ -334,8 +334,10 @@ typedef struct pa_rope_desc {
 
 /* A rotary embedding ready for use: plain data, to be filled by pa_rope_init
  * and copied freely.  step[i] is pair i's speed as a 64-bit binary fraction of
- * a turn per position, so position times step, modulo 2^64, is the pair's
- * angle with no error that grows with the position (2^-34 of a turn at 2^31). */
+ * a turn per position: position times step, modulo 2^64, is the pair's angle, whole
+ * turns dropped without a rounding.  The speed itself is made in double precision
+ * (off by at most 2^-53 of a turn per position where nothing scales or divides it:
+ * 2^-33 of a turn at a million, 2^-22 at 2^31). */
 typedef struct pa_rope {
   int layout;
   int rot_dim;
@@ -370,7 +372,8 @@ PA_API int pa_rope_init(const pa_rope_desc* desc, const double* divisors, pa_rop
  *   slot_mapping_dev  as for pa_reshape_and_cache: a negative slot skips the
  *                 write (the token's query is rotated all the same), a slot
  *                 past the pool is skipped and sets PA_ERR_BOUNDS
- * Angles are exact to 2^-34 of a turn; the rotation is done in fp32 and
+ * The angle of a position is that of its pa_rope's speeds, rounded to 2^-26 of a
+ * turn for its cosine and sine; the rotation is done in fp32 and
  * rounded once: to 16 bits for q_out and 16-bit pools, and for FP8 pools to the
  * code that pa_reshape_and_cache gives the fp32 value (not its 16-bit
  * rounding).  PA_FP8_E4M3_BLOCK pools take runs and tile scales as described

@@ -6,7 +6,9 @@
 // fp32 rate on this part.  So the speed is kept as a 64-bit binary fraction of
 // a turn, F_i = f_i / (2 pi) * 2^64: p F_i modulo 2^64 is the angle's fraction
 // of a turn, one integer multiply with no reduction step, and its upper bits as a
-// signed fraction of half a turn are the argument of sincospi.
+// signed fraction of half a turn are the argument of sincospi.  F_i comes from a
+// double: off by at most 2^-53 of a turn per position (2^-33 of a turn at a million, 2^-22
+// at 2^31); the argument's rounding to fp32 is 2^-26 of a turn.
 //
 // The work is a copy with some arithmetic in it, bound by HBM: 16-byte loads
 // and stores, each thread owning both halves of eight pairs.  A warp makes its
