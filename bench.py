@@ -93,12 +93,12 @@ DESCRIPTION = {
 # measured.
 NCU_TRAFFIC = {
     # hash of the decode source with comments and blank lines removed (see _source_sha)
-    "source_sha256": "7cd4fd5c241a58e580d4709bfc92e95ee1e5107adb05735098d6b0ec1f55c6e2",
+    "source_sha256": "95687e02e65c146698d006bb021b5436a4c434915f59be22490306ca973363bb",
     # dram__bytes_read.sum + dram__bytes_write.sum of one decode launch
-    "bytes_per_launch": {"llama3_70b_fp8_a": 1073979904 + 3283456,
-                         "llama3_70b_fp8_b": 2152001536 + 4656384,
-                         "llama3_70b_fp8_block_a": 1076186624 + 2825728,
-                         "llama3_70b_fp8_block_b": 2156264960 + 4898304},
+    "bytes_per_launch": {"llama3_70b_fp8_a": 1074016512 + 3611392,
+                         "llama3_70b_fp8_b": 2151990272 + 4702976,
+                         "llama3_70b_fp8_block_a": 1076191232 + 2869248,
+                         "llama3_70b_fp8_block_b": 2156261376 + 4988672},
 }
 
 # --------------------------------------------------------------------- workers
