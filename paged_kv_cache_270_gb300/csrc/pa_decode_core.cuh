@@ -342,6 +342,10 @@ __device__ __forceinline__ int totals_end(int end, const DecodeArgs& a) {
 
 // One page of a consumer warp: S^T = K_page . Q^T for the group, the online
 // softmax update of (m, l) and the rescale of O, then O^T += V_page^T . P^T.
+// The product with V takes P in V's 16-bit type, as it is rounded to that (2^-12 of
+// a weight in binary16, 2^-9 in bfloat16), or with PSPLIT as the sum of that
+// and what the rounding dropped, in a second product (2^-22, 2^-17): bfloat16
+// pools, fp32 outputs and pa_decode_weights.  Row sums and maxima are fp32.
 // Ks, Vs: the page's K and V tiles in shared memory; tok0: its first token;
 // sc: its (K, V) tile scales (block-scaled pools).  SC: the page's scores are
 // also stored, at score [16 tokens][gs heads] (behind the context: -inf), of the

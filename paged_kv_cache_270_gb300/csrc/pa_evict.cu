@@ -37,7 +37,7 @@ constexpr unsigned kAll = 0xffffffffu;
 // tests where a key lies; and the bin search reads 64 sums of 32 bins from each
 // CTA, then 32 bins.  32 rows of 131072 tokens: 21 us (their 17 MB would take 2.5
 // at a copy's rate), with eight-bit digits and one key at a time 46; 512 rows of up to
-// 4096: 9.7 us.
+// 4096: 10.3 us.
 constexpr int kSelBins = 2048;
 constexpr int kSelMaxKeys = 49152;  // keys a CTA keeps (192 KiB); longer shares are read again in each pass
 constexpr uint32_t kKeyNone = 0u;            // behind the context
@@ -329,8 +329,9 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 5 : 2) select_kernel(const Sel
 // from wherever they lie.  Lanes 0-15 resolve the rows' addresses; the rows
 // then move as 16-byte vectors, all loads of a batch in flight before the
 // first store.  Bound by HBM where rows are copied: 4 x 32768 of 131072 tokens,
-// bf16 166 us (6.5 TB/s), FP8 86 us (6.3).  With a scale per tile 117 us: the
-// conversions between the loads and the stores; 296 with a division per code.
+// bf16 166 us (6.5 TB/s), FP8 87 us (6.2).  With a scale per tile 117 us, and 127
+// with totals in rows of 131072: the conversions between the loads and the
+// stores; 296 with a division per code.
 struct CompactArgs {
   const int32_t* keep;
   int keep_heads, budget;
@@ -565,7 +566,8 @@ int pa_evict_select(pa_pool* pool, const float* weights, size_t weights_stride, 
   a.kept = kept_lens_dev;
   a.err = err;
   // CTAs per row: one up to 8192 tokens, then enough that a share is at most
-  // 16384 keys (64 KiB, three CTAs per SM), up to the portable cluster of eight.
+  // 16384 keys (64 KiB; with the histograms' 16 two CTAs fit an SM), up to the portable
+  // cluster of eight: past 131072 tokens the shares grow.
   const long long tokens = a.stride;
   const int C = tokens <= 8192 ? 1 : tokens <= 32768 ? 2 : tokens <= 65536 ? 4 : 8;
   a.max_keys = (int)std::min<long long>(((tokens + C - 1) / C + 127) / 128 * 128, kSelMaxKeys);

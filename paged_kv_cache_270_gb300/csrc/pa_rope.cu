@@ -37,7 +37,7 @@ constexpr int kRopeWarps = 8;  // per CTA
 // A token gets one warp, or up to eight while the call has fewer than this many
 // warps: each warp makes its own table, so more warps a token cost instructions,
 // fewer leave SMs idle.  64 tokens of 32 / 8 heads (bf16): 6.1 us with one warp a
-// token, 3.5 with eight; 1024 of 64 / 8 (FP8): 17.3 with one, 12.6 with two, 13.8
+// token, 3.7 with eight; 1024 of 64 / 8 (FP8): 17.3 with one, 12.6 with two, 13.8
 // with eight; 8192: 56 us with one or two (5.7 TB/s), 83 with eight.
 constexpr int kRopeFewWarps = 2048;
 

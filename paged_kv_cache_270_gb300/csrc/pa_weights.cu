@@ -14,12 +14,15 @@
 // cost D e (50%).
 //
 // Measured against pa_decode's balanced schedule: 256 x 4096 tokens of FP8, G =
-// 8, 390 us against 326 (the totals' own bytes are 10 of the difference); 4 x
-// 131072, 209 against 168; 64 ragged sequences of bf16, G = 4, 107 against 97.
+// 8, 396 us against 326 (the totals' own bytes are 10 of the difference); 4 x
+// 131072, 209 against 165; 64 ragged sequences of bf16, G = 4, 101 against 91.
+// Other groups, 128 x 4096 tokens of FP8 (plain 164-171): G = 1 182, 2 199, 3 and 4
+// 196, 5 and 6 233 (add_weights takes them two heads at a time), 7 and 8 211.
 // Dropping used scores from L2 took 24 us off the first and 11 off the second (HBM
 // writes of the decode kernel 220 -> 87 MB); the L2 hint on the stores another 9.
-// Tried and slower: weighing a unit page by page inside the consumers' loop (539 us)
-// or on the producer warp (544), for either becomes the pace of the stream.
+// Tried and slower, against 390 us: weighing a unit page by page inside the
+// consumers' loop (539) or on the producer warp (544), for either becomes the pace
+// of the stream.
 #include <mutex>
 
 #include "pa_decode_core.cuh"
@@ -45,7 +48,7 @@ int score_heads(int G) { return G == 1 ? 1 : (G + 1) & ~1; }
 // For every unit (sequence, kv head) of which the range holds a part: the
 // rows' (M, 1 / L) from all the unit's pieces, then the weights of the range's
 // tokens.  The output rows of a unit that spans n CTAs are merged by those n
-// CTAs, each a slice of the G x D values.  (Whole units are done.)  Of the 390 and
+// CTAs, each a slice of the G x D values.  (Whole units are done.)  Of the 396 and
 // 209 us above, 22 and 17 are this kernel: 8 of launch, dependent reads and merge, the
 // rest the scores, most of them still in L2.  Bulk copies through shared memory,
 // or one CTA per range end, were no faster.
