@@ -385,6 +385,39 @@ PA_API int pa_rope_and_cache(pa_pool* pool, int layer, const pa_rope* rope, cons
                              const int32_t* positions_dev, const int64_t* slot_mapping_dev, int T,
                              void* stream);
 
+/* Positions of several axes (time, height and width of images and video): pair i
+ * turns with the position on axis axis[i].
+ *   n_axes  1 .. PA_ROPE_MAX_AXES
+ *   axis    of every pair, all 64 entries below n_axes (those past rot_dim / 2
+ *           are not used) */
+#define PA_ROPE_MAX_AXES 4
+typedef struct pa_rope_axes {
+  int n_axes;
+  uint8_t axis[64];
+} pa_rope_axes;
+
+/* pa_rope_and_cache for models that normalise every head's query and key before
+ * the rotation, and for positions of several axes, in the same pass:
+ *   x' = x / sqrt(mean(x^2) + eps) * (weight_offset + w)
+ * over all head_dim dimensions of a head, those that do not turn among them;
+ * then the rotation, the rounding and the write of pa_rope_and_cache.
+ *   axes            NULL: one axis
+ *   q_weight, k_weight  device [head_dim], or [n_q_heads][head_dim] and
+ *                   [n_kv_heads][head_dim] with weights_per_head 1, of the
+ *                   pool's input dtype; NULL: that side is not normalised
+ *   eps             finite, >= 0 (with 0 a head of zeros gives NaN)
+ *   weight_offset   finite; 1 for models whose weights are kept as w - 1
+ *   positions_dev   device int32 [n_axes][T], axis by axis
+ * The squares are added up in fp32, and all is rounded once at the end.  Everything
+ * else is as for pa_rope_and_cache (q_out may be q; v is stored as it is). */
+PA_API int pa_norm_rope_and_cache(pa_pool* pool, int layer, const pa_rope* rope,
+                                  const pa_rope_axes* axes, const void* q_weight,
+                                  const void* k_weight, int weights_per_head, float eps,
+                                  float weight_offset, const void* q, size_t q_stride, void* q_out,
+                                  int n_q_heads, const void* k, size_t k_stride, const void* v,
+                                  size_t v_stride, const int32_t* positions_dev,
+                                  const int64_t* slot_mapping_dev, int T, void* stream);
+
 /* num_splits value that asks pa_decode for the balanced schedule (batches of
  * at most 4096 sequences, else PA_ERR_UNSUPPORTED): one CTA per resident slot
  * of the GPU, four per SM (the kernel's shared memory keeps a fifth off); the
@@ -586,6 +619,79 @@ PA_API int pa_evict_compact(pa_pool* pool, int layer, const int32_t* keep_dev, i
                             const int32_t* dst_tables_dev, int dst_max_blocks, int S,
                             const float* weights_in, size_t weights_in_stride, float* weights_out,
                             size_t weights_out_stride, void* stream);
+
+/* ---- speculative decoding ----
+ * (The pages have no counterpart.)  A step checks a tree of drafted tokens per
+ * sequence at once.  The tree's tokens (its nodes, in an order where a parent
+ * comes before its children) are written behind the sequence's history like any
+ * new tokens (pa_norm_rope_and_cache or pa_rope_and_cache, with the position history
+ * + depth, into the slots of history + node); pa_decode_tree attends, in every layer,
+ * each node to the history and to the nodes that it sees; and once the model's answer
+ * has settled which path holds, pa_tree_accept moves that path's tokens together. */
+#define PA_TREE_MAX_NODES 256
+
+/* Device scratch bytes pa_decode_tree needs, for any batch: the split units' partial
+ * states of the schedule on the current device. */
+PA_API int pa_decode_tree_workspace_bytes(const pa_pool* pool, int n_q_heads, int max_nodes,
+                                          size_t* bytes);
+
+/* Attention of every node of every sequence's tree over its paged history and the nodes
+ * that it sees, for layer `layer`: softmax(softmax_scale * q K^T) V over those tokens.
+ *   out, q         device [T][n_q_heads][head_dim]; sequence s's nodes are rows
+ *                  q_start[s] .. q_start[s+1] - 1; types as for pa_decode.  Rows behind
+ *                  q_start[S] are padding: neither read nor written
+ *   T              rows of q and out
+ *   q_start_dev    device int32 [S + 1], non-decreasing, at most T, q_start[0] >= 0
+ *   ctx_lens_dev   device int32 [S]: tokens of each sequence in the cache, its nodes included:
+ *                  node j is token ctx - nodes + j
+ *   max_nodes      1 .. PA_TREE_MAX_NODES: no sequence has more nodes
+ *   tree_mask_dev  device uint64 [T][ceil(max_nodes / 64)]: bit j % 64 of word j / 64 of a
+ *                  node's row is set if the node sees node j of its sequence (itself
+ *                  included, so usually its own bit is set too); bits from the
+ *                  sequence's nodes on are not used.  NULL: a chain, every node sees
+ *                  those before it and itself
+ *   workspace      device scratch of at least pa_decode_tree_workspace_bytes; calls that
+ *                  may overlap on the GPU need one each
+ * Grouped-query heads, block tables and softmax_scale are as for pa_decode.  Sequences
+ * without nodes are skipped; a node that sees nothing (no history, no bit) gets
+ * zeros.  What a node does not see does not touch its result, whatever the cache holds there
+ * (infinities and NaN among it).  The weights keep their precision in the product with
+ * V.  A sequence with more than max_nodes nodes, a decreasing or negative q_start or
+ * one above T, a context shorter than its nodes or longer than 16 * max_blocks_per_seq
+ * is skipped (its rows are not written), a table entry outside [0, num_blocks) gives
+ * an undefined result for its sequence; both set PA_ERR_BOUNDS in the device error
+ * word.  PA_ERR_UNSUPPORTED for tables of more than 2^27 - 256 blocks.  Equal inputs give
+ * equal bits on equal devices. */
+PA_API int pa_decode_tree(pa_pool* pool, int layer, void* out, int out_dtype, const void* q, int T,
+                          const int32_t* q_start_dev, const int32_t* block_tables_dev,
+                          int max_blocks_per_seq, const int32_t* ctx_lens_dev, int S, int n_q_heads,
+                          int max_nodes, const uint64_t* tree_mask_dev, float softmax_scale,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Keeps one path of each sequence's tree: the K and V of node paths[s][i], i <
+ * path_lens[s], move to node place i, right behind the history, in n_layers layers from
+ * `layer` on (the path is the same in all of them).
+ *   paths_dev      device int32 [S][max_path]: nodes in ascending order, each below the
+ *                  sequence's node count; entries from path_lens[s] on are not read
+ *   path_lens_dev  device int32 [S]: 0 .. max_path
+ *   q_start_dev, block_tables_dev, ctx_lens_dev  as for pa_decode_tree
+ *   new_lens_dev   device int32 [S], out: the context length after it,
+ *                  ctx - nodes + path_len; another buffer than ctx_lens_dev
+ * 16-bit and FP8 pools move the bytes.  In PA_FP8_E4M3_BLOCK pools a destination tile's
+ * scale grows to s = max(s_old, fl32(m / 448)), m the largest |fl32(decode(c) * s_src)| of
+ * the rows that come from other tiles; if it grew, the codes of the tile's 16 rows become
+ * E4M3(fl32(fl32(decode(c) * s_old) / s)); a moved row's codes are
+ * E4M3(fl32(fl32(decode(c) * s_src) / s)) (0 when s = 0).  Rows behind the path keep their
+ * contents up to that.  The blocks that hold nodes must not be shared with another sequence
+ * (pa_cow_prepare).  A path that is out of range or not ascending, a path_len outside
+ * [0, max_path] or above the nodes, or lengths that pa_decode_tree would skip
+ * set PA_ERR_BOUNDS; nothing of that sequence moves, and new_lens gets its context
+ * length unchanged.  A table entry outside [0, num_blocks) sets PA_ERR_BOUNDS, and the rows in
+ * that block are skipped. */
+PA_API int pa_tree_accept(pa_pool* pool, int layer, int n_layers, const int32_t* paths_dev,
+                          int max_path, const int32_t* path_lens_dev, const int32_t* q_start_dev,
+                          const int32_t* block_tables_dev, int max_blocks_per_seq,
+                          const int32_t* ctx_lens_dev, int S, int32_t* new_lens_dev, void* stream);
 
 /* Chunked prefill: causal attention of a chunk of new tokens per sequence over
  * its paged history ("Optimización de KV Cache ...", sections 5 and 6.3:

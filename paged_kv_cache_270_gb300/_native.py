@@ -37,6 +37,8 @@ PA_ROPE_SCALE_LINEAR = 1
 PA_ROPE_SCALE_NTK = 2
 PA_ROPE_SCALE_BANDS = 3
 PA_ROPE_SCALE_YARN = 4
+PA_ROPE_MAX_AXES = 4
+PA_TREE_MAX_NODES = 256
 
 PA_SPLITS_BALANCED = -1  # num_splits: the balanced decode schedule
 
@@ -70,6 +72,10 @@ class pa_rope_desc(ctypes.Structure):
 class pa_rope(ctypes.Structure):
     _fields_ = [("layout", ctypes.c_int), ("rot_dim", ctypes.c_int), ("gain", ctypes.c_float),
                 ("reserved", ctypes.c_int), ("step", ctypes.c_uint64 * 64)]
+
+
+class pa_rope_axes(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int), ("axis", ctypes.c_uint8 * 64)]
 
 
 _lock = threading.Lock()
@@ -108,6 +114,8 @@ _SIGS = [
     ("pa_rope_init", [ctypes.POINTER(pa_rope_desc), _P, ctypes.POINTER(pa_rope)]),
     ("pa_rope_and_cache", [_P, _I, ctypes.POINTER(pa_rope), _P, _SZ, _P, _I, _P, _SZ, _P, _SZ, _P,
                            _P, _I, _P]),
+    ("pa_norm_rope_and_cache", [_P, _I, ctypes.POINTER(pa_rope), ctypes.POINTER(pa_rope_axes), _P, _P, _I,
+                                ctypes.c_float, ctypes.c_float, _P, _SZ, _P, _I, _P, _SZ, _P, _SZ, _P, _P, _I, _P]),
     ("pa_decode_num_splits", [_P, _I, _I, _I, ctypes.POINTER(_I)]),
     ("pa_decode_workspace_bytes", [_P, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
     ("pa_decode", [_P, _I, _P, _I, _P, _P, _I, _P, _I, _I, ctypes.c_float, _I, _P, _SZ, _P]),
@@ -118,6 +126,9 @@ _SIGS = [
                            ctypes.c_float, _P, _SZ, _P]),
     ("pa_evict_select", [_P, _P, _SZ, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
     ("pa_evict_compact", [_P, _I, _P, _I, _I, _P, _P, _I, _P, _I, _I, _P, _SZ, _P, _SZ, _P]),
+    ("pa_decode_tree_workspace_bytes", [_P, _I, _I, ctypes.POINTER(_SZ)]),
+    ("pa_decode_tree", [_P, _I, _P, _I, _P, _I, _P, _P, _I, _P, _I, _I, _I, _P, ctypes.c_float, _P, _SZ, _P]),
+    ("pa_tree_accept", [_P, _I, _I, _P, _I, _P, _P, _P, _I, _P, _I, _P, _P]),
     ("pa_set_pipeline_wait_limit_ns", [ctypes.c_uint64]),
     ("pa_get_device_error", [_P, ctypes.POINTER(_I), _P]),
 ]
@@ -328,6 +339,16 @@ def pa_rope_and_cache(pool: int, layer: int, rope: pa_rope, q_ptr: int, q_stride
                                    stream))
 
 
+def pa_norm_rope_and_cache(pool: int, layer: int, rope: pa_rope, axes: pa_rope_axes | None, q_weight_ptr: int,
+                           k_weight_ptr: int, weights_per_head: int, eps: float, weight_offset: float,
+                           q_ptr: int, q_stride: int, q_out_ptr: int, n_q_heads: int, k_ptr: int, k_stride: int,
+                           v_ptr: int, v_stride: int, positions_ptr: int, slot_mapping_ptr: int, T: int,
+                           stream: int) -> None:
+    _check(lib().pa_norm_rope_and_cache(pool, layer, rope, axes, q_weight_ptr, k_weight_ptr, weights_per_head, eps,
+                                        weight_offset, q_ptr, q_stride, q_out_ptr, n_q_heads, k_ptr, k_stride,
+                                        v_ptr, v_stride, positions_ptr, slot_mapping_ptr, T, stream))
+
+
 def pa_decode_num_splits(pool: int, S: int, n_q_heads: int, max_blocks_per_seq: int) -> int:
     n = _I()
     _check(lib().pa_decode_num_splits(pool, S, n_q_heads, max_blocks_per_seq, ctypes.byref(n)))
@@ -386,6 +407,28 @@ def pa_evict_compact(pool: int, layer: int, keep_ptr: int, keep_heads: int, budg
                                   src_tables_ptr, src_max_blocks, dst_tables_ptr, dst_max_blocks, S,
                                   weights_in_ptr, weights_in_stride, weights_out_ptr,
                                   weights_out_stride, stream))
+
+
+def pa_decode_tree_workspace_bytes(pool: int, n_q_heads: int, max_nodes: int) -> int:
+    n = _SZ()
+    _check(lib().pa_decode_tree_workspace_bytes(pool, n_q_heads, max_nodes, ctypes.byref(n)))
+    return n.value
+
+
+def pa_decode_tree(pool: int, layer: int, out_ptr: int, out_dtype: int, q_ptr: int, T: int, q_start_ptr: int,
+                   tables_ptr: int, max_blocks_per_seq: int, ctx_lens_ptr: int, S: int, n_q_heads: int,
+                   max_nodes: int, mask_ptr: int, softmax_scale: float, workspace_ptr: int,
+                   workspace_bytes: int, stream: int) -> None:
+    _check(lib().pa_decode_tree(pool, layer, out_ptr, out_dtype, q_ptr, T, q_start_ptr, tables_ptr,
+                                max_blocks_per_seq, ctx_lens_ptr, S, n_q_heads, max_nodes, mask_ptr,
+                                softmax_scale, workspace_ptr, workspace_bytes, stream))
+
+
+def pa_tree_accept(pool: int, layer: int, n_layers: int, paths_ptr: int, max_path: int, path_lens_ptr: int,
+                   q_start_ptr: int, tables_ptr: int, max_blocks_per_seq: int, ctx_lens_ptr: int, S: int,
+                   new_lens_ptr: int, stream: int) -> None:
+    _check(lib().pa_tree_accept(pool, layer, n_layers, paths_ptr, max_path, path_lens_ptr, q_start_ptr, tables_ptr,
+                                max_blocks_per_seq, ctx_lens_ptr, S, new_lens_ptr, stream))
 
 
 def pa_prefill(pool: int, layer: int, out_ptr: int, out_dtype: int, q_ptr: int, q_start_ptr: int,

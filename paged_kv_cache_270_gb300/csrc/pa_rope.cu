@@ -60,6 +60,14 @@ struct RopeArgs {
   float* vsc;
   unsigned int* err;
   pa_rope rope;
+  // pa_norm_rope_and_cache (EXT builds): weights of the heads' norms (nullptr: that side
+  // keeps its scale), the elements from one head's weights to the next's (0: shared),
+  // and the axis whose positions a pair turns with (axis a's are pos[a T ..])
+  const uint16_t* qw;
+  const uint16_t* kw;
+  int q_wstride, k_wstride;
+  float eps, w_offset;
+  uint8_t axis[64];
 };
 
 // cos and sin of pair i at position p, times gain.
@@ -139,10 +147,59 @@ __device__ __forceinline__ void plain_unit(const UnitIn<LAY>& in, float (&y)[16]
   }
 }
 
-// The unit's 16 values after the rotation.  FULL: all of the row turns.
-template <bool BF, int D, int LAY, bool FULL>
-__device__ __forceinline__ void turn_unit(const UnitIn<LAY>& in, int u, int rot, const float2* cs, float (&y)[16]) {
+// What a head's norm multiplies a unit with: rs = 1 / sqrt(mean x^2 + eps) and the
+// weights of the unit's two vectors, in the pool's 16-bit type; w: the head's weights
+// (for the partners of ROPE_HALF_ODD).
+struct UnitNorm {
+  float rs, offset;
+  uint4 w0, w1;
+  const uint16_t* w;
+};
+
+// x rs (offset + w), of two neighbours.
+template <bool BF>
+__device__ __forceinline__ float2 scaled2(float x0, float x1, uint32_t w, const UnitNorm& n) {
+  const float2 v = unpack2<BF>(w);
+  return make_float2(x0 * n.rs * (n.offset + v.x), x1 * n.rs * (n.offset + v.y));
+}
+
+template <bool BF>
+__device__ __forceinline__ void scale_unit(const UnitNorm& n, float (&y)[16]) {
+  uint32_t w0[4], w1[4];
+  words(n.w0, w0);
+  words(n.w1, w1);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 a = scaled2<BF>(y[2 * j], y[2 * j + 1], w0[j], n), b = scaled2<BF>(y[8 + 2 * j], y[9 + 2 * j], w1[j], n);
+    y[2 * j] = a.x;
+    y[2 * j + 1] = a.y;
+    y[8 + 2 * j] = b.x;
+    y[9 + 2 * j] = b.y;
+  }
+}
+
+// 1 / sqrt(mean x^2 + eps) of the rows that the warp's lanes hold, D / 16 lanes a row
+// (every lane takes part).
+template <bool BF, int D, int LAY>
+__device__ __forceinline__ float row_rsqrt(const UnitIn<LAY>& in, float eps) {
+  float y[16];
   plain_unit<BF, LAY>(in, y);
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 16; ++j) s[j & 3] = fmaf(y[j], y[j], s[j & 3]);
+  float sum = (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll
+  for (int off = 1; off < D / 16; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  return rsqrtf(fmaf(sum, 1.f / D, eps));
+}
+
+// The unit's 16 values after the rotation.  FULL: all of the row turns.  norm: the
+// head's norm, which comes first (nullptr: none).
+template <bool BF, int D, int LAY, bool FULL>
+__device__ __forceinline__ void turn_unit(const UnitIn<LAY>& in, int u, int rot, const float2* cs, float (&y)[16],
+                                          const UnitNorm* norm = nullptr) {
+  plain_unit<BF, LAY>(in, y);
+  if (norm) scale_unit<BF>(*norm, y);
   if constexpr (LAY == ROPE_HALF) {
     if (!FULL && u >= (rot >> 4)) return;
 #pragma unroll
@@ -175,7 +232,8 @@ __device__ __forceinline__ void turn_unit(const UnitIn<LAY>& in, int u, int rot,
       const int e = 16 * u + j;
       if (e < rot) {
         const float2 t = cs[e < half ? e : e - half];
-        const float2 p2 = unpack2<BF>(in.partner[j]);
+        float2 p2 = unpack2<BF>(in.partner[j]);
+        if (norm) p2 = scaled2<BF>(p2.x, 0.f, norm->w[e < half ? e + half : e - half], *norm);
         y[j] = e < half ? y[j] * t.x - p2.x * t.y : y[j] * t.x + p2.x * t.y;
       }
     }
@@ -206,16 +264,30 @@ __device__ __forceinline__ uint2 codes8(const float* y, float s) {
 // put(h, v0, v1, in, y) stores the turned unit.  The rounds are counted per warp,
 // not per lane: in a last round with fewer than 32 items the lanes without one
 // take part in the warp's barrier all the same.
-template <bool BF, int D, int LAY, bool FULL, typename First, typename Put>
+// EXT: with the heads' norm where w, their weights, is given.
+template <bool BF, int D, int LAY, bool FULL, bool EXT, typename First, typename Put>
 __device__ __forceinline__ void turn_heads(const uint16_t* src, int items, int rot, int lt, int nt, const float2* cs,
-                                           First first, Put put) {
+                                           const uint16_t* w, int wstride, float eps, float w_offset, First first, Put put) {
   constexpr int UNITS = D / 16, IPT = LAY == ROPE_HALF_ODD ? 1 : 2;
   const int lane = lt & 31, warp0 = lt - lane;
+  UnitNorm norm = {};
+  auto weights = [&](int h) {  // (a lane's unit is the same in every round)
+    int v0, v1;
+    unit_vecs<LAY>(lane % UNITS, FULL ? D : rot, v0, v1);
+    norm.w = w + (long long)h * wstride;
+    norm.w0 = *reinterpret_cast<const uint4*>(norm.w + 8 * v0);
+    norm.w1 = *reinterpret_cast<const uint4*>(norm.w + 8 * v1);
+  };
+  if constexpr (EXT) {
+    norm.offset = w_offset;
+    if (w) weights(0);
+  }
   for (int base = warp0; base < items || base == warp0; base += nt * IPT) {
     UnitIn<LAY> in[IPT];
 #pragma unroll
     for (int j = 0; j < IPT; ++j) {
       const int i = base + lane + j * nt;
+      if constexpr (EXT) in[j] = {};
       if (i < items) load_unit<LAY, FULL>(src + (i / UNITS) * D, i % UNITS, FULL ? D : rot, in[j]);
     }
     if (base == warp0) first();
@@ -225,11 +297,14 @@ __device__ __forceinline__ void turn_heads(const uint16_t* src, int items, int r
 #pragma unroll
     for (int j = 0; j < IPT; ++j) {
       const int i = base + lane + j * nt;
+      const bool normed = EXT && w;
+      if (normed) norm.rs = row_rsqrt<BF, D, LAY>(in[j], eps);
       if (i < items) {
+        if (normed && wstride) weights(i / UNITS);
         int v0, v1;
         unit_vecs<LAY>(i % UNITS, FULL ? D : rot, v0, v1);
         float y[16];
-        turn_unit<BF, D, LAY, FULL>(in[j], i % UNITS, FULL ? D : rot, cs, y);
+        turn_unit<BF, D, LAY, FULL>(in[j], i % UNITS, FULL ? D : rot, cs, y, normed ? &norm : nullptr);
         put(i / UNITS, v0, v1, y);
       }
     }
@@ -238,16 +313,19 @@ __device__ __forceinline__ void turn_heads(const uint16_t* src, int items, int r
 
 // One token by `nt` threads (whole warps) of which this is `lt`: its query heads,
 // then (KV) its key and value heads into their slot.  cs: this warp's table.
-template <bool BF, bool FP8, bool KV, int D, int LAY, bool FULL>
+template <bool BF, bool FP8, bool KV, int D, int LAY, bool FULL, bool EXT>
 __device__ __forceinline__ void rope_token(const RopeArgs& a, int t, int lt, int nt, float2* cs) {
   constexpr int UNITS = D / 16;
   const int rot = FULL ? D : a.rope.rot_dim;
   uint16_t* q_out = a.q_out + (long long)t * a.Hq * D;
-  turn_heads<BF, D, LAY, FULL>(
-      a.q + t * a.qs, a.Hq * UNITS, rot, lt, nt, cs,
+  turn_heads<BF, D, LAY, FULL, EXT>(
+      a.q + t * a.qs, a.Hq * UNITS, rot, lt, nt, cs, a.qw, a.q_wstride, a.eps, a.w_offset,
       [&] {
-        const int p = a.pos[t];
-        for (int i = lt & 31; i < (rot >> 1); i += 32) cs[cs_index<D, LAY>(i)] = turn(a.rope, i, p);
+        int p = a.pos[t];
+        for (int i = lt & 31; i < (rot >> 1); i += 32) {
+          if constexpr (EXT) p = a.pos[(long long)a.axis[i] * a.T + t];
+          cs[cs_index<D, LAY>(i)] = turn(a.rope, i, p);
+        }
       },
       [&](int h, int v0, int v1, const float* y) {
         *reinterpret_cast<uint4*>(q_out + h * D + 8 * v0) = pack8<BF>(y);
@@ -262,8 +340,8 @@ __device__ __forceinline__ void rope_token(const RopeArgs& a, int t, int lt, int
     constexpr int EB = FP8 ? 1 : 2;
     uint8_t* kp = a.kpool + EB * e0;
     uint8_t* vp = a.vpool + EB * e0;
-    turn_heads<BF, D, LAY, FULL>(
-        a.k + t * a.ks, a.Hkv * UNITS, rot, lt, nt, cs, [] {},
+    turn_heads<BF, D, LAY, FULL, EXT>(
+        a.k + t * a.ks, a.Hkv * UNITS, rot, lt, nt, cs, a.kw, a.k_wstride, a.eps, a.w_offset, [] {},
         [&](int h, int v0, int v1, const float* y) {
           uint8_t* dst = kp + (long long)h * (16 * D * EB);
           if constexpr (FP8) {
@@ -297,15 +375,15 @@ __device__ __forceinline__ void rope_token(const RopeArgs& a, int t, int lt, int
   }
 }
 
-// FULL: every dimension turns (ROPE_HALF and ROPE_INTER).
-template <bool BF, bool FP8, int D, int LAY, bool FULL>
+// FULL: every dimension turns (ROPE_HALF and ROPE_INTER).  EXT: pa_norm_rope_and_cache.
+template <bool BF, bool FP8, int D, int LAY, bool FULL, bool EXT>
 __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_cache_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ __align__(16) float2 cs[kRopeWarps][D / 2];
   grid_dependents_launch();  // a decode behind this kernel waits for its writes itself
   const int warp = threadIdx.x >> 5, wpt = a.warps_per_token, tok = warp / wpt;
   const int t = blockIdx.x * (kRopeWarps / wpt) + tok;
   if (t < a.T)
-    rope_token<BF, FP8, true, D, LAY, FULL>(a, t, threadIdx.x - tok * wpt * 32, wpt * 32, cs[warp]);
+    rope_token<BF, FP8, true, D, LAY, FULL, EXT>(a, t, threadIdx.x - tok * wpt * 32, wpt * 32, cs[warp]);
 }
 
 // Block-scaled pools.  For each token come a.parts CTAs, K and V of eight heads
@@ -317,7 +395,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_cache_kernel(const __
 // (four CTAs on an SM in the place of two).  2048 tokens of 64 / 8 heads (80 MB):
 // 25 us; 29 with the queries first, 41 with the values kept in fp32.  Bound by
 // the runs' latency: slots, rows, the table, the maximum, the division.
-template <int D, int LAY>
+template <int D, int LAY, bool EXT>
 __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_cache_block_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ __align__(16) float2 cs[16][D / 2];
   grid_dependents_launch();
@@ -327,7 +405,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_cache_block_kernel(co
     const int wpt = a.warps_per_token, tok = warp / wpt;
     const int t = (r - kv_ctas) * (kRopeWarps / wpt) + tok;
     if (t < a.T)
-      rope_token<true, true, false, D, LAY, false>(a, t, threadIdx.x - tok * wpt * 32, wpt * 32, cs[warp]);
+      rope_token<true, true, false, D, LAY, false, EXT>(a, t, threadIdx.x - tok * wpt * 32, wpt * 32, cs[warp]);
     return;
   }
   const int t = r / a.parts, part = r % a.parts;
@@ -370,11 +448,28 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_cache_block_kernel(co
   if (!is_v) {  // the run's tables, while the rows are in flight
     for (int i = threadIdx.x; i < n * (rot >> 1); i += blockDim.x) {
       const int tk = i / (rot >> 1), p = i - tk * (rot >> 1);
-      cs[tk][cs_index<D, LAY>(p)] = turn(a.rope, p, a.pos[t + tk]);
+      const long long at = EXT ? (long long)a.axis[p] * a.T : 0;
+      cs[tk][cs_index<D, LAY>(p)] = turn(a.rope, p, a.pos[at + t + tk]);
     }
     __syncthreads();
   }
   if (!live) return;
+  const bool normed = EXT && !is_v && a.kw;
+  UnitNorm norm = {};
+  float rs[ITERS];
+  if (normed) {
+    norm.offset = a.w_offset;
+    norm.w = a.kw + (long long)h * a.k_wstride;
+    norm.w0 = *reinterpret_cast<const uint4*>(norm.w + 8 * v0);
+    norm.w1 = *reinterpret_cast<const uint4*>(norm.w + 8 * v1);
+#pragma unroll
+    for (int i = 0; i < ITERS; ++i) {
+      UnitIn<LAY> in = {};
+      in.x0 = x[i][0];
+      in.x1 = x[i][1];
+      rs[i] = row_rsqrt<true, D, LAY>(in, a.eps);
+    }
+  }
   auto values = [&](int i, float (&y)[16]) {
     UnitIn<LAY> in;
     in.x0 = x[i][0];
@@ -383,7 +478,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_cache_block_kernel(co
       plain_unit<true, LAY>(in, y);
     } else {
       if constexpr (LAY == ROPE_HALF_ODD) load_unit<LAY, false>(row_at(i), u, rot, in);
-      turn_unit<true, D, LAY, false>(in, u, rot, cs[i * ROWS + r0], y);
+      if (normed) norm.rs = rs[i];
+      turn_unit<true, D, LAY, false>(in, u, rot, cs[i * ROWS + r0], y, normed ? &norm : nullptr);
     }
   };
   uint32_t mb = 0;  // largest |y|: without the sign bit, magnitudes order like their bits (a NaN above all)
@@ -432,28 +528,119 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_cache_block_kernel(co
 // ---------------------------------------------------------------- host side
 typedef void (*RopeKernel)(RopeArgs);
 
-template <bool BF, bool FP8, int D>
+template <bool BF, bool FP8, int D, bool EXT>
 RopeKernel pick_lay(int lay, bool full) {
-  if (lay == ROPE_HALF_ODD) return rope_cache_kernel<BF, FP8, D, ROPE_HALF_ODD, false>;
+  if (lay == ROPE_HALF_ODD) return rope_cache_kernel<BF, FP8, D, ROPE_HALF_ODD, false, EXT>;
   if (lay == ROPE_HALF)
-    return full ? rope_cache_kernel<BF, FP8, D, ROPE_HALF, true> : rope_cache_kernel<BF, FP8, D, ROPE_HALF, false>;
-  return full ? rope_cache_kernel<BF, FP8, D, ROPE_INTER, true> : rope_cache_kernel<BF, FP8, D, ROPE_INTER, false>;
+    return full ? rope_cache_kernel<BF, FP8, D, ROPE_HALF, true, EXT>
+                : rope_cache_kernel<BF, FP8, D, ROPE_HALF, false, EXT>;
+  return full ? rope_cache_kernel<BF, FP8, D, ROPE_INTER, true, EXT>
+              : rope_cache_kernel<BF, FP8, D, ROPE_INTER, false, EXT>;
 }
 
-template <int D>
+template <int D, bool EXT>
 RopeKernel pick_kernel(int kv_dtype, int lay, bool full) {
   if (kv_dtype == PA_FP8_E4M3_BLOCK)
-    return lay == ROPE_HALF    ? rope_cache_block_kernel<D, ROPE_HALF>
-           : lay == ROPE_INTER ? rope_cache_block_kernel<D, ROPE_INTER>
-                               : rope_cache_block_kernel<D, ROPE_HALF_ODD>;
-  if (kv_dtype == PA_FP8_E4M3) return pick_lay<true, true, D>(lay, full);
-  return kv_dtype == PA_BF16 ? pick_lay<true, false, D>(lay, full) : pick_lay<false, false, D>(lay, full);
+    return lay == ROPE_HALF    ? rope_cache_block_kernel<D, ROPE_HALF, EXT>
+           : lay == ROPE_INTER ? rope_cache_block_kernel<D, ROPE_INTER, EXT>
+                               : rope_cache_block_kernel<D, ROPE_HALF_ODD, EXT>;
+  if (kv_dtype == PA_FP8_E4M3) return pick_lay<true, true, D, EXT>(lay, full);
+  return kv_dtype == PA_BF16 ? pick_lay<true, false, D, EXT>(lay, full) : pick_lay<false, false, D, EXT>(lay, full);
+}
+
+template <bool EXT>
+RopeKernel pick_kernel(int head_dim, int kv_dtype, int lay, bool full) {
+  return head_dim == 64 ? pick_kernel<64, EXT>(kv_dtype, lay, full) : pick_kernel<128, EXT>(kv_dtype, lay, full);
 }
 
 int check_stride(const char* name, size_t stride, int heads, int head_dim) {
   if (stride < (size_t)heads * head_dim || stride % 8 != 0 || stride >= (size_t)1 << 40)
     return fail(PA_ERR_INVALID, "%s_stride %zu must be a multiple of 8, at least %zu and below 2^40", name, stride,
                 (size_t)heads * head_dim);
+  return PA_OK;
+}
+
+// What pa_norm_rope_and_cache adds to a call.
+struct RopeExt {
+  const void* q_weight;
+  const void* k_weight;
+  int weights_per_head;
+  float eps, offset;
+  const pa_rope_axes* axes;
+};
+
+// Both entry points.  ext: pa_norm_rope_and_cache's norms and axes, checked; nullptr for pa_rope_and_cache.
+int rope_call(pa_pool* pool, int layer, const pa_rope* rope, const RopeExt* ext, const void* q, size_t q_stride,
+              void* q_out, int n_q_heads, const void* k, size_t k_stride, const void* v, size_t v_stride,
+              const int32_t* positions_dev, const int64_t* slot_mapping_dev, int T, void* stream) {
+  int st = check_pool_layer(pool, layer);
+  if (st) return st;
+  const pa_pool_desc& d = pool->desc;
+  if (!rope) return fail(PA_ERR_INVALID, "null rope");
+  if ((rope->layout != PA_ROPE_HALF && rope->layout != PA_ROPE_INTERLEAVED) || rope->rot_dim < 2 ||
+      rope->rot_dim % 2 != 0 || !std::isfinite(rope->gain))
+    return fail(PA_ERR_INVALID, "the rope was not filled by pa_rope_init");
+  if (rope->rot_dim > d.head_dim)
+    return fail(PA_ERR_INVALID, "rot_dim %d above the pool's head_dim %d", rope->rot_dim, d.head_dim);
+  if (T < 0) return fail(PA_ERR_INVALID, "T must be >= 0");
+  if (n_q_heads < 1) return fail(PA_ERR_INVALID, "n_q_heads must be >= 1");
+  // the items of a token are counted in 32 bits
+  if ((long long)n_q_heads + 2ll * d.n_kv_heads > (1 << 20))
+    return fail(PA_ERR_UNSUPPORTED, "at most 2^20 query, key and value heads together");
+  if ((st = check_stride("q", q_stride, n_q_heads, d.head_dim))) return st;
+  if ((st = check_stride("k", k_stride, d.n_kv_heads, d.head_dim))) return st;
+  if ((st = check_stride("v", v_stride, d.n_kv_heads, d.head_dim))) return st;
+  if (T == 0) return PA_OK;
+  if (!q || !q_out || !k || !v || !positions_dev || !slot_mapping_dev) return fail(PA_ERR_INVALID, "null argument");
+  if (((uintptr_t)q | (uintptr_t)q_out | (uintptr_t)k | (uintptr_t)v) & 15u)
+    return fail(PA_ERR_INVALID, "q, q_out, k and v must be 16-byte aligned");
+  if (q_out == q && q_stride != (size_t)n_q_heads * d.head_dim)
+    return fail(PA_ERR_INVALID, "q_out may be q only when q is contiguous");
+  unsigned int* err = device_error_word();
+  if (!err) return PA_ERR_CUDA;
+  RopeArgs a = {};
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.qs = (long long)q_stride;
+  a.ks = (long long)k_stride;
+  a.vs = (long long)v_stride;
+  a.pos = positions_dev;
+  a.slots = slot_mapping_dev;
+  a.T = T;
+  a.Hq = n_q_heads;
+  a.Hkv = d.n_kv_heads;
+  a.num_slots = (long long)d.num_blocks * 16;
+  a.kpool = pool->k + (size_t)layer * pool->layer_bytes;
+  a.vpool = pool->v + (size_t)layer * pool->layer_bytes;
+  a.k_scale = d.k_scale;
+  a.v_scale = d.v_scale;
+  a.ksc = pool->block_scaled ? layer_scales(pool, pool->k, layer) : nullptr;
+  a.vsc = pool->block_scaled ? layer_scales(pool, pool->v, layer) : nullptr;
+  a.err = err;
+  a.rope = *rope;
+  const int lay = rope->layout == PA_ROPE_INTERLEAVED ? ROPE_INTER : rope->rot_dim % 16 == 0 ? ROPE_HALF : ROPE_HALF_ODD;
+  const bool full = rope->rot_dim == d.head_dim;
+  if (ext) {
+    a.qw = static_cast<const uint16_t*>(ext->q_weight);
+    a.kw = static_cast<const uint16_t*>(ext->k_weight);
+    a.q_wstride = a.k_wstride = ext->weights_per_head ? d.head_dim : 0;
+    a.eps = ext->eps;
+    a.w_offset = ext->offset;
+    if (ext->axes) std::copy(ext->axes->axis, ext->axes->axis + 64, a.axis);
+  }
+  const RopeKernel kern =
+      ext ? pick_kernel<true>(d.head_dim, d.kv_dtype, lay, full) : pick_kernel<false>(d.head_dim, d.kv_dtype, lay, full);
+  a.warps_per_token = 1;
+  while (a.warps_per_token < kRopeWarps && (long long)T * a.warps_per_token < kRopeFewWarps) a.warps_per_token *= 2;
+  const unsigned q_ctas = (unsigned)((T - 1) / (kRopeWarps / a.warps_per_token) + 1);
+  a.parts = 2u * (unsigned)((d.n_kv_heads + kRopeWarps - 1) / kRopeWarps);
+  const long long ctas = q_ctas + (pool->block_scaled ? (long long)T * a.parts : 0);
+  if (ctas > 0x7FFFFFFF) return fail(PA_ERR_UNSUPPORTED, "too many tokens and kv heads for one call");
+  kern<<<(unsigned)ctas, kRopeWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(PA_ERR_CUDA, "rope_and_cache launch: %s", cudaGetErrorString(e));
   return PA_OK;
 }
 
@@ -523,67 +710,31 @@ int pa_rope_and_cache(pa_pool* pool, int layer, const pa_rope* rope, const void*
                       int n_q_heads, const void* k, size_t k_stride, const void* v, size_t v_stride,
                       const int32_t* positions_dev, const int64_t* slot_mapping_dev, int T, void* stream) {
   pa::TraceRange trace_("pa_rope_and_cache");
-  int st = check_pool_layer(pool, layer);
-  if (st) return st;
-  const pa_pool_desc& d = pool->desc;
-  if (!rope) return fail(PA_ERR_INVALID, "null rope");
-  if ((rope->layout != PA_ROPE_HALF && rope->layout != PA_ROPE_INTERLEAVED) || rope->rot_dim < 2 ||
-      rope->rot_dim % 2 != 0 || !std::isfinite(rope->gain))
-    return fail(PA_ERR_INVALID, "the rope was not filled by pa_rope_init");
-  if (rope->rot_dim > d.head_dim)
-    return fail(PA_ERR_INVALID, "rot_dim %d above the pool's head_dim %d", rope->rot_dim, d.head_dim);
-  if (T < 0) return fail(PA_ERR_INVALID, "T must be >= 0");
-  if (n_q_heads < 1) return fail(PA_ERR_INVALID, "n_q_heads must be >= 1");
-  // the items of a token are counted in 32 bits
-  if ((long long)n_q_heads + 2ll * d.n_kv_heads > (1 << 20))
-    return fail(PA_ERR_UNSUPPORTED, "at most 2^20 query, key and value heads together");
-  if ((st = check_stride("q", q_stride, n_q_heads, d.head_dim))) return st;
-  if ((st = check_stride("k", k_stride, d.n_kv_heads, d.head_dim))) return st;
-  if ((st = check_stride("v", v_stride, d.n_kv_heads, d.head_dim))) return st;
-  if (T == 0) return PA_OK;
-  if (!q || !q_out || !k || !v || !positions_dev || !slot_mapping_dev) return fail(PA_ERR_INVALID, "null argument");
-  if (((uintptr_t)q | (uintptr_t)q_out | (uintptr_t)k | (uintptr_t)v) & 15u)
-    return fail(PA_ERR_INVALID, "q, q_out, k and v must be 16-byte aligned");
-  if (q_out == q && q_stride != (size_t)n_q_heads * d.head_dim)
-    return fail(PA_ERR_INVALID, "q_out may be q only when q is contiguous");
-  unsigned int* err = device_error_word();
-  if (!err) return PA_ERR_CUDA;
-  RopeArgs a;
-  a.q = static_cast<const uint16_t*>(q);
-  a.q_out = static_cast<uint16_t*>(q_out);
-  a.k = static_cast<const uint16_t*>(k);
-  a.v = static_cast<const uint16_t*>(v);
-  a.qs = (long long)q_stride;
-  a.ks = (long long)k_stride;
-  a.vs = (long long)v_stride;
-  a.pos = positions_dev;
-  a.slots = slot_mapping_dev;
-  a.T = T;
-  a.Hq = n_q_heads;
-  a.Hkv = d.n_kv_heads;
-  a.num_slots = (long long)d.num_blocks * 16;
-  a.kpool = pool->k + (size_t)layer * pool->layer_bytes;
-  a.vpool = pool->v + (size_t)layer * pool->layer_bytes;
-  a.k_scale = d.k_scale;
-  a.v_scale = d.v_scale;
-  a.ksc = pool->block_scaled ? layer_scales(pool, pool->k, layer) : nullptr;
-  a.vsc = pool->block_scaled ? layer_scales(pool, pool->v, layer) : nullptr;
-  a.err = err;
-  a.rope = *rope;
-  const int lay = rope->layout == PA_ROPE_INTERLEAVED ? ROPE_INTER : rope->rot_dim % 16 == 0 ? ROPE_HALF : ROPE_HALF_ODD;
-  const bool full = rope->rot_dim == d.head_dim;
-  const RopeKernel kern =
-      d.head_dim == 64 ? pick_kernel<64>(d.kv_dtype, lay, full) : pick_kernel<128>(d.kv_dtype, lay, full);
-  a.warps_per_token = 1;
-  while (a.warps_per_token < kRopeWarps && (long long)T * a.warps_per_token < kRopeFewWarps) a.warps_per_token *= 2;
-  const unsigned q_ctas = (unsigned)((T - 1) / (kRopeWarps / a.warps_per_token) + 1);
-  a.parts = 2u * (unsigned)((d.n_kv_heads + kRopeWarps - 1) / kRopeWarps);
-  const long long ctas = q_ctas + (pool->block_scaled ? (long long)T * a.parts : 0);
-  if (ctas > 0x7FFFFFFF) return fail(PA_ERR_UNSUPPORTED, "too many tokens and kv heads for one call");
-  kern<<<(unsigned)ctas, kRopeWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(PA_ERR_CUDA, "rope_and_cache launch: %s", cudaGetErrorString(e));
-  return PA_OK;
+  return rope_call(pool, layer, rope, nullptr, q, q_stride, q_out, n_q_heads, k, k_stride, v, v_stride, positions_dev,
+                   slot_mapping_dev, T, stream);
+}
+
+int pa_norm_rope_and_cache(pa_pool* pool, int layer, const pa_rope* rope, const pa_rope_axes* axes, const void* q_weight,
+                           const void* k_weight, int weights_per_head, float eps, float weight_offset, const void* q,
+                           size_t q_stride, void* q_out, int n_q_heads, const void* k, size_t k_stride, const void* v,
+                           size_t v_stride, const int32_t* positions_dev, const int64_t* slot_mapping_dev, int T,
+                           void* stream) {
+  pa::TraceRange trace_("pa_norm_rope_and_cache");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(PA_ERR_INVALID, "eps must be finite and at least 0");
+  if (!std::isfinite(weight_offset)) return fail(PA_ERR_INVALID, "weight_offset must be finite");
+  if (weights_per_head != 0 && weights_per_head != 1) return fail(PA_ERR_INVALID, "weights_per_head must be 0 or 1");
+  if (((uintptr_t)q_weight | (uintptr_t)k_weight) & 15u)
+    return fail(PA_ERR_INVALID, "the weights must be 16-byte aligned");
+  if (axes) {
+    if (axes->n_axes < 1 || axes->n_axes > PA_ROPE_MAX_AXES)
+      return fail(PA_ERR_INVALID, "n_axes must be 1 to %d (got %d)", PA_ROPE_MAX_AXES, axes->n_axes);
+    for (int i = 0; i < 64; ++i)
+      if (axes->axis[i] >= axes->n_axes)
+        return fail(PA_ERR_INVALID, "pair %d turns with axis %d of %d", i, (int)axes->axis[i], axes->n_axes);
+  }
+  const RopeExt ext = {q_weight, k_weight, weights_per_head, eps, weight_offset, axes};
+  return rope_call(pool, layer, rope, &ext, q, q_stride, q_out, n_q_heads, k, k_stride, v, v_stride, positions_dev,
+                   slot_mapping_dev, T, stream);
 }
 
 }  // extern "C"

@@ -67,6 +67,26 @@ def make_rope(rot_dim: int, layout: str = "half", theta: float = 10000.0, scalin
                                          factor, original_len, low, high, gain), divisors)
 
 
+def make_rope_axes(sections, order: str = "sections") -> N.pa_rope_axes:
+    """Which axis each rotary pair turns with, for ``KVPool.norm_rope_and_cache``: sections[a]
+    pairs turn with axis a's positions, rot_dim / 2 in all.  `order`: "sections" (the first
+    sections[0] pairs with axis 0, and so on), or "turns" (pair i with axis i mod n for the
+    first n sections[a] pairs of each axis a > 0; axis 0 has the rest)."""
+    sections = [int(n) for n in sections]
+    n, pairs = len(sections), sum(sections)
+    if not 1 <= n <= N.PA_ROPE_MAX_AXES or min(sections) < 0 or not 1 <= pairs <= 64:
+        raise ValueError(f"need 1 to {N.PA_ROPE_MAX_AXES} sections of 1 to 64 pairs together")
+    if order == "sections":
+        of = [a for a in range(n) for _ in range(sections[a])]
+    elif order == "turns":
+        of = [i % n if i < n * sections[i % n] else 0 for i in range(pairs)]
+        if [of.count(a) for a in range(n)] != sections:
+            raise ValueError(f"sections {sections} cannot take turns")
+    else:
+        raise ValueError("order must be 'sections' or 'turns'")
+    return N.pa_rope_axes(n, (N.ctypes.c_uint8 * 64)(*of))
+
+
 def _token_rows(t: torch.Tensor, name: str, dtype, device) -> int:
     """The token stride, in elements, of a [T, heads, head_dim] tensor whose tokens may lie
     apart (a slice of a fused projection) but are contiguous in themselves."""
@@ -197,12 +217,8 @@ class KVPool:
         N.pa_reshape_and_cache(self.handle, layer, k.data_ptr(), v.data_ptr(),
                                slot_mapping.data_ptr(), T, _stream_handle(stream))
 
-    def rope_and_cache(self, rope: N.pa_rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
-                       positions: torch.Tensor, slot_mapping: torch.Tensor,
-                       q_out: torch.Tensor | None = None, layer: int = 0, stream=None) -> torch.Tensor:
-        """Rotate q [T, Hq, D] and k [T, Hkv, D] at `positions` (int32) and write k and v
-        into their slots; returns the rotated q (`q_out`, which may be q itself when it is
-        contiguous).  q, k and v may be slices of one fused projection."""
+    def _rope_args(self, q, k, v, positions, slot_mapping, q_out, n_axes, stream):
+        """Checks what the rotary writes share; returns q_out and the C call's last arguments."""
         qs = _token_rows(q, "q", self.in_dtype, self.device)
         ks = _token_rows(k, "k", self.in_dtype, self.device)
         vs = _token_rows(v, "v", self.in_dtype, self.device)
@@ -211,17 +227,53 @@ class KVPool:
         kv = (T, self.n_kv_heads, self.head_dim)
         if D != self.head_dim or k.shape != kv or v.shape != kv:
             raise ValueError("q must be [T, n_q_heads, head_dim], k and v [T, n_kv_heads, head_dim]")
-        if positions.numel() != T or slot_mapping.numel() != T:
-            raise ValueError("positions and slot_mapping must hold one entry per token")
+        if positions.numel() != n_axes * T or slot_mapping.numel() != T:
+            raise ValueError("positions and slot_mapping must hold one entry per token (positions: and axis)")
         if q_out is None:
             q_out = self._new((T, Hq, D), q.dtype, stream)
         else:
             _need(q_out, "q_out", self.in_dtype, self.device)
             if q_out.shape != q.shape:
                 raise ValueError("q_out must have q's shape")
-        self._launch(N.pa_rope_and_cache,
-                     (self.handle, layer, rope, q.data_ptr(), qs, q_out.data_ptr(), Hq, k.data_ptr(), ks,
-                      v.data_ptr(), vs, positions.data_ptr(), slot_mapping.data_ptr(), T), stream)
+        return q_out, (q.data_ptr(), qs, q_out.data_ptr(), Hq, k.data_ptr(), ks, v.data_ptr(), vs,
+                       positions.data_ptr(), slot_mapping.data_ptr(), T)
+
+    def rope_and_cache(self, rope: N.pa_rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                       positions: torch.Tensor, slot_mapping: torch.Tensor,
+                       q_out: torch.Tensor | None = None, layer: int = 0, stream=None) -> torch.Tensor:
+        """Rotate q [T, Hq, D] and k [T, Hkv, D] at `positions` (int32) and write k and v
+        into their slots; returns the rotated q (`q_out`, which may be q itself when it is
+        contiguous).  q, k and v may be slices of one fused projection."""
+        q_out, args = self._rope_args(q, k, v, positions, slot_mapping, q_out, 1, stream)
+        self._launch(N.pa_rope_and_cache, (self.handle, layer, rope, *args), stream)
+        return q_out
+
+    def norm_rope_and_cache(self, rope: N.pa_rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                            positions: torch.Tensor, slot_mapping: torch.Tensor,
+                            q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                            eps: float = 1e-6, weight_offset: float = 0.0,
+                            axes: N.pa_rope_axes | None = None, q_out: torch.Tensor | None = None,
+                            layer: int = 0, stream=None) -> torch.Tensor:
+        """``rope_and_cache`` that first divides every head of q and of k by its root mean square
+        and multiplies it with `weight_offset` + its weights ([D], or [heads, D] for both; None: that
+        side is not normalised).  With `axes` (``make_rope_axes``) positions is [n_axes, T]."""
+        n_axes = axes.n_axes if axes is not None else 1
+        q_out, args = self._rope_args(q, k, v, positions, slot_mapping, q_out, n_axes, stream)
+        per_head = False
+        for w, name, heads in ((q_weight, "q_weight", q.shape[1]), (k_weight, "k_weight", self.n_kv_heads)):
+            if w is None:
+                continue
+            _need(w, name, self.in_dtype, self.device)
+            if w.shape not in ((self.head_dim,), (heads, self.head_dim)):
+                raise ValueError(f"{name} must be [head_dim] or [heads, head_dim]")
+            per_head = w.dim() == 2
+        if q_weight is not None and k_weight is not None and q_weight.dim() != k_weight.dim():
+            raise ValueError("q_weight and k_weight must both be [head_dim] or both [heads, head_dim]")
+        if n_axes > 1 and (positions.dim() != 2 or positions.shape[0] != n_axes):
+            raise ValueError("positions must be [n_axes, T]")
+        self._launch(N.pa_norm_rope_and_cache,
+                     (self.handle, layer, rope, axes, q_weight.data_ptr() if q_weight is not None else 0,
+                      k_weight.data_ptr() if k_weight is not None else 0, per_head, eps, weight_offset, *args), stream)
         return q_out
 
     def copy_blocks(self, pairs: torch.Tensor, layer: int = 0, stream=None) -> None:
@@ -391,6 +443,82 @@ class KVPool:
                       block_tables.data_ptr(), block_tables.shape[1], dst_tables.data_ptr(),
                       dst_tables.shape[1], S, w_in, in_stride, w_out, out_stride), stream)
         return weights_out
+
+    def tree_workspace_bytes(self, n_q_heads: int, max_nodes: int) -> int:
+        with torch.cuda.device(self.device):
+            return N.pa_decode_tree_workspace_bytes(self.handle, n_q_heads, max_nodes)
+
+    def decode_tree(self, q: torch.Tensor, q_start: torch.Tensor, block_tables: torch.Tensor,
+                    ctx_lens: torch.Tensor, max_nodes: int, mask: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                    softmax_scale: float | None = None, layer: int = 0,
+                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Attention of a tree of drafted tokens per sequence: rows q_start[s] .. q_start[s+1]-1 of
+        q [T, Hq, D] are sequence s's nodes, the last ones of its ctx_lens[s] cached tokens.  Each
+        attends to the history in front of them and to the nodes whose bits are set in its row of
+        `mask`, int64 [T, ceil(max_nodes / 64)] (None: those before it and itself).  Rows of q
+        and out behind q_start[S] are neither read nor written."""
+        dev = self.device
+        _all_need(dev, (q, "q", self.in_dtype), (q_start, "q_start", torch.int32),
+                  (block_tables, "block_tables", torch.int32), (ctx_lens, "ctx_lens", torch.int32))
+        if q.dim() != 3 or q.shape[2] != self.head_dim:
+            raise ValueError("q must be [T, n_q_heads, head_dim]")
+        T, Hq, D = q.shape
+        S = ctx_lens.numel()
+        if block_tables.dim() != 2 or block_tables.shape[0] != S or q_start.numel() != S + 1:
+            raise ValueError("block_tables must be [S, max_blocks], ctx_lens [S] and q_start [S + 1]")
+        if mask is not None:
+            _need(mask, "mask", torch.int64, dev)
+            if mask.shape != (T, -(-max_nodes // 64)):
+                raise ValueError("mask must be [T, ceil(max_nodes / 64)]")
+        if out is None:
+            out = self._new((T, Hq, D), out_dtype or q.dtype, stream)
+        else:
+            _need(out, "out", None, dev)
+            if out.shape != q.shape:
+                raise ValueError("out must have q's shape")
+        if out.dtype not in _OUT_CODES:
+            raise TypeError(f"out cannot be {out.dtype}")
+        if softmax_scale is None:
+            softmax_scale = 1.0 / math.sqrt(D)
+        if workspace is None:
+            workspace = self._new(self.tree_workspace_bytes(Hq, max_nodes), torch.uint8, stream)
+        else:
+            _need(workspace, "workspace", None, dev)
+        self._launch(N.pa_decode_tree,
+                     (self.handle, layer, out.data_ptr(), _OUT_CODES[out.dtype], q.data_ptr(), T, q_start.data_ptr(),
+                      block_tables.data_ptr(), block_tables.shape[1], ctx_lens.data_ptr(), S, Hq, max_nodes,
+                      mask.data_ptr() if mask is not None else 0, softmax_scale, workspace.data_ptr(),
+                      workspace.numel() * workspace.element_size()), stream)
+        return out
+
+    def tree_accept(self, paths: torch.Tensor, path_lens: torch.Tensor, q_start: torch.Tensor,
+                    block_tables: torch.Tensor, ctx_lens: torch.Tensor, new_lens: torch.Tensor | None = None,
+                    layer: int = 0, n_layers: int | None = None, stream=None) -> torch.Tensor:
+        """Move the K and V of the accepted nodes paths[s, :path_lens[s]] (ascending) of each sequence's
+        tree right behind its history, in `n_layers` layers from `layer` on (None: all that follow).
+        Returns the new context lengths (`new_lens`, which must not be ctx_lens itself)."""
+        _all_need(self.device, (paths, "paths", torch.int32), (path_lens, "path_lens", torch.int32),
+                  (q_start, "q_start", torch.int32), (block_tables, "block_tables", torch.int32),
+                  (ctx_lens, "ctx_lens", torch.int32))
+        S = ctx_lens.numel()
+        if paths.dim() != 2 or paths.shape[0] != S or path_lens.numel() != S or q_start.numel() != S + 1:
+            raise ValueError("paths must be [S, max_path], path_lens and ctx_lens [S], q_start [S + 1]")
+        if block_tables.dim() != 2 or block_tables.shape[0] != S:
+            raise ValueError("block_tables must be [S, max_blocks]")
+        if new_lens is None:
+            new_lens = self._new(S, torch.int32, stream)
+        else:
+            _need(new_lens, "new_lens", torch.int32, self.device)
+            if new_lens.numel() != S:
+                raise ValueError("new_lens must be [S]")
+        if n_layers is None:
+            n_layers = self.n_layers - layer
+        self._launch(N.pa_tree_accept,
+                     (self.handle, layer, n_layers, paths.data_ptr(), paths.shape[1], path_lens.data_ptr(),
+                      q_start.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], ctx_lens.data_ptr(), S,
+                      new_lens.data_ptr()), stream)
+        return new_lens
 
     def prefill(self, q: torch.Tensor, q_start: torch.Tensor, block_tables: torch.Tensor,
                 ctx_lens: torch.Tensor, max_chunk: int, out: torch.Tensor | None = None,
