@@ -1,143 +1,1072 @@
 // pa_tree.cu -- attention of a tree of drafted tokens per sequence over the paged KV cache.
 //
-// A node's result is softmax(scale q K^T) V over its sequence's history and the nodes
-// whose bits its mask row has.  One warp per (node, kv head): the group's queries
-// in registers, one token at a time.
+// A node's result is softmax(scale q K^T) V over its sequence's history and the nodes whose
+// bits its mask row has.  All the nodes of a sequence read the same pages, so per kv
+// head their queries are the rows of one matrix product with K and one with V:
+// nodes x G rows, up to 128 of them (a tile) on the tcgen05 tensor cores, and the pages
+// are read once per tile.  K and V are the bytes that the work cannot do without, and up
+// to about 128 rows the products take no longer than HBM does to deliver them.
+//
+// The pipeline of a CTA is that of the chunked prefill (pa_prefill_tc.cu: operand layouts, the
+// two E4M3 terms of a query, V converted to binary16, the two threads of a row, S and P in
+// one buffer).  What differs:
+//  * one CTA per SM for the whole call, and a schedule made on the device: the blocks of 128
+//    keys of all (sequence, kv head, tile) units, in order, are cut into ranges of equal
+//    cost, one per CTA (a unit costs kUnitCost blocks besides its own).  A range goes from
+//    unit to unit without draining: the copies, the products and the softmax run on over
+//    its pieces (segments), whose descriptions the copying warp hands to the other roles.
+//  * a unit that spans several CTAs leaves partial states (O, m, l) per piece, which
+//    tree_merge_kernel joins.  A long history is thus read by the whole GPU.
+//  * the queries of the next segment are put into the second of two places in tensor memory
+//    while this one runs.
+//  * a mask: blocks that reach the tree take 64 bits per thread from the node's row.
+//  * what a row does not see must not touch it.  A masked key's weight is 0, but 0 times an
+//    infinity or a NaN among V is not: such values of nodes are taken out of the block in shared
+//    memory, and put back for the rows that see them when the output is written.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
-#include "pa_device.cuh"
+#include "pa_tc.cuh"
 
 namespace pa {
 namespace {
 
+using namespace tc;
+
+constexpr int kRows = 128;     // MMA rows of a tile: nodes x the G heads of a kv head
+constexpr int kThreads = 448;  // 14 warps: producer, MMA, 4 for V, 8 softmax
 constexpr unsigned kAll = 0xffffffffu;
+constexpr uint32_t kTmemCols = 512;
+// TMEM columns (one lane per row): S in buffers of 128 at 0 and 128 by block parity, overwritten by
+// P as in the prefill; O at 256; the queries of even segments at 384, of odd ones at 448 (FP8
+// pools: the two E4M3 terms 32 columns apart).
+constexpr uint32_t kOCol = 256, kQCol = 384;
+constexpr int kScaleRing = 8;  // block-scaled pools: blocks whose scales are held
+constexpr int kSegRing = 4;    // segments whose descriptions are held
+// The largest weight is kept near 2^7 and below 2^15, so that small ones stay normal
+// binary16 numbers; the reference point moves when the maximum has grown by 2^8.
+constexpr float kTop = 7.f, kGrow = 15.f;
+
+enum Kind { K_E4M3 = 0, K_E4M3B = 1, K_BF16 = 2, K_F16 = 3 };
+
+template <int KIND, int D>
+struct Lay {
+  static constexpr bool kF8 = KIND == K_E4M3 || KIND == K_E4M3B;
+  static constexpr bool kBlk = KIND == K_E4M3B;
+  static constexpr bool kBf = KIND == K_BF16;
+  static constexpr int kRow = D * (kF8 ? 1 : 2);       // bytes of a key
+  static constexpr int kHalves = kRow == 256 ? 2 : 1;  // 128-byte parts, loaded and laid out apart
+  static constexpr int kPart = kRow / kHalves;
+  static constexpr int kSlot = 128 * kRow;  // a block of K, or of V
+  static constexpr int kRing = kSlot == 32768 ? 3 : 4;
+  static constexpr int kVT = 2 * kRing * kSlot;      // FP8: two blocks of V in binary16
+  static constexpr int kVTBlock = 128 * D * 2;
+  static constexpr int kData = kVT + (kF8 ? 2 * kVTBlock : 0);
+  // a block needs kUnitCost more for its unit's queries and output rows
+  static constexpr int kUnitCost = kF8 ? 3 : 2;
+};
+
+// A segment: blocks [b0, b1) of a unit; b1 == b0 ends the list.
+struct Seg {
+  int seq, h, tile, b0;
+  int b1, n, base, q0;
+  int nblk, last_cta, pad0, pad1;
+};
+
+struct Ctrl {
+  Seg seg[kSegRing];
+  uint64_t seg_full[kSegRing], seg_empty[kSegRing];
+  uint64_t kv_full[4], kv_empty[4], s_full[2], p_full[2], vt_full[2], vt_empty[2];
+  uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
+  uint64_t q_ready[2], o_full, drain, xchg[4];
+  uint64_t tail_ready[2], tail_done[2];  // 16-bit pools: blocks that reach the tree, by their parity
+  float2 sc[kScaleRing][8];              // block-scaled pools: (K scale, V scale) of each page of a block
+  float xbuf[2][128][2];                 // the two half-row threads' partials
+  long long warp_sums[kThreads / 32];
+  long long start_off;
+  int start_seq;
+  int bad[8];  // segment j's V had infinities or NaN among its nodes: bad[j % 8] == j + 1
+  uint32_t tmem;
+  int abort;
+};
+
+template <int KIND, int D>
+constexpr int smem_bytes() {
+  // (at least 116 KiB: two CTAs on an SM would wait for each other's tensor memory)
+  constexpr int n = 1024 + Lay<KIND, D>::kData + (int)sizeof(Ctrl);
+  static_assert(n <= 232448, "shared memory budget");
+  return n > 118784 ? n : 118784;
+}
 
 struct TreeArgs {
   const uint16_t* q;
   void* out;
-  const uint64_t* mask;
+  const uint64_t* mask;  // nullptr: chains
   const int32_t* q_start;
   const int32_t* tables;
   const int32_t* ctx;
-  const uint8_t* k;
-  const uint8_t* v;
-  const float* ksc;
+  const uint8_t* v;  // this layer's V, for the values put back
+  const float* ksc;  // block-scaled pools: this layer's scales [num_blocks][Hkv]
   const float* vsc;
-  int T, S, Hq, Hkv, G, max_blocks, num_blocks, max_nodes, words;
-  float scale, k_scale, v_scale;
+  float* ws_o;       // [2 ctas][128][D]
+  float2* ws_ml;     // [2 ctas][128] (m in log2 units, l)
+  int4* jobs;        // [ctas] units to merge: (sequence, kv head and tile, last CTA, slot)
+  int T, S, Hq, Hkv, G, tile_nodes, max_nodes, words, max_blocks, num_blocks, ctas;
+  float qk_scale_log2;  // softmax_scale * log2(e) (* k_scale of a static FP8 pool)
+  float v_scale;        // static FP8 pool's V scale, else 1
   unsigned int* err;
 };
 
-// Two neighbouring elements of a row.
-template <int KV>
-__device__ __forceinline__ float2 elem2(const uint8_t* row, int pair) {
-  if constexpr (KV == PA_FP16 || KV == PA_BF16)
-    return unpack2<KV == PA_BF16>(reinterpret_cast<const uint32_t*>(row)[pair]);
-  else
-    return unpack2<false>(e4m3x2_to_f16x2(reinterpret_cast<const uint16_t*>(row)[pair]));
+// A sequence's place in the schedule.
+struct SeqInfo {
+  int q0, n, ctx, tiles, nblk;
+  bool bad;
+  __device__ long long units(int Hkv) const { return (long long)tiles * Hkv; }
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const TreeArgs& a, int s) {
+  SeqInfo i;
+  i.q0 = a.q_start[s];
+  const long long q1 = a.q_start[s + 1], n = q1 - i.q0;
+  i.n = i.ctx = i.tiles = i.nblk = 0;
+  i.bad = false;
+  if (n == 0) return i;
+  i.ctx = a.ctx[s];
+  if (i.q0 < 0 || n < 0 || q1 > a.T || n > a.max_nodes || i.ctx < n || i.ctx > 16 * a.max_blocks) {
+    i.bad = true;
+    return i;
+  }
+  i.n = (int)n;
+  i.tiles = (i.n + a.tile_nodes - 1) / a.tile_nodes;
+  i.nblk = (i.ctx + 127) >> 7;
+  return i;
 }
 
-template <int KV, int D, bool F32>
-__global__ void __launch_bounds__(128) tree_kernel(const TreeArgs a) {
-  constexpr int EB = KV == PA_FP16 || KV == PA_BF16 ? 2 : 1;
-  constexpr int P = D / 64;  // pairs of dimensions a lane holds
-  const int lane = threadIdx.x & 31;
-  const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int h = (int)(unit % a.Hkv), node0 = (int)(unit / a.Hkv % a.max_nodes);
-  const long long s = unit / a.Hkv / a.max_nodes;
-  if (s >= a.S) return;
-  const int q0 = a.q_start[s], q1 = a.q_start[s + 1];
-  const long long n = (long long)q1 - q0;
-  if (n == 0) return;
-  const int ctx = a.ctx[s];
-  if (q0 < 0 || n < 0 || q1 > a.T || n > a.max_nodes || ctx < n || ctx > 16ll * a.max_blocks) {
-    if (lane == 0) record_error(a.err, PA_ERR_BOUNDS);
-    return;
+// The mask of a row over the 64 nodes from j0 on (bits of nodes below 0, history, are set).
+__device__ __forceinline__ uint64_t sees64(const TreeArgs& a, long long row, int own, int n, int j0) {
+  if (j0 <= -64) return ~0ull;
+  if (!a.mask) {
+    const int last = own - j0;  // the last bit set
+    return last < 0 ? 0ull : last >= 63 ? ~0ull : (2ull << last) - 1;
   }
-  if (node0 >= n) return;
-  const int t = q0 + node0;
-  const int base = ctx - (int)n;
-  float2 q[8][P], o[8][P];
-  float m[8], l[8];
+  const uint64_t* w = a.mask + row * a.words;
+  uint64_t v;
+  if (j0 < 0) {
+    v = (w[0] << -j0) | ((1ull << -j0) - 1);
+  } else {
+    const int i = j0 >> 6, sh = j0 & 63;
+    const uint64_t lo = i < a.words ? w[i] : 0, hi = i + 1 < a.words ? w[i + 1] : 0;
+    v = sh ? (lo >> sh) | (hi << (64 - sh)) : lo;
+  }
+  const int valid = n - j0;
+  return valid <= 0 ? 0ull : valid >= 64 ? v : v & ((1ull << valid) - 1);
+}
+
+__device__ __forceinline__ bool sees(const TreeArgs& a, long long row, int own, int j) {
+  return a.mask ? a.mask[row * a.words + (j >> 6)] >> (j & 63) & 1 : j <= own;
+}
+
+// The infinities and NaN among 16 bytes of V, taken out (true if there were any).
+template <int KIND>
+__device__ __forceinline__ bool take_out(uint4& x) {
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t any = 0;
 #pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    m[g] = -INFINITY;
-    l[g] = 0.f;
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      o[g][p] = make_float2(0.f, 0.f);
-      q[g][p] = make_float2(0.f, 0.f);
-      if (g < a.G)
-        q[g][p] = unpack2<KV != PA_FP16>(reinterpret_cast<const uint32_t*>(a.q + ((size_t)t * a.Hq + h * a.G + g) * D)[32 * p + lane]);
+  for (int i = 0; i < 4; ++i) {
+    uint32_t m;
+    if constexpr (KIND == K_BF16) m = __vcmpeq2(w[i] & 0x7F807F80u, 0x7F807F80u);
+    else if constexpr (KIND == K_F16) m = __vcmpeq2(w[i] & 0x7C007C00u, 0x7C007C00u);
+    else m = __vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    any |= m;
+    w[i] &= ~m;
+  }
+  x = make_uint4(w[0], w[1], w[2], w[3]);
+  return any != 0;
+}
+
+// Adds to o (32 columns from dim d0) the infinities and NaN of V of the nodes that the row sees in the
+// segment.
+template <int KIND, int D>
+__device__ __noinline__ void put_back(const TreeArgs& a, const Seg& sg, long long row, int own, int d0, float* o) {
+  using L = Lay<KIND, D>;
+  for (int j = max(0, 128 * sg.b0 - sg.base); j < min(sg.n, 128 * sg.b1 - sg.base); ++j) {
+    if (!sees(a, row, own, j)) continue;
+    const int t = sg.base + j, blk = a.tables[(size_t)sg.seq * a.max_blocks + (t >> 4)];
+    if (blk < 0 || blk >= a.num_blocks) continue;
+    const uint8_t* v = a.v + (((size_t)blk * a.Hkv + sg.h) * 16 + (t & 15)) * L::kRow;
+    for (int e = 0; e < 32; ++e) {
+      float x;
+      if constexpr (KIND == K_BF16) x = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(v)[d0 + e]);
+      else if constexpr (KIND == K_F16) x = __half2float(reinterpret_cast<const __half*>(v)[d0 + e]);
+      else x = (v[d0 + e] & 0x7F) == 0x7F ? NAN : 0.f;
+      if (!(fabsf(x) < INFINITY)) o[e] += x;
     }
   }
-  for (int j = 0; j < ctx; ++j) {
-    const int node = j - base;
-    if (node >= 0 && !(a.mask ? a.mask[(size_t)t * a.words + (node >> 6)] >> (node & 63) & 1 : node <= t - q0)) continue;
-    const int blk = a.tables[(size_t)s * a.max_blocks + (j >> 4)];
-    if (blk < 0 || blk >= a.num_blocks) {
-      if (lane == 0) record_error(a.err, PA_ERR_BOUNDS);
-      continue;
+}
+
+template <int KIND, int D, int OUT, bool PSPLIT>
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk,
+                                                           const __grid_constant__ CUtensorMap tmv) {
+  using L = Lay<KIND, D>;
+  constexpr bool F8 = L::kF8, BLK = L::kBlk, BF = L::kBf;
+  constexpr int R = L::kRing;
+  constexpr int DH = D / 2;  // a half-row thread's share of the head dim
+  constexpr uint32_t kIdescQK = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24) | (BF ? (1u << 7) | (1u << 10) : 0u);
+  constexpr uint32_t kIdescPV =
+      (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24) | (BF ? (1u << 7) | (1u << 10) : 0u);
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Ctrl* ctl = reinterpret_cast<Ctrl*>(sm + L::kData);
+  volatile int* abort_flag = &ctl->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSegRing; ++i) {
+      mbar_init(&ctl->seg_full[i], 1);
+      mbar_init(&ctl->seg_empty[i], 13);  // MMA, 4 warps for V, 8 softmax
     }
-    const size_t tile = (size_t)blk * a.Hkv + h;
-    const uint8_t* kr = a.k + (tile * 16 + (j & 15)) * D * EB;
-    const uint8_t* vr = a.v + (tile * 16 + (j & 15)) * D * EB;
-    const float ks = a.ksc ? a.ksc[tile] : a.k_scale, vs = a.vsc ? a.vsc[tile] : a.v_scale;
-    float2 k[P], v[P];
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      k[p] = elem2<KV>(kr, 32 * p + lane);
-      v[p] = elem2<KV>(vr, 32 * p + lane);
+    for (int i = 0; i < R; ++i) {
+      mbar_init(&ctl->kv_full[i], 1);
+      mbar_init(&ctl->kv_empty[i], F8 ? 5 : 1);  // FP8: the Q K MMAs and four warps; 16-bit: the P V MMAs
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->s_full[i], 1);
+      mbar_init(&ctl->p_full[i], 8);
+      mbar_init(&ctl->vt_full[i], 4);
+      mbar_init(&ctl->vt_empty[i], 1);
+      mbar_init(&ctl->q_ready[i], 8);
+      mbar_init(&ctl->tail_ready[i], 1);
+      mbar_init(&ctl->tail_done[i], 4);
+    }
+    for (int i = 0; i < kScaleRing; ++i) {
+      mbar_init(&ctl->sc_full[i], 1);
+      mbar_init(&ctl->sc_empty[i], 8);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&ctl->xchg[i], 2);
+    for (int i = 0; i < 8; ++i) ctl->bad[i] = 0;
+    mbar_init(&ctl->o_full, 1);
+    mbar_init(&ctl->drain, 1);
+    ctl->abort = 0;
+    ctl->start_seq = -1;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&tmk);
+    prefetch_tensormap(&tmv);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 ::"r"(smem_addr(&ctl->tmem)), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  grid_dependency_wait();  // the kernel before may still write lengths, tables, queries and pages
+
+  // ---------------------------------------------------------------- schedule
+  // Positions: a unit of nblk blocks takes kUnitCost + nblk of them, its blocks behind; units in
+  // (sequence, kv head, tile) order.  Each CTA takes T positions.
+  constexpr int kUnit = L::kUnitCost;
+  const int per = (a.S + kThreads - 1) / kThreads;
+  const int s0 = min(a.S, (int)threadIdx.x * per), s1 = min(a.S, s0 + per);
+  long long mine = 0;
+  for (int s = s0; s < s1; ++s) {
+    const SeqInfo i = seq_info(a, s);
+    if (i.bad) record_error(a.err, PA_ERR_BOUNDS);
+    mine += i.units(a.Hkv) * (i.nblk + kUnit);
+  }
+  long long before, total = 0;
+  {
+    long long x = mine;
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      if (g >= a.G) break;
-      float x = 0.f;
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long y = __shfl_up_sync(kAll, x, off);
+      if (lane >= off) x += y;
+    }
+    if (lane == 31) ctl->warp_sums[warp] = x;
+    __syncthreads();
+    long long ahead = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      ahead += w < warp ? ctl->warp_sums[w] : 0;
+      total += ctl->warp_sums[w];
+    }
+    before = ahead + x - mine;
+  }
+  const long long T = max((total + a.ctas - 1) / a.ctas, (long long)kUnit + 1);
+  const long long pos0 = (long long)blockIdx.x * T, pos_end = min(total, pos0 + T);
+  if (pos0 < total && before <= pos0 && pos0 < before + mine) {
+    long long cum = before;
+    for (int s = s0; s < s1; ++s) {
+      const SeqInfo i = seq_info(a, s);
+      const long long c = i.units(a.Hkv) * (i.nblk + kUnit);
+      if (pos0 < cum + c) {
+        ctl->start_seq = s;
+        ctl->start_off = pos0 - cum;
+        break;
+      }
+      cum += c;
+    }
+  }
+  if (threadIdx.x == 0) a.jobs[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+
+  if (pos0 >= total || ctl->start_seq < 0) {
+    // no work for this CTA
+  } else if (warp == 0) {
+    // ---------------------------------------------------------- schedule and TMA producer
+    const uint64_t policy = l2_evict_first_policy();
+    int seq = ctl->start_seq;
+    SeqInfo info = seq_info(a, seq);
+    int span = info.nblk + kUnit;
+    long long u = ctl->start_off / span;
+    int v = (int)(ctl->start_off - u * span);
+    long long pos = pos0;
+    bool ok = true;
+    int made = 0;  // descriptions handed out
+    auto produce = [&]() -> Seg {
+      Seg sg = {};
+      while (pos < pos_end) {
+        while (u >= info.units(a.Hkv)) {
+          if (++seq >= a.S) break;
+          info = seq_info(a, seq);
+          span = info.nblk + kUnit;
+          u = 0;
+          v = 0;
+        }
+        if (seq >= a.S) break;  // (the lengths changed under the kernel)
+        const int take = (int)min((long long)(span - v), pos_end - pos);
+        const int b0 = max(0, v - kUnit), b1 = max(0, v + take - kUnit);
+        const long long ustart = pos - v;
+        const int unit = (int)u, nblk = info.nblk;
+        pos += take;
+        v += take;
+        if (v == span) {
+          v = 0;
+          ++u;
+        }
+        if (b1 > b0) {
+          sg.seq = seq;
+          sg.h = unit / info.tiles;
+          sg.tile = unit - sg.h * info.tiles;
+          sg.b0 = b0;
+          sg.b1 = b1;
+          sg.n = info.n;
+          sg.base = info.ctx - info.n;
+          sg.q0 = info.q0;
+          sg.nblk = nblk;
+          sg.last_cta = (int)((ustart + span - 1) / T);
+          if (b0 == 0 && b1 < nblk && lane == 0)
+            a.jobs[blockIdx.x] = make_int4(seq, unit, sg.last_cta, 2 * blockIdx.x + (made > 0));
+          break;
+        }
+      }
+      const int e = made % kSegRing;
+      if (made >= kSegRing)
+        ok = ok && __all_sync(kAll, wait_or_abort(&ctl->seg_empty[e], ((made / kSegRing) - 1) & 1, abort_flag, a.err));
+      if (ok && lane == 0) {
+        ctl->seg[e] = sg;
+        mbar_arrive(&ctl->seg_full[e]);
+      }
+      ++made;
+      if (!ok) sg.b1 = sg.b0;
+      return sg;
+    };
+    Seg cur = produce(), nxt = {};
+    if (cur.b1 > cur.b0) nxt = produce();
+    int g = 0;  // blocks issued
+    while (ok && cur.b1 > cur.b0) {
+      const int32_t* trow = a.tables + (size_t)cur.seq * a.max_blocks;
+      const int page_end = min(8 * cur.b1, (cur.base + cur.n + 15) >> 4);
+      // lane i holds the entry (and tile scales) of page i of a batch of four blocks; the
+      // next batch's entries are loaded one batch ahead
+      auto entry = [&](int page) { return page < page_end ? trow[page] : 0; };
+      int phys = 0, next = entry(8 * cur.b0 + 32 + lane);
+      float sk = 1.f, sv = 0.f;
+      auto take = [&](int raw, int page) {
+        phys = raw;
+        if (page < page_end && (raw < 0 || raw >= a.num_blocks)) {
+          record_error(a.err, PA_ERR_BOUNDS);
+          phys = 0;
+        }
+        if constexpr (BLK) {
+          sk = 1.f;
+          sv = 0.f;
+          if (page < page_end) {
+            sk = a.ksc[(size_t)phys * a.Hkv + cur.h];
+            sv = a.vsc[(size_t)phys * a.Hkv + cur.h];
+            // a tile without a finite scale holds NaN: marked by -1
+            if (!(fabsf(sk) < INFINITY)) sk = -1.f;
+            if (!(fabsf(sv) < INFINITY)) sv = -1.f;
+          }
+        }
+      };
+      take(entry(8 * cur.b0 + lane), 8 * cur.b0 + lane);
+      for (int b = cur.b0; b < cur.b1; ++b, ++g) {
+        const int slot = g % R, j = b - cur.b0, pb = 8 * (j & 3);
+        if (j > 0 && pb == 0) {
+          take(next, 8 * b + lane);
+          next = entry(8 * b + 32 + lane);
+        }
+        if (g >= R) ok = __all_sync(kAll, wait_or_abort(&ctl->kv_empty[slot], ((g / R) - 1) & 1, abort_flag, a.err));
+        if (!ok) break;
+        const int cnt = min(8, page_end - 8 * b);
+        if constexpr (BLK) {
+          const int e = g % kScaleRing;
+          if (g >= kScaleRing)
+            ok = __all_sync(kAll, wait_or_abort(&ctl->sc_empty[e], ((g / kScaleRing) - 1) & 1, abort_flag, a.err));
+          if (!ok) break;
+          if (lane >= pb && lane < pb + 8) ctl->sc[e][lane - pb] = make_float2(sk, sv);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->sc_full[e]);
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&ctl->kv_full[slot], (uint32_t)cnt * 32u * L::kRow);
+        const int i = lane - pb;  // this lane's page of the block
+        if (i >= 0 && i < cnt) {
+          const int row0 = (phys * a.Hkv + cur.h) * 16;
+          uint8_t* kd = sm + slot * L::kSlot + i * 16 * L::kPart;
+          uint8_t* vd = kd + R * L::kSlot;
 #pragma unroll
-      for (int p = 0; p < P; ++p) x += q[g][p].x * k[p].x + q[g][p].y * k[p].y;
+          for (int hh = 0; hh < L::kHalves; ++hh) {
+            tma_load_2d(kd + hh * 16384, &tmk, 128 * hh, row0, &ctl->kv_full[slot], policy);
+            tma_load_2d(vd + hh * 16384, &tmv, 128 * hh, row0, &ctl->kv_full[slot], policy);
+          }
+        }
+      }
+      if (!ok) break;
+      cur = nxt;
+      if (cur.b1 > cur.b0) nxt = produce();
+    }
+    // no copy may still target shared memory when the CTA exits
+    if (lane == 0)
+      for (int j = max(0, g - R); j < g; ++j)
+        if (!mbar_wait(&ctl->kv_full[j % R], (j / R) & 1)) record_error(a.err, PA_ERR_TIMEOUT);
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issue
+    if (lane == 0) {
+      const uint64_t kdesc0 = L::kPart == 64
+                                  ? (uint64_t)((smem_addr(sm) & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) |
+                                        ((uint64_t)(512 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)4 << 61)
+                                  : kmajor(smem_addr(sm));
+      const uint64_t vdesc0 = mnmajor(smem_addr(sm + (F8 ? L::kVT : R * L::kSlot)));
+      bool run = true;
+      // cursors over the blocks: Q K^T, two blocks ahead of P V
+      int gq = 0, jq = -1, bq = 0, bq1 = 0, qbase = 0, tq = 0;
+      bool q_end = false;
+      int gp = 0, jp = -1, bp = 0, bp0 = 0, bp1 = 0, pbase = 0, tp = 0;
+      auto seg_wait = [&](int j) { return wait_or_abort(&ctl->seg_full[j % kSegRing], (j / kSegRing) & 1, abort_flag, a.err); };
+      auto issue_qk = [&]() -> bool {
+        if (q_end) return true;
+        if (bq == bq1) {
+          ++jq;
+          if (!seg_wait(jq)) return false;
+          const Seg& sg = ctl->seg[jq % kSegRing];
+          bq = sg.b0;
+          bq1 = sg.b1;
+          qbase = sg.base;
+          if (bq == bq1) {
+            q_end = true;
+            return true;
+          }
+          if (!wait_or_abort(&ctl->q_ready[jq & 1], (jq >> 1) & 1, abort_flag, a.err)) return false;
+        }
+        const int slot = gq % R, sb = gq & 1;
+        if (!wait_or_abort(&ctl->kv_full[slot], (gq / R) & 1, abort_flag, a.err)) return false;
+        tc_fence_after();
+        if constexpr (!F8)
+          if (128 * bq + 127 >= qbase) {  // V of a block that reaches the tree is looked through first
+            mbar_arrive(&ctl->tail_ready[tq & 1]);
+            ++tq;
+          }
+        const uint64_t kd = kdesc0 + (uint64_t)(slot * (L::kSlot >> 4));
+        const uint32_t qcol = tmem + kQCol + 64 * (jq & 1);
+        if constexpr (F8) {
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(kAll, x, off);
-      x *= a.scale * ks;
-      const float mn = fmaxf(m[g], x);
-      if (mn == -INFINITY && x == x) continue;  // (a NaN counts)
-      const float f = expf(m[g] - mn), w = expf(x - mn);
-      m[g] = mn;
-      l[g] = l[g] * f + w;
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        o[g][p].x = o[g][p].x * f + w * (v[p].x * vs);
-        o[g][p].y = o[g][p].y * f + w * (v[p].y * vs);
+            for (int k = 0; k < D / 32; ++k)
+              mma_f8_ts(tmem + sb * 128, qcol + 32 * t + 8 * k, kd + 2 * k, kIdescQK, (uint32_t)(t | k));
+        } else {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_f16_ts(tmem + sb * 128, qcol + 8 * k, kd + (k >> 2) * (16384 >> 4) + (k & 3) * 2, kIdescQK, (uint32_t)k);
+        }
+        mma_commit(&ctl->s_full[sb]);
+        if constexpr (F8) mma_commit(&ctl->kv_empty[slot]);
+        ++gq;
+        ++bq;
+        return true;
+      };
+      run = issue_qk() && issue_qk();
+      while (run) {
+        if (bp == bp1) {
+          ++jp;
+          if (!(run = seg_wait(jp))) break;
+          const Seg& sg = ctl->seg[jp % kSegRing];
+          bp = bp0 = sg.b0;
+          bp1 = sg.b1;
+          pbase = sg.base;
+          mbar_arrive(&ctl->seg_empty[jp % kSegRing]);
+          if (bp == bp1) break;
+        }
+        const int vb = gp & 1;
+        run = wait_or_abort(&ctl->p_full[vb], (gp >> 1) & 1, abort_flag, a.err);
+        if constexpr (F8) {
+          run = run && wait_or_abort(&ctl->vt_full[vb], (gp >> 1) & 1, abort_flag, a.err);
+        } else if (run && 128 * bp + 127 >= pbase) {
+          run = wait_or_abort(&ctl->tail_done[tp & 1], (tp >> 1) & 1, abort_flag, a.err);
+          ++tp;
+        }
+        if (!run) break;
+        tc_fence_after();
+        const uint64_t vd = vdesc0 + (uint64_t)(F8 ? vb * (L::kVTBlock >> 4) : (gp % R) * (L::kSlot >> 4));
+#pragma unroll
+        for (int part = 0; part < (PSPLIT ? 2 : 1); ++part)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_f16_ts(tmem + kOCol, tmem + vb * 128 + 32 * (k >> 1) + 16 * part + 8 * (k & 1), vd + k * (2048 >> 4),
+                       kIdescPV, (uint32_t)((bp > bp0) | k | part));
+        if constexpr (F8) mma_commit(&ctl->vt_empty[vb]);
+        else mma_commit(&ctl->kv_empty[gp % R]);  // K and V of the block are read
+        if (bp + 1 == bp1) mma_commit(&ctl->o_full);
+        ++gp;
+        ++bp;
+        run = issue_qk();
+      }
+      // every MMA issued above has finished before TMEM is released
+      mma_commit(&ctl->drain);
+      if (!mbar_wait(&ctl->drain, 0)) record_error(a.err, PA_ERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (warp < 4 || warp >= 12) {
+    // ---------------------------------------------------------- V
+    const int ct = 32 * (warp < 4 ? warp - 2 : warp - 10) + lane;  // 0 .. 127
+    int g = 0, t = 0;
+    bool ok = true;
+    for (int j = 0; ok; ++j) {
+      const int e = j % kSegRing;
+      ok = __all_sync(kAll, wait_or_abort(&ctl->seg_full[e], (j / kSegRing) & 1, abort_flag, a.err));
+      if (!ok) break;
+      const int b0 = ctl->seg[e].b0, b1 = ctl->seg[e].b1, base = ctl->seg[e].base, ctx = base + ctl->seg[e].n;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->seg_empty[e]);
+      if (b0 == b1) break;
+      for (int b = b0; b < b1; ++b, ++g) {
+        const int slot = g % R;
+        const int nvalid = min(128, ctx - 128 * b);  // keys behind the context: zero
+        const int nplain = base - 128 * b;           // keys from here on are nodes
+        bool odd = false;                            // infinities or NaN among them
+        if constexpr (F8) {
+          const int half = g & 1;
+          ok = __all_sync(kAll, wait_or_abort(&ctl->kv_full[slot], (g / R) & 1, abort_flag, a.err));
+          if (ok && g >= 2) ok = __all_sync(kAll, wait_or_abort(&ctl->vt_empty[half], ((g >> 1) - 1) & 1, abort_flag, a.err));
+          if (!ok) break;
+          const uint8_t* vr = sm + (R + slot) * L::kSlot;
+          uint8_t* vt = sm + L::kVT + half * L::kVTBlock;
+          // consecutive lanes take consecutive keys of one 16-byte chunk
+#pragma unroll 4
+          for (int it = 0; it < D / 16; ++it) {
+            const int key = ct, ch = it;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            // a row's chunks are permuted by its line's place: 128-byte lines, or 64-byte rows two to a line
+            const uint32_t off = L::kPart == 64 ? key * 64 + ((ch ^ ((key >> 1) & 3)) << 4) : key * 128 + ((ch ^ (key & 7)) << 4);
+            if (key < nvalid) w = lds128(vr + off);
+            if (nplain < 128 && key >= nplain) odd |= take_out<KIND>(w);
+            const uint32_t cw[4] = {w.x, w.y, w.z, w.w};
+            uint32_t hv[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) e4m3x4_to_f16x2x2(cw[q], hv[2 * q], hv[2 * q + 1]);
+            uint8_t* row = vt + (ch >> 2) * 16384 + key * 128;
+            const int c0 = (ch & 3) * 2;
+            *reinterpret_cast<uint4*>(row + ((c0 ^ (key & 7)) << 4)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+            *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (key & 7)) << 4)) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
+          }
+          if (odd) ctl->bad[j & 7] = j + 1;
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&ctl->vt_full[half]);
+            mbar_arrive(&ctl->kv_empty[slot]);
+          }
+        } else if (nplain < 128) {
+          // read in place: rows behind the context are zeroed, nodes' rows looked through
+          ok = __all_sync(kAll, wait_or_abort(&ctl->tail_ready[t & 1], (t >> 1) & 1, abort_flag, a.err));
+          ok = ok && __all_sync(kAll, wait_or_abort(&ctl->kv_full[slot], (g / R) & 1, abort_flag, a.err));
+          if (!ok) break;
+          uint8_t* vr = sm + (R + slot) * L::kSlot;
+          constexpr int CH = D / 8;  // 16-byte chunks per key
+          const int first = max(0, nplain);
+          for (int idx = ct; idx < (128 - first) * CH; idx += 128) {
+            const int key = first + idx / CH, c = idx % CH;
+            uint4* p = reinterpret_cast<uint4*>(vr + (c >> 3) * 16384 + key * 128 + (c & 7) * 16);
+            if (key >= nvalid) {
+              *p = make_uint4(0, 0, 0, 0);
+            } else {
+              uint4 w = *p;
+              if (take_out<KIND>(w)) {
+                *p = w;
+                odd = true;
+              }
+            }
+          }
+          if (odd) ctl->bad[j & 7] = j + 1;
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->tail_done[t & 1]);
+          ++t;
+        }
       }
     }
+  } else {
+    // ---------------------------------------------------------- softmax rows
+    // Two threads per row, as in the prefill: row r in TMEM lane r; half hf takes keys 64 hf ..
+    // 64 hf + 63 of every block and the head dim's half hf of Q and O.  The two warps of 32
+    // rows exchange partials through shared memory (one phase of their barrier each).  Warps whose
+    // rows are all behind the tile's only keep the barriers in step.
+    const int sw = warp - 4, hf = sw >> 2, quad = sw & 3;
+    const int r = quad * 32 + lane;
+    const int tl = r / a.G, hh = r - tl * a.G;  // node of the tile, head of the group
+    const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
+    int xk = 0;  // next exchange phase
+    bool ok = true;
+    auto exchange = [&](float mine, float& lo_half, float& hi_half) {
+      ctl->xbuf[xk & 1][r][hf] = mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->xchg[quad]);
+      ok = __all_sync(kAll, (ok && wait_or_abort(&ctl->xchg[quad], xk & 1, abort_flag, a.err)));
+      lo_half = ctl->xbuf[xk & 1][r][0];
+      hi_half = ctl->xbuf[xk & 1][r][1];
+      ++xk;
+    };
+    constexpr float kMinFactor = 1.17549435e-38f;  // a zero factor would turn a masked -inf into NaN
+    auto read_seg = [&](int j, Seg& sg) {
+      const int e = j % kSegRing;
+      ok = __all_sync(kAll, ok && wait_or_abort(&ctl->seg_full[e], (j / kSegRing) & 1, abort_flag, a.err));
+      sg = {};
+      if (ok) sg = ctl->seg[e];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->seg_empty[e]);
+    };
+    auto tile_rows = [&](const Seg& sg) { return min(a.tile_nodes, sg.n - sg.tile * a.tile_nodes) * a.G; };
+    // Puts a segment's queries into tensor memory; returns the row's score factor.
+    auto put_q = [&](const Seg& sg, int j) -> float {
+      float row_scale = fabsf(a.qk_scale_log2);
+      const int rows = tile_rows(sg);
+      if (quad * 32 < rows) {
+        constexpr int QW = DH / 2;  // 32-bit words of this half
+        uint32_t qw[QW];
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + ((size_t)(sg.q0 + sg.tile * a.tile_nodes + tl) * a.Hq + (size_t)sg.h * a.G + hh) * D + DH * hf);
+#pragma unroll
+        for (int c = 0; c < QW / 4; ++c) {
+          const uint4 x = r < rows ? src[c] : make_uint4(0, 0, 0, 0);
+          qw[4 * c] = x.x;
+          qw[4 * c + 1] = x.y;
+          qw[4 * c + 2] = x.z;
+          qw[4 * c + 3] = x.w;
+        }
+        const uint32_t qcol = trow + kQCol + 64 * (j & 1);
+        if constexpr (!F8) {
+          if (a.qk_scale_log2 < 0.f) {  // a negative scale flips the queries' signs
+#pragma unroll
+            for (int w = 0; w < QW; ++w) qw[w] ^= 0x80008000u;
+          }
+          if constexpr (QW == 32) tmem_st32u(qcol + 32 * hf, qw);
+          else tmem_st16u(qcol + 16 * hf, qw);
+        } else {
+          float am = 0.f;
+#pragma unroll
+          for (int w = 0; w < QW; ++w)
+            am = fmaxf(am, fmaxf(fabsf(bf16_bits_to_float(qw[w] & 0xFFFFu)), fabsf(bf16_bits_to_float(qw[w] >> 16))));
+          float a0, a1;
+          exchange(am, a0, a1);
+          const float amax = fmaxf(a0, a1);
+          int ex = 0;
+          if (amax > 0.f) frexpf(amax, &ex);
+          const float sgn = a.qk_scale_log2 < 0.f ? -1.f : 1.f;
+          const float qs = sgn * (amax > 0.f ? ldexpf(1.f, 8 - ex) : 1.f);
+          row_scale *= amax > 0.f ? ldexpf(1.f, ex - 8) : 1.f;
+          uint32_t qhi[QW / 2], qlo[QW / 2];  // 4 dims per word
+#pragma unroll
+          for (int c = 0; c < QW / 2; ++c) {
+            const uint32_t w0 = qw[2 * c], w1 = qw[2 * c + 1];
+            const float2 x01 = make_float2(bf16_bits_to_float(w0 & 0xFFFFu) * qs, bf16_bits_to_float(w0 >> 16) * qs);
+            const float2 x23 = make_float2(bf16_bits_to_float(w1 & 0xFFFFu) * qs, bf16_bits_to_float(w1 >> 16) * qs);
+            const uint32_t h01 = __nv_cvt_float2_to_fp8x2(x01, __NV_SATFINITE, __NV_E4M3);
+            const uint32_t h23 = __nv_cvt_float2_to_fp8x2(x23, __NV_SATFINITE, __NV_E4M3);
+            const float2 d01 = unpack2<false>(e4m3x2_to_f16x2(h01));
+            const float2 d23 = unpack2<false>(e4m3x2_to_f16x2(h23));
+            const uint32_t l01 = __nv_cvt_float2_to_fp8x2(make_float2(x01.x - d01.x, x01.y - d01.y), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t l23 = __nv_cvt_float2_to_fp8x2(make_float2(x23.x - d23.x, x23.y - d23.y), __NV_SATFINITE, __NV_E4M3);
+            qhi[c] = (h01 & 0xFFFFu) | (h23 << 16);
+            qlo[c] = (l01 & 0xFFFFu) | (l23 << 16);
+          }
+          if constexpr (QW == 32) {
+            tmem_st16u(qcol + 16 * hf, qhi);
+            tmem_st16u(qcol + 32 + 16 * hf, qlo);
+          } else {
+            tmem_st8u(qcol + 8 * hf, qhi);
+            tmem_st8u(qcol + 32 + 8 * hf, qlo);
+          }
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->q_ready[j & 1]);
+      return fmaxf(row_scale, kMinFactor);
+    };
+
+    Seg cur, nxt;
+    read_seg(0, cur);
+    float next_scale = cur.b1 > cur.b0 ? put_q(cur, 0) : 0.f;
+    int g = 0;
+    for (int j = 0; ok && cur.b1 > cur.b0; ++j) {
+      const float row_scale = next_scale;
+      const int rows = tile_rows(cur);
+      const bool active = quad * 32 < rows;
+      const int own = cur.tile * a.tile_nodes + min(tl, rows / a.G - 1);  // this row's node
+      const long long qrow = (long long)cur.q0 + own;
+      float m = -INFINITY, l = 0.f, vref = 0.f;
+      for (int b = cur.b0; b < cur.b1; ++b, ++g) {
+        const int sb = g & 1, se = g % kScaleRing;
+        const bool first = b == cur.b0;
+        float ov = 1.f, vinv = 1.f;  // factor for this row's O; 1 / vref
+        if constexpr (BLK) {         // V weights are taken relative to the largest V scale seen (<= 1)
+          ok = __all_sync(kAll, ok && wait_or_abort(&ctl->sc_full[se], (g / kScaleRing) & 1, abort_flag, a.err));
+          float vb = vref;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) vb = fmaxf(vb, ctl->sc[se][i].y);
+          if (vb > vref) {
+            ov = vref / vb;
+            vref = vb;
+          }
+          vinv = vref > 0.f ? 1.f / vref : 0.f;
+        }
+        const int j0 = 128 * b + 64 * hf - cur.base;  // this thread's first key, as a node
+        const bool masked = j0 + 63 >= 0;
+        const uint64_t vis = active && masked ? sees64(a, qrow, own, cur.n, j0) : ~0ull;
+        ok = __all_sync(kAll, ok && wait_or_abort(&ctl->s_full[sb], (g >> 1) & 1, abort_flag, a.err));
+        const uint32_t sbase = trow + sb * 128;
+        if (active) {
+          float mh = -INFINITY;
+          float sv[2][32];  // this thread's 64 scores of the block, read from TMEM once
+          float pf[2][2];   // the score factor of each of the thread's four pages
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+            for (int hp = 0; hp < 2; ++hp)
+              pf[cc][hp] = BLK ? fmaxf(row_scale * ctl->sc[se][2 * (2 * hf + cc) + hp].x, kMinFactor) : row_scale;
+          if (ok) {
+            tc_fence_after();
+            tmem_ld32(sbase + 64 * hf, sv[0]);
+            tmem_ld32(sbase + 64 * hf + 32, sv[1]);
+            tmem_wait_ld();
+            float pm[2][2];  // each page's largest raw score
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              float* v = sv[cc];
+              if (masked) {
+                const uint32_t w = (uint32_t)(vis >> (32 * cc));
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!(w >> e & 1)) v[e] = -INFINITY;
+              }
+              if constexpr (BLK) {
+#pragma unroll
+                for (int hp = 0; hp < 2; ++hp)
+                  if (ctl->sc[se][2 * (2 * hf + cc) + hp].x < 0.f) {  // keys of no finite scale: NaN where seen
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                      if (vis >> (32 * cc + 16 * hp + e) & 1) v[16 * hp + e] = NAN;
+                  }
+              }
+              pm[cc][0] = max16(v);
+              pm[cc][1] = max16(v + 16);
+            }
+            if constexpr (BLK)
+              mh = fmaxf(fmax3f(pm[0][0] * pf[0][0], pm[0][1] * pf[0][1], pm[1][0] * pf[1][0]), pm[1][1] * pf[1][1]);
+            else  // one positive factor: the largest product is the largest score times it
+              mh = fmaxf(fmax3f(pm[0][0], pm[0][1], pm[1][0]), pm[1][1]) * row_scale;
+          }
+          float m0, m1;
+          exchange(mh, m0, m1);
+          const float mx = fmaxf(m0, m1);
+          if (mx > m + kGrow) {  // the first seen keys, or a maximum that grew
+            const float to = mx - kTop, alpha = fast_exp2(m - to);
+            l *= alpha;
+            ov *= alpha;
+            m = to;
+          }
+          const float mref = m == -INFINITY ? 0.f : m;  // (nothing seen yet: every weight is 0)
+          // O is rescaled once the previous block's P V is done (see the prefill for why this phase
+          // of its barrier is never mistaken)
+          if (ok && !first && __any_sync(kAll, ov != 1.f)) {
+            const int gl = g - 1;
+            ok = __all_sync(kAll, F8 ? wait_or_abort(&ctl->vt_empty[gl & 1], (gl >> 1) & 1, abort_flag, a.err)
+                                     : wait_or_abort(&ctl->kv_empty[gl % R], (gl / R) & 1, abort_flag, a.err));
+            if (ok) {
+              tc_fence_after();
+#pragma unroll 1
+              for (int cc = 0; cc < DH / 16; ++cc) {  // 16 columns at a time (the scores are live)
+                uint32_t o[16];
+                const uint32_t oc = trow + kOCol + DH * hf + 16 * cc;
+                tmem_ld16u(oc, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * ov);
+                tmem_st16u(oc, o);
+              }
+              tmem_wait_st();
+            }
+          }
+          // P in 16 bits over the chunk's own S columns (the low part 16 columns on)
+          if (ok) {
+            float rs = 0.f;
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              const int c = 2 * hf + cc;
+              float* v = sv[cc];
+#pragma unroll
+              for (int hp = 0; hp < 2; ++hp) {
+                const float2 f2 = make_float2(pf[cc][hp], pf[cc][hp]), nm = make_float2(-mref, -mref);
+                const float sc = BLK ? ctl->sc[se][2 * c + hp].y : 1.f;
+                const float vm = BLK ? fmaxf(sc, 0.f) * vinv : 1.f;
+                const float2 vm2 = make_float2(vm, vm);
+                float2 t01 = make_float2(0.f, 0.f), t23 = t01;
+                float* x = v + 16 * hp;
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                  const float2 za = __ffma2_rn(make_float2(x[e], x[e + 1]), f2, nm);
+                  const float2 zb = __ffma2_rn(make_float2(x[e + 2], x[e + 3]), f2, nm);
+                  float2 pa = make_float2(fast_exp2(za.x), fast_exp2(za.y));
+                  float2 pb = make_float2(fast_exp2(zb.x), fast_exp2(zb.y));
+                  t01 = __fadd2_rn(t01, pa);
+                  t23 = __fadd2_rn(t23, pb);
+                  if constexpr (BLK) {
+                    pa = __fmul2_rn(pa, vm2);
+                    pb = __fmul2_rn(pb, vm2);
+                  }
+                  x[e] = pa.x;
+                  x[e + 1] = pa.y;
+                  x[e + 2] = pb.x;
+                  x[e + 3] = pb.y;
+                }
+                rs += (t01.x + t01.y) + (t23.x + t23.y);
+                if constexpr (BLK)
+                  if (sc < 0.f) {  // values of no finite scale: NaN where seen
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                      if (vis >> (32 * cc + 16 * hp + e) & 1) x[e] = NAN;
+                  }
+              }
+              uint32_t ph[16], pl[16];  // in V's type: bfloat16 for bfloat16 pools, else binary16
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                ph[e] = pack2<BF>(v[2 * e], v[2 * e + 1]);
+                if constexpr (PSPLIT) {
+                  const float2 hv = unpack2<BF>(ph[e]);
+                  pl[e] = pack2<BF>(v[2 * e] - hv.x, v[2 * e + 1] - hv.y);
+                }
+              }
+              tmem_st16u(sbase + 32 * c, ph);
+              if constexpr (PSPLIT) tmem_st16u(sbase + 32 * c + 16, pl);
+            }
+            l += rs;
+            tmem_wait_st();
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (BLK) mbar_arrive(&ctl->sc_empty[se]);
+          mbar_arrive(&ctl->p_full[sb]);
+        }
+        if (first) {  // the next segment's queries, while this one runs
+          read_seg(j + 1, nxt);
+          if (ok && nxt.b1 > nxt.b0) next_scale = put_q(nxt, j + 1);
+        }
+        if (!ok) break;
+      }
+      // The segment's rows: the output, or a partial state.
+      float l0 = 0.f, l1 = 0.f;
+      if (active) exchange(l, l0, l1);
+      const float Ls = l0 + l1;
+      ok = __all_sync(kAll, ok && wait_or_abort(&ctl->o_full, j & 1, abort_flag, a.err));
+      if (ok && active) {
+        tc_fence_after();
+        const bool whole = cur.b0 == 0 && cur.b1 == cur.nblk;
+        const bool odd = *(volatile int*)&ctl->bad[j & 7] == j + 1;
+        const size_t prow = (size_t)(2 * blockIdx.x + (j > 0)) * kRows + r;
+        const float vs = BLK ? vref : 1.f;
+        const float inv = whole ? (Ls > 0.f ? (BLK ? vref : a.v_scale) / Ls : 0.f) : vs;
+        const size_t orow = ((size_t)qrow * a.Hq + (size_t)cur.h * a.G + hh) * D + DH * hf;
+#pragma unroll 1
+        for (int cc = 0; cc < DH / 32; ++cc) {
+          float o[32];
+          tmem_ld32(trow + kOCol + DH * hf + 32 * cc, o);
+          tmem_wait_ld();
+          if (r < rows) {
+            float sc = inv;
+            if (odd) {
+              float x[32];  // (a copy: o stays in registers where nothing is put back)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] = o[e] * inv;
+              sc = 1.f;
+              put_back<KIND, D>(a, cur, qrow, own, DH * hf + 32 * cc, x);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = x[e];
+            }
+            if (whole) store_row32<OUT>(a.out, orow + 32 * cc, o, sc);
+            else store_row32<PA_FP32>(a.ws_o, prow * D + DH * hf + 32 * cc, o, sc);
+          }
+        }
+        if (!whole && hf == 0 && r < rows) a.ws_ml[prow] = make_float2(m, Ls);
+      }
+      cur = nxt;
+    }
   }
-#pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    if (g >= a.G) break;
-    const float inv = m[g] == -INFINITY ? 0.f : 1.f / l[g];
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const size_t at = ((size_t)t * a.Hq + h * a.G + g) * (D / 2) + 32 * p + lane;
-      const float x = o[g][p].x * inv, y = o[g][p].y * inv;
-      if constexpr (F32) static_cast<float2*>(a.out)[at] = make_float2(x, y);
-      else static_cast<uint32_t*>(a.out)[at] = pack2<KV != PA_FP16>(x, y);
+
+  tc_fence_before();
+  __syncthreads();
+  grid_dependents_launch();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+// Joins the pieces of units that several CTAs shared: out = sum_i 2^(m_i - M) O_i / sum_i
+// 2^(m_i - M) l_i.  Piece i > 0 of CTA c's unit is the first segment of CTA c + i.  A warp
+// per row, all of a row's head dim in 16-byte loads.
+template <int D, int OUT>
+__global__ void __launch_bounds__(128) tree_merge_kernel(const TreeArgs a) {
+  grid_dependency_wait();
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  const int4 job = a.jobs[c0];
+  if (job.x < 0) return;
+  const SeqInfo info = seq_info(a, job.x);
+  if (info.tiles == 0) return;
+  const int h = job.y / info.tiles, tile = job.y - h * info.tiles;
+  const int rows = min(a.tile_nodes, info.n - tile * a.tile_nodes) * a.G;
+  const int pieces = job.z - c0 + 1;
+  constexpr int LPR = D / 4;        // lanes of a row
+  constexpr int RPW = 32 / LPR;     // rows of a warp
+  const int sub = lane / LPR, d4 = lane % LPR;
+  for (int r = (blockIdx.y * 4 + (threadIdx.x >> 5)) * RPW + sub; r < rows; r += gridDim.y * 4 * RPW) {
+    auto prow = [&](int i) { return (size_t)(i == 0 ? job.w : 2 * (c0 + i)) * kRows + r; };
+    float M = -INFINITY;
+    for (int i = 0; i < pieces; ++i) M = fmaxf(M, a.ws_ml[prow(i)].x);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float Ls = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < pieces; ++i) {
+      const float2 ml = a.ws_ml[prow(i)];
+      const float4 x = reinterpret_cast<const float4*>(a.ws_o)[prow(i) * (D / 4) + d4];
+      // a piece without any seen key holds zeros
+      const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : fast_exp2(ml.x - M);
+      if (w != 0.f) {
+        Ls += w * ml.y;
+        o.x += w * x.x;
+        o.y += w * x.y;
+        o.z += w * x.z;
+        o.w += w * x.w;
+      }
+    }
+    const float f = Ls > 0.f ? a.v_scale / Ls : Ls == 0.f ? 0.f : NAN;
+    const int node = r / a.G, hh = r - node * a.G;
+    const size_t at = ((size_t)(info.q0 + tile * a.tile_nodes + node) * a.Hq + (size_t)h * a.G + hh) * D + 4 * d4;
+    if constexpr (OUT == PA_FP32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+    } else {
+      constexpr bool BF = OUT == PA_BF16;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+          make_uint2(pack2<BF>(o.x * f, o.y * f), pack2<BF>(o.z * f, o.w * f));
     }
   }
 }
 
-typedef void (*TreeKernel)(TreeArgs);
+// ---------------------------------------------------------------- host side
+struct Build {
+  const void* fn;
+  int smem;
+  cudaError_t (*launch)(const TreeArgs&, const CUtensorMap*, const CUtensorMap*, cudaStream_t);
+  bool* configured;  // per device
+};
 
-template <int KV>
-TreeKernel pick_tree(int D, bool f32) {
-  if (D == 64) return f32 ? tree_kernel<KV, 64, true> : tree_kernel<KV, 64, false>;
-  return f32 ? tree_kernel<KV, 128, true> : tree_kernel<KV, 128, false>;
+template <int KIND, int D, int OUT, bool PSPLIT>
+struct Launch {
+  static cudaError_t go(const TreeArgs& a, const CUtensorMap* tk, const CUtensorMap* tv, cudaStream_t st) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<KIND, D>();
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_kernel<KIND, D, OUT, PSPLIT>, a, *tk, *tv);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(a.ctas, 8);
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, OUT>, a);
+  }
+  static Build get() {
+    static bool configured[128];
+    return {reinterpret_cast<const void*>(&tree_kernel<KIND, D, OUT, PSPLIT>), smem_bytes<KIND, D>(), &go, configured};
+  }
+};
+
+template <int D>
+Build pick(int kv_dtype, bool f32) {
+  switch (kv_dtype) {
+    case PA_FP8_E4M3:
+      return f32 ? Launch<K_E4M3, D, PA_FP32, true>::get() : Launch<K_E4M3, D, PA_BF16, false>::get();
+    case PA_FP8_E4M3_BLOCK:
+      return f32 ? Launch<K_E4M3B, D, PA_FP32, true>::get() : Launch<K_E4M3B, D, PA_BF16, false>::get();
+    case PA_BF16:  // 16-bit pools: P's low part too, or the weights would lose what the output can hold
+      return f32 ? Launch<K_BF16, D, PA_FP32, true>::get() : Launch<K_BF16, D, PA_BF16, true>::get();
+    default:
+      return f32 ? Launch<K_F16, D, PA_FP32, true>::get() : Launch<K_F16, D, PA_FP16, true>::get();
+  }
 }
 
-TreeKernel pick_tree(int kv, int D, bool f32) {
-  if (kv == PA_FP16) return pick_tree<PA_FP16>(D, f32);
-  return kv == PA_BF16 ? pick_tree<PA_BF16>(D, f32) : pick_tree<PA_FP8_E4M3>(D, f32);
+int sm_count(int* dev, int* sms) {
+  cudaError_t e = cudaGetDevice(dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+  if (e != cudaSuccess || *dev < 0 || *dev >= 128) return fail(PA_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
+  return PA_OK;
+}
+
+int configure(const Build& b, int dev) {
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!b.configured[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(b.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, b.smem);
+    if (e != cudaSuccess) return fail(PA_ERR_CUDA, "decode_tree configuration: %s", cudaGetErrorString(e));
+    b.configured[dev] = true;
+  }
+  return PA_OK;
+}
+
+// Bytes of the workspace's parts: partial O, (m, l), jobs.
+struct Workspace {
+  size_t ml, jobs, total;
+};
+
+Workspace layout(int ctas, int D) {
+  Workspace w;
+  w.ml = 2 * (size_t)ctas * kRows * D * 4;
+  w.jobs = w.ml + 2 * (size_t)ctas * kRows * 8;
+  w.total = w.jobs + (size_t)ctas * 16;
+  return w;
 }
 
 // What both calls check of a batch's trees.
@@ -150,6 +1079,9 @@ int check_tree(const pa_pool* pool, int n_q_heads, int max_nodes) {
 }
 
 }  // namespace
+
+int tree_set_wait_limit(unsigned long long ns) { return (int)set_pipe_wait_limit_here(ns); }
+
 }  // namespace pa
 
 using namespace pa;
@@ -157,10 +1089,12 @@ using namespace pa;
 extern "C" {
 
 int pa_decode_tree_workspace_bytes(const pa_pool* pool, int n_q_heads, int max_nodes, size_t* bytes) {
-  const int st = check_tree(pool, n_q_heads, max_nodes);
+  int st = check_tree(pool, n_q_heads, max_nodes);
   if (st) return st;
   if (!bytes) return fail(PA_ERR_INVALID, "null output");
-  *bytes = 16;
+  int dev = 0, sms = 0;
+  if ((st = sm_count(&dev, &sms))) return st;
+  *bytes = layout(sms, pool->desc.head_dim).total;
   return PA_OK;
 }
 
@@ -182,38 +1116,58 @@ int pa_decode_tree(pa_pool* pool, int layer, void* out, int out_dtype, const voi
   if ((uintptr_t)tree_mask_dev & 7u) return fail(PA_ERR_INVALID, "tree_mask must be 8-byte aligned");
   if (!workspace || ((uintptr_t)workspace & 15u))
     return fail(PA_ERR_INVALID, "a 16-byte aligned workspace is needed");
+  const pa_pool_desc& d = pool->desc;
+  const int D = d.head_dim;
+  int dev = 0, sms = 0;
+  if ((st = sm_count(&dev, &sms))) return st;
+  const Workspace ws = layout(sms, D);
+  if (workspace_bytes < ws.total)
+    return fail(PA_ERR_INVALID, "workspace of %zu bytes needed, %zu given", ws.total, workspace_bytes);
+  const Build b = D == 64 ? pick<64>(d.kv_dtype, out_dtype == PA_FP32) : pick<128>(d.kv_dtype, out_dtype == PA_FP32);
+  if ((st = configure(b, dev))) return st;
   unsigned int* err = device_error_word();
   if (!err) return PA_ERR_CUDA;
-  const pa_pool_desc& d = pool->desc;
+  const CUtensorMap *tk = nullptr, *tv = nullptr;
+  try {
+    st = D * pool->elem_bytes == 128 ? layer_maps(pool, layer, &tk, &tv) : layer_part_maps(pool, layer, &tk, &tv);
+  } catch (...) {  // (the pool's first use of a layer allocates its map on the host)
+    return fail(PA_ERR_NO_MEMORY, "host allocation failed");
+  }
+  if (st) return st;
   TreeArgs a = {};
   a.q = static_cast<const uint16_t*>(q);
   a.out = out;
   a.mask = tree_mask_dev;
-  a.q_start = q_start_dev;
-  a.tables = block_tables_dev;
-  a.ctx = ctx_lens_dev;
-  a.k = pool->k + (size_t)layer * pool->layer_bytes;
   a.v = pool->v + (size_t)layer * pool->layer_bytes;
   a.ksc = pool->block_scaled ? layer_scales(pool, pool->k, layer) : nullptr;
   a.vsc = pool->block_scaled ? layer_scales(pool, pool->v, layer) : nullptr;
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  a.ws_o = reinterpret_cast<float*>(base);
+  a.ws_ml = reinterpret_cast<float2*>(base + ws.ml);
+  a.jobs = reinterpret_cast<int4*>(base + ws.jobs);
   a.T = T;
-  a.S = S;
   a.Hq = n_q_heads;
   a.Hkv = d.n_kv_heads;
   a.G = n_q_heads / d.n_kv_heads;
-  a.max_blocks = max_blocks_per_seq;
-  a.num_blocks = d.num_blocks;
+  a.tile_nodes = kRows / a.G;
   a.max_nodes = max_nodes;
   a.words = (max_nodes + 63) / 64;
-  a.scale = softmax_scale;
-  a.k_scale = d.kv_dtype == PA_FP8_E4M3 ? d.k_scale : 1.f;
-  a.v_scale = d.kv_dtype == PA_FP8_E4M3 ? d.v_scale : 1.f;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = d.num_blocks;
+  a.ctas = sms;
+  const bool f8 = d.kv_dtype == PA_FP8_E4M3;
+  a.qk_scale_log2 = softmax_scale * 1.4426950408889634f * (f8 ? d.k_scale : 1.f);
+  a.v_scale = f8 ? d.v_scale : 1.f;
   a.err = err;
-  const long long ctas = ((long long)S * max_nodes * d.n_kv_heads + 3) / 4;
-  if (ctas > 0x7FFFFFFF) return fail(PA_ERR_UNSUPPORTED, "too many rows for one call");
-  pick_tree(d.kv_dtype, d.head_dim, out_dtype == PA_FP32)<<<(unsigned)ctas, 128, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(PA_ERR_CUDA, "decode_tree launch: %s", cudaGetErrorString(e));
+  // one schedule holds at most kBalancedMaxSeqs sequences: larger batches in turn
+  for (int s = 0; s < S; s += kBalancedMaxSeqs) {
+    a.S = std::min(S - s, kBalancedMaxSeqs);
+    a.q_start = q_start_dev + s;
+    a.tables = block_tables_dev + (size_t)s * max_blocks_per_seq;
+    a.ctx = ctx_lens_dev + s;
+    const cudaError_t e = b.launch(a, tk, tv, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(PA_ERR_CUDA, "decode_tree launch: %s", cudaGetErrorString(e));
+  }
   return PA_OK;
 }
 

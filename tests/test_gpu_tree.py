@@ -149,9 +149,13 @@ def _bad(b, **kw):
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
 def test_bad_sequences_are_skipped(kv):
-    """A sequence whose lengths do not fit is reported and skipped; the others are computed."""
+    """A sequence whose lengths do not fit is reported and skipped; the others are computed.
+    (A batch of other lengths is cut into other pieces, whose fp32 sums are joined in another
+    order: the rows are held to fp64, not to the bits of the whole batch's call.)"""
     b = Batch(kv, 2, 4, 128, [200, 77, 300], [13, 20, 5], seed=9, mask="chain")
-    want = b.run()
+    b.check(b.run())
+    y, tol = b.exact()
+    near = lambda got, r: bool(((got[r].double() - y[r]).abs() <= tol[r]).all())  # noqa: E731
     assert b.pool.device_error() == N.PA_OK
     i32 = dict(dtype=torch.int32, device="cuda")
     rows = [slice(0, 13), slice(13, 33), slice(33, 38)]
@@ -169,13 +173,13 @@ def test_bad_sequences_are_skipped(kv):
             if s in skipped:
                 assert bool((out[rows[s]] == 7.0).all()), (kw, s)
             else:
-                assert torch.equal(out[rows[s]], want[rows[s]]), (kw, s)
+                assert near(out, rows[s]), (kw, s)
     # a page outside the pool: reported, and the other sequences hold
     for page in (-1, b.pool.num_blocks, 2 ** 31 - 1):
         t = b.tables.clone()
         t[1, 2] = page
         out = _bad(b, tables=t)
-        assert torch.equal(out[rows[0]], want[rows[0]]) and torch.equal(out[rows[2]], want[rows[2]])
+        assert near(out, rows[0]) and near(out, rows[2])
     b.pool.close()
 
 
