@@ -32,10 +32,11 @@ struct pa_pool {
   // encoded on first use by pa_decode.
   std::vector<pa_tmap_blob> tmaps;
   std::vector<char> tmap_ready;  // per layer
-  // maps of the tensor-core kernels where a row is not 128 bytes (layer_part_maps),
+  // maps of the tensor-core kernels where a row is not 128 bytes: 16-bit pools, whose box is
+  // one 64-element half of each row (layer_half_maps), and 64-byte rows (pa_tree.cu);
   // encoded on first use the same way
-  std::vector<pa_tmap_blob> tmaps_part;
-  std::vector<char> tmap_part_ready;
+  std::vector<pa_tmap_blob> tmaps_half;
+  std::vector<char> tmap_half_ready;
   // Prefix cache: chain hash of a full block -> the block holding its K/V.
   // The cache owns one reference to each block it maps.
   struct prefix_entry {
@@ -81,16 +82,15 @@ namespace pa {
 // first use and kept in the pool; rows of one token of one kv head, a box is
 // one 16-token tile, 128-byte swizzled when a row is 128 or 256 bytes.
 int layer_maps(pa_pool* pool, int layer, const CUtensorMap_st** tk, const CUtensorMap_st** tv);
-// The same regions for the tensor cores' operand layouts: rows of 256 bytes with a 128-byte box, so
-// one page is loaded as two 64-element halves (x = 0 and x = 128 bytes), or rows of 64
-// bytes, 64-byte swizzled.
-int layer_part_maps(pa_pool* pool, int layer, const CUtensorMap_st** tk, const CUtensorMap_st** tv);
+// The same regions for 16-bit pools as rows of 256 bytes with a 128-byte box,
+// so one page is loaded as two 64-element halves (x = 0 and x = 128 bytes).
+int layer_half_maps(pa_pool* pool, int layer, const CUtensorMap_st** tk, const CUtensorMap_st** tv);
 
 // Set the pipeline wait limit of each translation unit's kernels (see
 // pa_set_pipeline_wait_limit_ns); they return a cudaError_t value.
 int decode_set_wait_limit(unsigned long long ns);
 int prefill_set_wait_limit(unsigned long long ns);
-int prefill_tc_set_wait_limit(unsigned long long ns);
+int prefill_tc_set_wait_limit(unsigned long long ns);  // and the tree's
 int weights_set_wait_limit(unsigned long long ns);
 int tree_set_wait_limit(unsigned long long ns);
 

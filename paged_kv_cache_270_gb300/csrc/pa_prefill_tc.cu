@@ -813,7 +813,7 @@ int prefill_tc(pa_pool* pool, int layer, void* out, int out_dtype, const void* q
   const pa_pool_desc& d = pool->desc;
   const bool f8 = d.kv_dtype == PA_FP8_E4M3 || d.kv_dtype == PA_FP8_E4M3_BLOCK;
   const CUtensorMap_st *tk = nullptr, *tv = nullptr;
-  int rc = f8 ? layer_maps(pool, layer, &tk, &tv) : layer_part_maps(pool, layer, &tk, &tv);
+  int rc = f8 ? layer_maps(pool, layer, &tk, &tv) : layer_half_maps(pool, layer, &tk, &tv);
   if (rc) return rc;
   TcArgs a;
   a.q = static_cast<const uint16_t*>(q);
@@ -859,6 +859,9 @@ int prefill_tc(pa_pool* pool, int layer, void* out, int out_dtype, const void* q
   return PA_OK;
 }
 
-int prefill_tc_set_wait_limit(unsigned long long ns) { return (int)set_pipe_wait_limit_here(ns); }
+int prefill_tc_set_wait_limit(unsigned long long ns) {
+  const int e = (int)set_pipe_wait_limit_here(ns);
+  return e ? e : tree_set_wait_limit(ns);
+}
 
 }  // namespace pa

@@ -38,7 +38,11 @@ namespace {
 using namespace tc;
 
 constexpr int kRows = 128;     // MMA rows of a tile: nodes x the G heads of a kv head
-constexpr int kThreads = 448;  // 14 warps: producer, MMA, 4 for V, 8 softmax
+// 16 warps, four on each scheduler: 0 copies, 1 issues MMAs, 4-11 softmax; 2, 3, 14 and 15 take V
+// (off the scheduler of the MMA warp, whose serial chain of instructions sets the pace), 12-15 the
+// queries and masks of the segment ahead (a warp reaches the 32 tensor-memory lanes of its
+// number modulo 4).
+constexpr int kThreads = 512;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr uint32_t kTmemCols = 512;
 // TMEM columns (one lane per row): S in buffers of 128 at 0 and 128 by block parity, overwritten by
@@ -46,10 +50,15 @@ constexpr uint32_t kTmemCols = 512;
 // pools: the two E4M3 terms 32 columns apart).
 constexpr uint32_t kOCol = 256, kQCol = 384;
 constexpr int kScaleRing = 8;  // block-scaled pools: blocks whose scales are held
-constexpr int kSegRing = 4;    // segments whose descriptions are held
+// Segments whose descriptions are held.  The copying warp hands out number c + 3 before it
+// issues the copies of segment c, and the MMA warp gives up number s only once it has issued
+// Q K^T of a block behind s, so c + 3 - kSegRing must lie two segments before c.
+constexpr int kSegRing = 8;
+constexpr int kRowRing = 4;  // segments whose masks and score factors are held
 // The largest weight is kept near 2^7 and below 2^15, so that small ones stay normal
 // binary16 numbers; the reference point moves when the maximum has grown by 2^8.
 constexpr float kTop = 7.f, kGrow = 15.f;
+constexpr float kMinFactor = 1.17549435e-38f;  // the smallest normal number
 
 enum Kind { K_E4M3 = 0, K_E4M3B = 1, K_BF16 = 2, K_F16 = 3 };
 
@@ -82,8 +91,10 @@ struct Ctrl {
   uint64_t seg_full[kSegRing], seg_empty[kSegRing];
   uint64_t kv_full[4], kv_empty[4], s_full[2], p_full[2], vt_full[2], vt_empty[2];
   uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
-  uint64_t q_ready[2], o_full, drain, xchg[4];
+  uint64_t q_ready[2], q_free[2], row_free[kRowRing], o_full, drain, xchg[4];
   uint64_t tail_ready[2], tail_done[2];  // 16-bit pools: blocks that reach the tree, by their parity
+  uint64_t mask[kRowRing][128][PA_TREE_MAX_NODES / 64];  // a tile's nodes' mask words
+  float row_scale[kRowRing][128];        // each row's score factor
   float2 sc[kScaleRing][8];              // block-scaled pools: (K scale, V scale) of each page of a block
   float xbuf[2][128][2];                 // the two half-row threads' partials
   long long warp_sums[kThreads / 32];
@@ -121,25 +132,34 @@ struct TreeArgs {
   unsigned int* err;
 };
 
-// A sequence's place in the schedule.
+// A sequence's place in the schedule, from its lengths (loaded apart, so that the loads of the next
+// one can be under way).
+struct SeqRaw {
+  int q0, q1, ctx;
+};
+
+__device__ __forceinline__ SeqRaw seq_raw(const TreeArgs& a, int s) {
+  return s < a.S ? SeqRaw{a.q_start[s], a.q_start[s + 1], a.ctx[s]} : SeqRaw{0, 0, 0};
+}
+
 struct SeqInfo {
   int q0, n, ctx, tiles, nblk;
   bool bad;
   __device__ long long units(int Hkv) const { return (long long)tiles * Hkv; }
 };
 
-__device__ __forceinline__ SeqInfo seq_info(const TreeArgs& a, int s) {
+__device__ __forceinline__ SeqInfo seq_info(const TreeArgs& a, const SeqRaw& r) {
   SeqInfo i;
-  i.q0 = a.q_start[s];
-  const long long q1 = a.q_start[s + 1], n = q1 - i.q0;
+  i.q0 = r.q0;
+  const long long n = (long long)r.q1 - r.q0;
   i.n = i.ctx = i.tiles = i.nblk = 0;
   i.bad = false;
   if (n == 0) return i;
-  i.ctx = a.ctx[s];
-  if (i.q0 < 0 || n < 0 || q1 > a.T || n > a.max_nodes || i.ctx < n || i.ctx > 16 * a.max_blocks) {
+  if (r.q0 < 0 || n < 0 || r.q1 > a.T || n > a.max_nodes || r.ctx < n || r.ctx > 16 * a.max_blocks) {
     i.bad = true;
     return i;
   }
+  i.ctx = r.ctx;
   i.n = (int)n;
   i.tiles = (i.n + a.tile_nodes - 1) / a.tile_nodes;
   i.nblk = (i.ctx + 127) >> 7;
@@ -147,19 +167,19 @@ __device__ __forceinline__ SeqInfo seq_info(const TreeArgs& a, int s) {
 }
 
 // The mask of a row over the 64 nodes from j0 on (bits of nodes below 0, history, are set).
-__device__ __forceinline__ uint64_t sees64(const TreeArgs& a, long long row, int own, int n, int j0) {
+// w: its words (nullptr: a chain, whose node `own` sees those up to itself).
+__device__ __forceinline__ uint64_t sees64(const uint64_t* w, int words, int own, int n, int j0) {
   if (j0 <= -64) return ~0ull;
-  if (!a.mask) {
+  if (!w) {
     const int last = own - j0;  // the last bit set
     return last < 0 ? 0ull : last >= 63 ? ~0ull : (2ull << last) - 1;
   }
-  const uint64_t* w = a.mask + row * a.words;
   uint64_t v;
   if (j0 < 0) {
     v = (w[0] << -j0) | ((1ull << -j0) - 1);
   } else {
     const int i = j0 >> 6, sh = j0 & 63;
-    const uint64_t lo = i < a.words ? w[i] : 0, hi = i + 1 < a.words ? w[i + 1] : 0;
+    const uint64_t lo = i < words ? w[i] : 0, hi = i + 1 < words ? w[i + 1] : 0;
     v = sh ? (lo >> sh) | (hi << (64 - sh)) : lo;
   }
   const int valid = n - j0;
@@ -227,8 +247,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSegRing; ++i) {
       mbar_init(&ctl->seg_full[i], 1);
-      mbar_init(&ctl->seg_empty[i], 13);  // MMA, 4 warps for V, 8 softmax
+      mbar_init(&ctl->seg_empty[i], 15);  // MMA, 6 warps for V and queries, 8 softmax
     }
+    for (int i = 0; i < kRowRing; ++i) mbar_init(&ctl->row_free[i], 8);
     for (int i = 0; i < R; ++i) {
       mbar_init(&ctl->kv_full[i], 1);
       mbar_init(&ctl->kv_empty[i], F8 ? 5 : 1);  // FP8: the Q K MMAs and four warps; 16-bit: the P V MMAs
@@ -238,7 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       mbar_init(&ctl->p_full[i], 8);
       mbar_init(&ctl->vt_full[i], 4);
       mbar_init(&ctl->vt_empty[i], 1);
-      mbar_init(&ctl->q_ready[i], 8);
+      mbar_init(&ctl->q_ready[i], 4);
+      mbar_init(&ctl->q_free[i], 1);
       mbar_init(&ctl->tail_ready[i], 1);
       mbar_init(&ctl->tail_done[i], 4);
     }
@@ -273,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
   const int s0 = min(a.S, (int)threadIdx.x * per), s1 = min(a.S, s0 + per);
   long long mine = 0;
   for (int s = s0; s < s1; ++s) {
-    const SeqInfo i = seq_info(a, s);
+    const SeqInfo i = seq_info(a, seq_raw(a, s));
     if (i.bad) record_error(a.err, PA_ERR_BOUNDS);
     mine += i.units(a.Hkv) * (i.nblk + kUnit);
   }
@@ -299,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
   if (pos0 < total && before <= pos0 && pos0 < before + mine) {
     long long cum = before;
     for (int s = s0; s < s1; ++s) {
-      const SeqInfo i = seq_info(a, s);
+      const SeqInfo i = seq_info(a, seq_raw(a, s));
       const long long c = i.units(a.Hkv) * (i.nblk + kUnit);
       if (pos0 < cum + c) {
         ctl->start_seq = s;
@@ -321,7 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
     // ---------------------------------------------------------- schedule and TMA producer
     const uint64_t policy = l2_evict_first_policy();
     int seq = ctl->start_seq;
-    SeqInfo info = seq_info(a, seq);
+    SeqInfo info = seq_info(a, seq_raw(a, seq));
+    SeqRaw ahead = seq_raw(a, seq + 1);
     int span = info.nblk + kUnit;
     long long u = ctl->start_off / span;
     int v = (int)(ctl->start_off - u * span);
@@ -333,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       while (pos < pos_end) {
         while (u >= info.units(a.Hkv)) {
           if (++seq >= a.S) break;
-          info = seq_info(a, seq);
+          info = seq_info(a, ahead);
+          ahead = seq_raw(a, seq + 1);
           span = info.nblk + kUnit;
           u = 0;
           v = 0;
@@ -376,58 +400,78 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       if (!ok) sg.b1 = sg.b0;
       return sg;
     };
-    Seg cur = produce(), nxt = {};
-    if (cur.b1 > cur.b0) nxt = produce();
+    // Batches of up to four blocks of a segment: the table entries of a batch are loaded two
+    // batches ahead (lane i: page i), its tile scales one ahead, for while the copies keep HBM
+    // busy such a load takes some microseconds.
+    struct Batch {
+      int seq, h, b, nb, page_end, raw;
+    };
+    // A segment's description is handed out before the first copies of the one in front of it, as the
+    // queries' warps look one segment ahead.
+    Seg front = {}, behind = produce();
+    int fb = 0;  // the next batch's first block, in the front segment
+    bool more = true;
+    auto fetch = [&]() -> Batch {
+      Batch x = {0, 0, 0, 0, 0, 0};
+      if (more && fb == front.b1) {
+        front = behind;
+        fb = front.b0;
+        more = front.b1 > front.b0;
+        if (more) behind = produce();
+      }
+      if (!more) return x;
+      x.seq = front.seq;
+      x.h = front.h;
+      x.b = fb;
+      x.nb = min(4, front.b1 - fb);
+      x.page_end = min(8 * (fb + x.nb), (front.base + front.n + 15) >> 4);
+      fb += x.nb;
+      const int page = 8 * x.b + lane;
+      if (page < x.page_end) x.raw = a.tables[(size_t)x.seq * a.max_blocks + page];
+      return x;
+    };
+    float sk = 1.f, sv = 0.f;
+    auto scales = [&](Batch& x) {  // checks the entries; block-scaled pools: loads their scales
+      const bool live = 8 * x.b + lane < x.page_end;
+      if (live && (x.raw < 0 || x.raw >= a.num_blocks)) {
+        record_error(a.err, PA_ERR_BOUNDS);
+        x.raw = 0;
+      }
+      if constexpr (BLK) {
+        sk = 1.f;
+        sv = 0.f;
+        if (live) {
+          sk = a.ksc[(size_t)x.raw * a.Hkv + x.h];
+          sv = a.vsc[(size_t)x.raw * a.Hkv + x.h];
+        }
+      }
+    };
+    Batch cur = fetch(), nxt = fetch();
+    scales(cur);
     int g = 0;  // blocks issued
-    while (ok && cur.b1 > cur.b0) {
-      const int32_t* trow = a.tables + (size_t)cur.seq * a.max_blocks;
-      const int page_end = min(8 * cur.b1, (cur.base + cur.n + 15) >> 4);
-      // lane i holds the entry (and tile scales) of page i of a batch of four blocks; the
-      // next batch's entries are loaded one batch ahead
-      auto entry = [&](int page) { return page < page_end ? trow[page] : 0; };
-      int phys = 0, next = entry(8 * cur.b0 + 32 + lane);
-      float sk = 1.f, sv = 0.f;
-      auto take = [&](int raw, int page) {
-        phys = raw;
-        if (page < page_end && (raw < 0 || raw >= a.num_blocks)) {
-          record_error(a.err, PA_ERR_BOUNDS);
-          phys = 0;
-        }
-        if constexpr (BLK) {
-          sk = 1.f;
-          sv = 0.f;
-          if (page < page_end) {
-            sk = a.ksc[(size_t)phys * a.Hkv + cur.h];
-            sv = a.vsc[(size_t)phys * a.Hkv + cur.h];
-            // a tile without a finite scale holds NaN: marked by -1
-            if (!(fabsf(sk) < INFINITY)) sk = -1.f;
-            if (!(fabsf(sv) < INFINITY)) sv = -1.f;
-          }
-        }
-      };
-      take(entry(8 * cur.b0 + lane), 8 * cur.b0 + lane);
-      for (int b = cur.b0; b < cur.b1; ++b, ++g) {
-        const int slot = g % R, j = b - cur.b0, pb = 8 * (j & 3);
-        if (j > 0 && pb == 0) {
-          take(next, 8 * b + lane);
-          next = entry(8 * b + 32 + lane);
-        }
+    while (ok && cur.nb > 0) {
+      const Batch far = fetch();
+      // a tile without a finite scale holds NaN: marked by -1
+      const float csk = fabsf(sk) < INFINITY ? sk : -1.f, csv = fabsf(sv) < INFINITY ? sv : -1.f;
+      scales(nxt);
+      for (int j = 0; j < cur.nb; ++j, ++g) {
+        const int slot = g % R, pb = 8 * j, b = cur.b + j;
         if (g >= R) ok = __all_sync(kAll, wait_or_abort(&ctl->kv_empty[slot], ((g / R) - 1) & 1, abort_flag, a.err));
         if (!ok) break;
-        const int cnt = min(8, page_end - 8 * b);
+        const int cnt = min(8, cur.page_end - 8 * b);
         if constexpr (BLK) {
           const int e = g % kScaleRing;
           if (g >= kScaleRing)
             ok = __all_sync(kAll, wait_or_abort(&ctl->sc_empty[e], ((g / kScaleRing) - 1) & 1, abort_flag, a.err));
           if (!ok) break;
-          if (lane >= pb && lane < pb + 8) ctl->sc[e][lane - pb] = make_float2(sk, sv);
+          if (lane >= pb && lane < pb + 8) ctl->sc[e][lane - pb] = make_float2(csk, csv);
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->sc_full[e]);
         }
         if (lane == 0) mbar_arrive_expect_tx(&ctl->kv_full[slot], (uint32_t)cnt * 32u * L::kRow);
         const int i = lane - pb;  // this lane's page of the block
         if (i >= 0 && i < cnt) {
-          const int row0 = (phys * a.Hkv + cur.h) * 16;
+          const int row0 = (cur.raw * a.Hkv + cur.h) * 16;
           uint8_t* kd = sm + slot * L::kSlot + i * 16 * L::kPart;
           uint8_t* vd = kd + R * L::kSlot;
 #pragma unroll
@@ -439,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       }
       if (!ok) break;
       cur = nxt;
-      if (cur.b1 > cur.b0) nxt = produce();
+      nxt = far;
     }
     // no copy may still target shared memory when the CTA exits
     if (lane == 0)
@@ -498,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
         mma_commit(&ctl->s_full[sb]);
         if constexpr (F8) mma_commit(&ctl->kv_empty[slot]);
         ++gq;
-        ++bq;
+        if (++bq == bq1) mma_commit(&ctl->q_free[jq & 1]);  // the segment's queries are read
         return true;
       };
       run = issue_qk() && issue_qk();
@@ -543,56 +587,157 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
     }
     __syncwarp();
   } else if (warp < 4 || warp >= 12) {
-    // ---------------------------------------------------------- V
-    const int ct = 32 * (warp < 4 ? warp - 2 : warp - 10) + lane;  // 0 .. 127
-    int g = 0, t = 0;
+    // ---------------------------------------------------------- V, queries and masks
+    const bool has_v = warp < 4 || warp >= 14, has_q = warp >= 12;
+    const int ct = 32 * (warp < 4 ? warp - 2 : warp - 12) + lane;  // 0 .. 127 among those that take V
+    const int qr = 32 * (warp & 3) + lane;                          // this lane's row
+    constexpr int QW = D / 2;                                       // 32-bit words of a query
+    uint32_t qw[QW];
+    uint64_t mw[PA_TREE_MAX_NODES / 64];
     bool ok = true;
-    for (int j = 0; ok; ++j) {
+    // The queries and masks of segment j, loaded in one piece of the work and stored in another, so that
+    // nothing waits for the loads.
+    auto load_rows = [&](const Seg& sg) {
+      const int nodes = min(a.tile_nodes, sg.n - sg.tile * a.tile_nodes), rows = nodes * a.G;
+      const int tl = qr / a.G, hh = qr - tl * a.G;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.q + ((size_t)(sg.q0 + sg.tile * a.tile_nodes + tl) * a.Hq + (size_t)sg.h * a.G + hh) * D);
+#pragma unroll
+      for (int c = 0; c < QW / 4; ++c) {
+        const uint4 x = qr < rows ? src[c] : make_uint4(0, 0, 0, 0);
+        qw[4 * c] = x.x;
+        qw[4 * c + 1] = x.y;
+        qw[4 * c + 2] = x.z;
+        qw[4 * c + 3] = x.w;
+      }
+      if (a.mask) {
+#pragma unroll
+        for (int w = 0; w < PA_TREE_MAX_NODES / 64; ++w) {
+          mw[w] = 0;
+          if (qr < nodes && w < a.words)
+            mw[w] = a.mask[(size_t)(sg.q0 + sg.tile * a.tile_nodes + qr) * a.words + w];
+        }
+      }
+    };
+    auto store_rows = [&](int j) {
+      // segment j - 2's queries are read, and the rows of segment j - kRowRing are done
+      if (j >= 2) ok = __all_sync(kAll, ok && wait_or_abort(&ctl->q_free[j & 1], ((j >> 1) - 1) & 1, abort_flag, a.err));
+      if (j >= kRowRing)
+        ok = __all_sync(kAll, ok && wait_or_abort(&ctl->row_free[j % kRowRing], ((j / kRowRing) - 1) & 1, abort_flag, a.err));
+      if (!ok) return;
+      tc_fence_after();
+      if (a.mask) {
+#pragma unroll
+        for (int w = 0; w < PA_TREE_MAX_NODES / 64; ++w) ctl->mask[j % kRowRing][qr][w] = mw[w];
+      }
+      const uint32_t qcol = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kQCol + 64 * (j & 1);
+      float row_scale = fabsf(a.qk_scale_log2);
+      if constexpr (!F8) {
+        if (a.qk_scale_log2 < 0.f) {  // a negative scale flips the queries' signs
+#pragma unroll
+          for (int w = 0; w < QW; ++w) qw[w] ^= 0x80008000u;
+        }
+#pragma unroll
+        for (int w = 0; w < QW; w += 32) tmem_st32u(qcol + w, qw + w);
+      } else {
+        // scaled by a power of two (the largest |q| in [128, 256)) and split into two E4M3 terms
+        float amax = 0.f;
+#pragma unroll
+        for (int w = 0; w < QW; ++w)
+          amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_float(qw[w] & 0xFFFFu)), fabsf(bf16_bits_to_float(qw[w] >> 16))));
+        int ex = 0;
+        if (amax > 0.f) frexpf(amax, &ex);
+        const float sgn = a.qk_scale_log2 < 0.f ? -1.f : 1.f;
+        const float qs = sgn * (amax > 0.f ? ldexpf(1.f, 8 - ex) : 1.f);
+        row_scale *= amax > 0.f ? ldexpf(1.f, ex - 8) : 1.f;
+#pragma unroll
+        for (int part = 0; part < QW / 32; ++part) {
+          uint32_t qhi[16], qlo[16];  // 4 dims per word
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const uint32_t w0 = qw[32 * part + 2 * c], w1 = qw[32 * part + 2 * c + 1];
+            const float2 x01 = make_float2(bf16_bits_to_float(w0 & 0xFFFFu) * qs, bf16_bits_to_float(w0 >> 16) * qs);
+            const float2 x23 = make_float2(bf16_bits_to_float(w1 & 0xFFFFu) * qs, bf16_bits_to_float(w1 >> 16) * qs);
+            const uint32_t h01 = __nv_cvt_float2_to_fp8x2(x01, __NV_SATFINITE, __NV_E4M3);
+            const uint32_t h23 = __nv_cvt_float2_to_fp8x2(x23, __NV_SATFINITE, __NV_E4M3);
+            const float2 d01 = unpack2<false>(e4m3x2_to_f16x2(h01));
+            const float2 d23 = unpack2<false>(e4m3x2_to_f16x2(h23));
+            const uint32_t l01 = __nv_cvt_float2_to_fp8x2(make_float2(x01.x - d01.x, x01.y - d01.y), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t l23 = __nv_cvt_float2_to_fp8x2(make_float2(x23.x - d23.x, x23.y - d23.y), __NV_SATFINITE, __NV_E4M3);
+            qhi[c] = (h01 & 0xFFFFu) | (h23 << 16);
+            qlo[c] = (l01 & 0xFFFFu) | (l23 << 16);
+          }
+          tmem_st16u(qcol + 16 * part, qhi);
+          tmem_st16u(qcol + 32 + 16 * part, qlo);
+        }
+      }
+      // (a zero factor would turn a masked -inf into NaN)
+      ctl->row_scale[j % kRowRing][qr] = fmaxf(row_scale, kMinFactor);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->q_ready[j & 1]);
+    };
+    auto read_seg = [&](int j, Seg& sg) {
       const int e = j % kSegRing;
-      ok = __all_sync(kAll, wait_or_abort(&ctl->seg_full[e], (j / kSegRing) & 1, abort_flag, a.err));
-      if (!ok) break;
-      const int b0 = ctl->seg[e].b0, b1 = ctl->seg[e].b1, base = ctl->seg[e].base, ctx = base + ctl->seg[e].n;
+      ok = __all_sync(kAll, ok && wait_or_abort(&ctl->seg_full[e], (j / kSegRing) & 1, abort_flag, a.err));
+      sg = {};
+      if (ok) sg = ctl->seg[e];
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->seg_empty[e]);
-      if (b0 == b1) break;
-      for (int b = b0; b < b1; ++b, ++g) {
+    };
+    Seg sg, ahead;
+    read_seg(0, sg);
+    if (has_q && ok && sg.b1 > sg.b0) {
+      load_rows(sg);
+      store_rows(0);
+    }
+    int g = 0, t = 0;
+    for (int j = 0; ok && sg.b1 > sg.b0; ++j) {
+      read_seg(j + 1, ahead);
+      const bool rows_ahead = has_q && ok && ahead.b1 > ahead.b0;
+      if (rows_ahead) load_rows(ahead);
+      const int ctx = sg.base + sg.n;
+      for (int b = sg.b0; b < sg.b1; ++b, ++g) {
         const int slot = g % R;
         const int nvalid = min(128, ctx - 128 * b);  // keys behind the context: zero
-        const int nplain = base - 128 * b;           // keys from here on are nodes
+        const int nplain = sg.base - 128 * b;        // keys from here on are nodes
         bool odd = false;                            // infinities or NaN among them
         if constexpr (F8) {
-          const int half = g & 1;
-          ok = __all_sync(kAll, wait_or_abort(&ctl->kv_full[slot], (g / R) & 1, abort_flag, a.err));
-          if (ok && g >= 2) ok = __all_sync(kAll, wait_or_abort(&ctl->vt_empty[half], ((g >> 1) - 1) & 1, abort_flag, a.err));
-          if (!ok) break;
-          const uint8_t* vr = sm + (R + slot) * L::kSlot;
-          uint8_t* vt = sm + L::kVT + half * L::kVTBlock;
-          // consecutive lanes take consecutive keys of one 16-byte chunk
+          if (has_v) {
+            const int half = g & 1;
+            ok = __all_sync(kAll, wait_or_abort(&ctl->kv_full[slot], (g / R) & 1, abort_flag, a.err));
+            if (ok && g >= 2) ok = __all_sync(kAll, wait_or_abort(&ctl->vt_empty[half], ((g >> 1) - 1) & 1, abort_flag, a.err));
+            if (!ok) break;
+            const uint8_t* vr = sm + (R + slot) * L::kSlot;
+            uint8_t* vt = sm + L::kVT + half * L::kVTBlock;
+            // consecutive lanes take consecutive keys of one 16-byte chunk
 #pragma unroll 4
-          for (int it = 0; it < D / 16; ++it) {
-            const int key = ct, ch = it;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            // a row's chunks are permuted by its line's place: 128-byte lines, or 64-byte rows two to a line
-            const uint32_t off = L::kPart == 64 ? key * 64 + ((ch ^ ((key >> 1) & 3)) << 4) : key * 128 + ((ch ^ (key & 7)) << 4);
-            if (key < nvalid) w = lds128(vr + off);
-            if (nplain < 128 && key >= nplain) odd |= take_out<KIND>(w);
-            const uint32_t cw[4] = {w.x, w.y, w.z, w.w};
-            uint32_t hv[8];
+            for (int ch = 0; ch < D / 16; ++ch) {
+              const int key = ct;
+              uint4 w = make_uint4(0, 0, 0, 0);
+              // a row's chunks are permuted by its line's place: 128-byte lines, or 64-byte rows two to a line
+              const uint32_t off = L::kPart == 64 ? key * 64 + ((ch ^ ((key >> 1) & 3)) << 4) : key * 128 + ((ch ^ (key & 7)) << 4);
+              if (key < nvalid) w = lds128(vr + off);
+              if (nplain < 128 && key >= nplain) odd |= take_out<KIND>(w);
+              const uint32_t cw[4] = {w.x, w.y, w.z, w.w};
+              uint32_t hv[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) e4m3x4_to_f16x2x2(cw[q], hv[2 * q], hv[2 * q + 1]);
-            uint8_t* row = vt + (ch >> 2) * 16384 + key * 128;
-            const int c0 = (ch & 3) * 2;
-            *reinterpret_cast<uint4*>(row + ((c0 ^ (key & 7)) << 4)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-            *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (key & 7)) << 4)) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
+              for (int q = 0; q < 4; ++q) e4m3x4_to_f16x2x2(cw[q], hv[2 * q], hv[2 * q + 1]);
+              uint8_t* row = vt + (ch >> 2) * 16384 + key * 128;
+              const int c0 = (ch & 3) * 2;
+              *reinterpret_cast<uint4*>(row + ((c0 ^ (key & 7)) << 4)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+              *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (key & 7)) << 4)) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
+            }
+            if (odd) ctl->bad[j & 7] = j + 1;
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&ctl->vt_full[half]);
+              mbar_arrive(&ctl->kv_empty[slot]);
+            }
           }
-          if (odd) ctl->bad[j & 7] = j + 1;
-          fence_proxy_async_shared();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&ctl->vt_full[half]);
-            mbar_arrive(&ctl->kv_empty[slot]);
-          }
-        } else if (nplain < 128) {
+        } else if (has_v && nplain < 128) {
           // read in place: rows behind the context are zeroed, nodes' rows looked through
           ok = __all_sync(kAll, wait_or_abort(&ctl->tail_ready[t & 1], (t >> 1) & 1, abort_flag, a.err));
           ok = ok && __all_sync(kAll, wait_or_abort(&ctl->kv_full[slot], (g / R) & 1, abort_flag, a.err));
@@ -619,7 +764,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
           if (lane == 0) mbar_arrive(&ctl->tail_done[t & 1]);
           ++t;
         }
+        if (rows_ahead && b == sg.b0) store_rows(j + 1);
+        if (!ok) break;
       }
+      sg = ahead;
     }
   } else {
     // ---------------------------------------------------------- softmax rows
@@ -642,7 +790,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       hi_half = ctl->xbuf[xk & 1][r][1];
       ++xk;
     };
-    constexpr float kMinFactor = 1.17549435e-38f;  // a zero factor would turn a masked -inf into NaN
     auto read_seg = [&](int j, Seg& sg) {
       const int e = j % kSegRing;
       ok = __all_sync(kAll, ok && wait_or_abort(&ctl->seg_full[e], (j / kSegRing) & 1, abort_flag, a.err));
@@ -651,87 +798,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->seg_empty[e]);
     };
-    auto tile_rows = [&](const Seg& sg) { return min(a.tile_nodes, sg.n - sg.tile * a.tile_nodes) * a.G; };
-    // Puts a segment's queries into tensor memory; returns the row's score factor.
-    auto put_q = [&](const Seg& sg, int j) -> float {
-      float row_scale = fabsf(a.qk_scale_log2);
-      const int rows = tile_rows(sg);
-      if (quad * 32 < rows) {
-        constexpr int QW = DH / 2;  // 32-bit words of this half
-        uint32_t qw[QW];
-        const uint4* src = reinterpret_cast<const uint4*>(
-            a.q + ((size_t)(sg.q0 + sg.tile * a.tile_nodes + tl) * a.Hq + (size_t)sg.h * a.G + hh) * D + DH * hf);
-#pragma unroll
-        for (int c = 0; c < QW / 4; ++c) {
-          const uint4 x = r < rows ? src[c] : make_uint4(0, 0, 0, 0);
-          qw[4 * c] = x.x;
-          qw[4 * c + 1] = x.y;
-          qw[4 * c + 2] = x.z;
-          qw[4 * c + 3] = x.w;
-        }
-        const uint32_t qcol = trow + kQCol + 64 * (j & 1);
-        if constexpr (!F8) {
-          if (a.qk_scale_log2 < 0.f) {  // a negative scale flips the queries' signs
-#pragma unroll
-            for (int w = 0; w < QW; ++w) qw[w] ^= 0x80008000u;
-          }
-          if constexpr (QW == 32) tmem_st32u(qcol + 32 * hf, qw);
-          else tmem_st16u(qcol + 16 * hf, qw);
-        } else {
-          float am = 0.f;
-#pragma unroll
-          for (int w = 0; w < QW; ++w)
-            am = fmaxf(am, fmaxf(fabsf(bf16_bits_to_float(qw[w] & 0xFFFFu)), fabsf(bf16_bits_to_float(qw[w] >> 16))));
-          float a0, a1;
-          exchange(am, a0, a1);
-          const float amax = fmaxf(a0, a1);
-          int ex = 0;
-          if (amax > 0.f) frexpf(amax, &ex);
-          const float sgn = a.qk_scale_log2 < 0.f ? -1.f : 1.f;
-          const float qs = sgn * (amax > 0.f ? ldexpf(1.f, 8 - ex) : 1.f);
-          row_scale *= amax > 0.f ? ldexpf(1.f, ex - 8) : 1.f;
-          uint32_t qhi[QW / 2], qlo[QW / 2];  // 4 dims per word
-#pragma unroll
-          for (int c = 0; c < QW / 2; ++c) {
-            const uint32_t w0 = qw[2 * c], w1 = qw[2 * c + 1];
-            const float2 x01 = make_float2(bf16_bits_to_float(w0 & 0xFFFFu) * qs, bf16_bits_to_float(w0 >> 16) * qs);
-            const float2 x23 = make_float2(bf16_bits_to_float(w1 & 0xFFFFu) * qs, bf16_bits_to_float(w1 >> 16) * qs);
-            const uint32_t h01 = __nv_cvt_float2_to_fp8x2(x01, __NV_SATFINITE, __NV_E4M3);
-            const uint32_t h23 = __nv_cvt_float2_to_fp8x2(x23, __NV_SATFINITE, __NV_E4M3);
-            const float2 d01 = unpack2<false>(e4m3x2_to_f16x2(h01));
-            const float2 d23 = unpack2<false>(e4m3x2_to_f16x2(h23));
-            const uint32_t l01 = __nv_cvt_float2_to_fp8x2(make_float2(x01.x - d01.x, x01.y - d01.y), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t l23 = __nv_cvt_float2_to_fp8x2(make_float2(x23.x - d23.x, x23.y - d23.y), __NV_SATFINITE, __NV_E4M3);
-            qhi[c] = (h01 & 0xFFFFu) | (h23 << 16);
-            qlo[c] = (l01 & 0xFFFFu) | (l23 << 16);
-          }
-          if constexpr (QW == 32) {
-            tmem_st16u(qcol + 16 * hf, qhi);
-            tmem_st16u(qcol + 32 + 16 * hf, qlo);
-          } else {
-            tmem_st8u(qcol + 8 * hf, qhi);
-            tmem_st8u(qcol + 32 + 8 * hf, qlo);
-          }
-        }
-        tmem_wait_st();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->q_ready[j & 1]);
-      return fmaxf(row_scale, kMinFactor);
-    };
-
-    Seg cur, nxt;
-    read_seg(0, cur);
-    float next_scale = cur.b1 > cur.b0 ? put_q(cur, 0) : 0.f;
     int g = 0;
-    for (int j = 0; ok && cur.b1 > cur.b0; ++j) {
-      const float row_scale = next_scale;
-      const int rows = tile_rows(cur);
+    for (int j = 0; ok; ++j) {
+      Seg cur;
+      read_seg(j, cur);
+      if (!ok || cur.b1 == cur.b0) break;
+      const int rows = min(a.tile_nodes, cur.n - cur.tile * a.tile_nodes) * a.G;
       const bool active = quad * 32 < rows;
       const int own = cur.tile * a.tile_nodes + min(tl, rows / a.G - 1);  // this row's node
       const long long qrow = (long long)cur.q0 + own;
-      float m = -INFINITY, l = 0.f, vref = 0.f;
+      const uint64_t* words = a.mask ? ctl->mask[j % kRowRing][own - cur.tile * a.tile_nodes] : nullptr;
+      float m = -INFINITY, l = 0.f, vref = 0.f, row_scale = 1.f;
       for (int b = cur.b0; b < cur.b1; ++b, ++g) {
         const int sb = g & 1, se = g % kScaleRing;
         const bool first = b == cur.b0;
@@ -749,8 +826,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
         }
         const int j0 = 128 * b + 64 * hf - cur.base;  // this thread's first key, as a node
         const bool masked = j0 + 63 >= 0;
-        const uint64_t vis = active && masked ? sees64(a, qrow, own, cur.n, j0) : ~0ull;
         ok = __all_sync(kAll, ok && wait_or_abort(&ctl->s_full[sb], (g >> 1) & 1, abort_flag, a.err));
+        // (S was made from the segment's queries, so its masks and factors are there too)
+        if (first) row_scale = ctl->row_scale[j % kRowRing][r];
+        const uint64_t vis = active && masked ? sees64(words, a.words, own, cur.n, j0) : ~0ull;
         const uint32_t sbase = trow + sb * 128;
         if (active) {
           float mh = -INFINITY;
@@ -886,12 +965,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
           if constexpr (BLK) mbar_arrive(&ctl->sc_empty[se]);
           mbar_arrive(&ctl->p_full[sb]);
         }
-        if (first) {  // the next segment's queries, while this one runs
-          read_seg(j + 1, nxt);
-          if (ok && nxt.b1 > nxt.b0) next_scale = put_q(nxt, j + 1);
-        }
         if (!ok) break;
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->row_free[j % kRowRing]);
       // The segment's rows: the output, or a partial state.
       float l0 = 0.f, l1 = 0.f;
       if (active) exchange(l, l0, l1);
@@ -927,7 +1004,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
         }
         if (!whole && hf == 0 && r < rows) a.ws_ml[prow] = make_float2(m, Ls);
       }
-      cur = nxt;
     }
   }
 
@@ -949,7 +1025,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeArgs a) {
   const int c0 = blockIdx.x, lane = threadIdx.x & 31;
   const int4 job = a.jobs[c0];
   if (job.x < 0) return;
-  const SeqInfo info = seq_info(a, job.x);
+  const SeqInfo info = seq_info(a, seq_raw(a, job.x));
   if (info.tiles == 0) return;
   const int h = job.y / info.tiles, tile = job.y - h * info.tiles;
   const int rows = min(a.tile_nodes, info.n - tile * a.tile_nodes) * a.G;
@@ -1036,6 +1112,40 @@ Build pick(int kv_dtype, bool f32) {
     default:
       return f32 ? Launch<K_F16, D, PA_FP32, true>::get() : Launch<K_F16, D, PA_FP16, true>::get();
   }
+}
+
+// Maps of a layer's K and V regions in rows of 64 bytes, 64-byte swizzled: 128 of them
+// are the K-major operand layout of that width.
+int layer_row64_maps(pa_pool* pool, int layer, const CUtensorMap** tk, const CUtensorMap** tv) {
+  typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  const pa_pool_desc& d = pool->desc;
+  if (pool->tmaps_half.size() != 2u * d.n_layers) {
+    pool->tmaps_half.assign(2u * d.n_layers, pa_tmap_blob{});
+    pool->tmap_half_ready.assign(d.n_layers, 0);
+  }
+  CUtensorMap* maps = reinterpret_cast<CUtensorMap*>(pool->tmaps_half.data()) + 2 * layer;
+  if (!pool->tmap_half_ready[layer]) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t dims[2] = {64, (cuuint64_t)d.num_blocks * d.n_kv_heads * d.block_size}, strides[1] = {64};
+    const cuuint32_t box[2] = {64, 16}, es[2] = {1, 1};
+    for (int which = 0; which < 2; ++which) {
+      uint8_t* base = (which ? pool->v : pool->k) + (size_t)layer * pool->layer_bytes;
+      const CUresult r = reinterpret_cast<Encode>(p)(
+          &maps[which], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+      if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    }
+    pool->tmap_half_ready[layer] = 1;
+  }
+  *tk = &maps[0];
+  *tv = &maps[1];
+  return PA_OK;
 }
 
 int sm_count(int* dev, int* sms) {
@@ -1129,7 +1239,10 @@ int pa_decode_tree(pa_pool* pool, int layer, void* out, int out_dtype, const voi
   if (!err) return PA_ERR_CUDA;
   const CUtensorMap *tk = nullptr, *tv = nullptr;
   try {
-    st = D * pool->elem_bytes == 128 ? layer_maps(pool, layer, &tk, &tv) : layer_part_maps(pool, layer, &tk, &tv);
+    const int row = D * pool->elem_bytes;
+    st = row == 128   ? layer_maps(pool, layer, &tk, &tv)
+         : row == 256 ? layer_half_maps(pool, layer, &tk, &tv)
+                      : layer_row64_maps(pool, layer, &tk, &tv);
   } catch (...) {  // (the pool's first use of a layer allocates its map on the host)
     return fail(PA_ERR_NO_MEMORY, "host allocation failed");
   }
