@@ -29,6 +29,7 @@
 #include <algorithm>
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "pa_tc.cuh"
 
@@ -38,10 +39,10 @@ namespace {
 using namespace tc;
 
 constexpr int kRows = 128;     // MMA rows of a tile: nodes x the G heads of a kv head
-// 16 warps, four on each scheduler: 0 copies, 1 issues MMAs, 4-11 softmax; 2, 3, 14 and 15 take V
-// (off the scheduler of the MMA warp, whose serial chain of instructions sets the pace), 12-15 the
-// queries and masks of the segment ahead (a warp reaches the 32 tensor-memory lanes of its
-// number modulo 4).
+// 16 warps, four on each scheduler: 0 issues MMAs, 1 copies, 2 and 3 fetch masks, 4-11 softmax, 12-15
+// take V, the queries of the segment ahead and the output of the one behind.  A warp reaches the 32 tensor-memory lanes of its
+// number modulo 4, so a tile's rows are put into the highest lanes: with 96 rows or fewer the MMA
+// warp's scheduler has no softmax warp at work.
 constexpr int kThreads = 512;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr uint32_t kTmemCols = 512;
@@ -71,10 +72,11 @@ struct Lay {
   static constexpr int kHalves = kRow == 256 ? 2 : 1;  // 128-byte parts, loaded and laid out apart
   static constexpr int kPart = kRow / kHalves;
   static constexpr int kSlot = 128 * kRow;  // a block of K, or of V
-  static constexpr int kRing = kSlot == 32768 ? 3 : 4;
-  static constexpr int kVT = 2 * kRing * kSlot;      // FP8: two blocks of V in binary16
+  static constexpr int kRing = kF8 || kSlot == 32768 ? 3 : 4;  // blocks of K, and of V
+  static constexpr int kVT = 2 * kRing * kSlot;  // FP8: two blocks of V in binary16
   static constexpr int kVTBlock = 128 * D * 2;
-  static constexpr int kData = kVT + (kF8 ? 2 * kVTBlock : 0);
+  static constexpr int kQ = kVT + (kF8 ? 2 * kVTBlock : 0);  // FP8: the next segment's queries as they are
+  static constexpr int kData = kQ + (kF8 ? kRows * D * 2 : 0);
   // a block needs kUnitCost more for its unit's queries and output rows
   static constexpr int kUnitCost = kF8 ? 3 : 2;
 };
@@ -89,18 +91,19 @@ struct Seg {
 struct Ctrl {
   Seg seg[kSegRing];
   uint64_t seg_full[kSegRing], seg_empty[kSegRing];
-  uint64_t kv_full[4], kv_empty[4], s_full[2], p_full[2], vt_full[2], vt_empty[2];
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], vt_empty[2];
   uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
-  uint64_t q_ready[2], q_free[2], row_free[kRowRing], o_full, drain, xchg[4];
+  uint64_t q_ready[2], q_free[2], row_free[kRowRing], o_full, o_free, drain, xchg[4];
   uint64_t tail_ready[2], tail_done[2];  // 16-bit pools: blocks that reach the tree, by their parity
   uint64_t mask[kRowRing][128][PA_TREE_MAX_NODES / 64];  // a tile's nodes' mask words
   float row_scale[kRowRing][128];        // each row's score factor
+  float4 fin[kRowRing][128];             // each row's (m, V scale of O, the two threads' l) at the segment's end
   float2 sc[kScaleRing][8];              // block-scaled pools: (K scale, V scale) of each page of a block
   float xbuf[2][128][2];                 // the two half-row threads' partials
   long long warp_sums[kThreads / 32];
   long long start_off;
   int start_seq;
-  int bad[8];  // segment j's V had infinities or NaN among its nodes: bad[j % 8] == j + 1
+  int bad[8];  // segment j has infinities or NaN in its nodes' V or a tile without a finite scale: bad[j % 8] == j + 1
   uint32_t tmem;
   int abort;
 };
@@ -166,6 +169,9 @@ __device__ __forceinline__ SeqInfo seq_info(const TreeArgs& a, const SeqRaw& r) 
   return i;
 }
 
+// The tensor-memory lane of a tile's first row (a multiple of 32, so that warps are whole).
+__device__ __forceinline__ int first_lane(int rows) { return (kRows - rows) & ~31; }
+
 // The mask of a row over the 64 nodes from j0 on (bits of nodes below 0, history, are set).
 // w: its words (nullptr: a chain, whose node `own` sees those up to itself).
 __device__ __forceinline__ uint64_t sees64(const uint64_t* w, int words, int own, int n, int j0) {
@@ -209,15 +215,33 @@ __device__ __forceinline__ bool take_out(uint4& x) {
 }
 
 // Adds to o (32 columns from dim d0) the infinities and NaN of V of the nodes that the row sees in the
-// segment.
+// segment, and NaN for a seen token whose tile has no finite scale.
 template <int KIND, int D>
 __device__ __noinline__ void put_back(const TreeArgs& a, const Seg& sg, long long row, int own, int d0, float* o) {
   using L = Lay<KIND, D>;
-  for (int j = max(0, 128 * sg.b0 - sg.base); j < min(sg.n, 128 * sg.b1 - sg.base); ++j) {
+  const int first = max(0, 128 * sg.b0 - sg.base);
+  const int end = min(sg.n, 128 * sg.b1 - sg.base);
+  auto tile_of = [&](int t) -> long long {
+    const int blk = a.tables[(size_t)sg.seq * a.max_blocks + (t >> 4)];
+    return blk < 0 || blk >= a.num_blocks ? -1 : (long long)blk * a.Hkv + sg.h;
+  };
+  auto lost = [&](long long tile) { return L::kBlk && !(fabsf(a.ksc[tile]) < INFINITY && fabsf(a.vsc[tile]) < INFINITY); };
+  bool nan = false;
+  if (L::kBlk)  // tiles of the history
+#pragma unroll 1
+    for (int t = 128 * sg.b0; t < min(sg.base, 128 * sg.b1); t += 16) {
+      const long long tile = tile_of(t);
+      nan = nan || (tile >= 0 && lost(tile));
+    }
+#pragma unroll 1
+  for (int j = first; j < end; ++j) {
     if (!sees(a, row, own, j)) continue;
-    const int t = sg.base + j, blk = a.tables[(size_t)sg.seq * a.max_blocks + (t >> 4)];
-    if (blk < 0 || blk >= a.num_blocks) continue;
-    const uint8_t* v = a.v + (((size_t)blk * a.Hkv + sg.h) * 16 + (t & 15)) * L::kRow;
+    const int t = sg.base + j;
+    const long long tile = tile_of(t);
+    if (tile < 0) continue;
+    nan = nan || lost(tile);
+    const uint8_t* v = a.v + ((size_t)tile * 16 + (t & 15)) * L::kRow;
+#pragma unroll 1
     for (int e = 0; e < 32; ++e) {
       float x;
       if constexpr (KIND == K_BF16) x = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(v)[d0 + e]);
@@ -226,6 +250,39 @@ __device__ __noinline__ void put_back(const TreeArgs& a, const Seg& sg, long lon
       if (!(fabsf(x) < INFINITY)) o[e] += x;
     }
   }
+  if (nan)
+#pragma unroll 1
+    for (int e = 0; e < 32; ++e) o[e] = NAN;
+}
+
+// Whether the phase of the given parity is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(done) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+  return done != 0;
+}
+
+// D (TMEM) = A x B (+ D) with A in tensor memory; lo: the low word of B's descriptor, whose high one is a
+// constant of its layout.
+template <bool F8>
+__device__ __forceinline__ void mma_lo(uint32_t d, uint32_t a_tmem, uint32_t lo, uint32_t hi, uint32_t idesc, uint32_t acc) {
+  if constexpr (F8)
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], b, %4, p;\n\t}"
+                 ::"r"(d), "r"(a_tmem), "r"(lo), "r"(hi), "r"(idesc), "r"(acc) : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
+                 ::"r"(d), "r"(a_tmem), "r"(lo), "r"(hi), "r"(idesc), "r"(acc) : "memory");
+}
+
+// As tc::wait_or_abort, whose retries are kept out of line: inlined at every wait they make up most of the code.
+__device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
+  return wait_or_abort(reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(bar)), parity, abort_flag, err);
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
+  return mbar_try_wait(bar, parity) || wait_more(smem_addr(bar), parity, abort_flag, err);
 }
 
 template <int KIND, int D, int OUT, bool PSPLIT>
@@ -245,42 +302,51 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+#pragma unroll 1
     for (int i = 0; i < kSegRing; ++i) {
       mbar_init(&ctl->seg_full[i], 1);
-      mbar_init(&ctl->seg_empty[i], 15);  // MMA, 6 warps for V and queries, 8 softmax
+      mbar_init(&ctl->seg_empty[i], 15);  // MMA, 2 for masks, 8 softmax, 4 for V
     }
+#pragma unroll 1
     for (int i = 0; i < kRowRing; ++i) mbar_init(&ctl->row_free[i], 8);
+#pragma unroll 1
     for (int i = 0; i < R; ++i) {
-      mbar_init(&ctl->kv_full[i], 1);
-      mbar_init(&ctl->kv_empty[i], F8 ? 5 : 1);  // FP8: the Q K MMAs and four warps; 16-bit: the P V MMAs
+      mbar_init(&ctl->k_full[i], 1);
+      mbar_init(&ctl->k_empty[i], 1);           // the Q K MMAs
+      mbar_init(&ctl->v_full[i], 1);
+      mbar_init(&ctl->v_empty[i], F8 ? 4 : 1);  // FP8: the warps that convert it; 16-bit: the P V MMAs
     }
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->s_full[i], 1);
-      mbar_init(&ctl->p_full[i], 8);
-      mbar_init(&ctl->vt_full[i], 4);
+      mbar_init(&ctl->p_full[i], F8 ? 12 : 8);  // softmax; FP8: and the four warps that convert V
       mbar_init(&ctl->vt_empty[i], 1);
-      mbar_init(&ctl->q_ready[i], 4);
+      mbar_init(&ctl->q_ready[i], 6);
       mbar_init(&ctl->q_free[i], 1);
       mbar_init(&ctl->tail_ready[i], 1);
       mbar_init(&ctl->tail_done[i], 4);
     }
+#pragma unroll 1
     for (int i = 0; i < kScaleRing; ++i) {
       mbar_init(&ctl->sc_full[i], 1);
       mbar_init(&ctl->sc_empty[i], 8);
     }
+#pragma unroll 1
     for (int i = 0; i < 4; ++i) mbar_init(&ctl->xchg[i], 2);
+#pragma unroll 1
     for (int i = 0; i < 8; ++i) ctl->bad[i] = 0;
     mbar_init(&ctl->o_full, 1);
+    mbar_init(&ctl->o_free, 4);
     mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
     ctl->start_seq = -1;
     fence_barrier_init();
   }
-  if (warp == 0 && lane == 0) {
+  if (warp == 1 && lane == 0) {
     prefetch_tensormap(&tmk);
     prefetch_tensormap(&tmv);
   }
-  if (warp == 1) {
+  if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                  ::"r"(smem_addr(&ctl->tmem)), "r"(kTmemCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -294,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
   const int per = (a.S + kThreads - 1) / kThreads;
   const int s0 = min(a.S, (int)threadIdx.x * per), s1 = min(a.S, s0 + per);
   long long mine = 0;
+#pragma unroll 1
   for (int s = s0; s < s1; ++s) {
     const SeqInfo i = seq_info(a, seq_raw(a, s));
     if (i.bad) record_error(a.err, PA_ERR_BOUNDS);
@@ -310,6 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
     if (lane == 31) ctl->warp_sums[warp] = x;
     __syncthreads();
     long long ahead = 0;
+#pragma unroll 1
     for (int w = 0; w < kThreads / 32; ++w) {
       ahead += w < warp ? ctl->warp_sums[w] : 0;
       total += ctl->warp_sums[w];
@@ -320,7 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
   const long long pos0 = (long long)blockIdx.x * T, pos_end = min(total, pos0 + T);
   if (pos0 < total && before <= pos0 && pos0 < before + mine) {
     long long cum = before;
-    for (int s = s0; s < s1; ++s) {
+  #pragma unroll 1
+  for (int s = s0; s < s1; ++s) {
       const SeqInfo i = seq_info(a, seq_raw(a, s));
       const long long c = i.units(a.Hkv) * (i.nblk + kUnit);
       if (pos0 < cum + c) {
@@ -331,15 +400,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       cum += c;
     }
   }
-  if (threadIdx.x == 0) a.jobs[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x == 32) a.jobs[blockIdx.x] = make_int4(-1, 0, 0, 0);  // (the copying warp's lane 0 may set it)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl->tmem;
+  // A 512-column allocation spans the whole tensor memory, so its base is 0, and taken as the constant:
+  // every tensor-memory operand of the MMA warp is then an immediate.
+  constexpr uint32_t tmem = 0;
 
   if (pos0 >= total || ctl->start_seq < 0) {
     // no work for this CTA
-  } else if (warp == 0) {
+  } else if (ctl->tmem != 0) {
+    if (threadIdx.x == 0) record_error(a.err, PA_ERR_UNSUPPORTED);
+  } else if (warp == 1) {
     // ---------------------------------------------------------- schedule and TMA producer
     const uint64_t policy = l2_evict_first_policy();
     int seq = ctl->start_seq;
@@ -351,7 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
     long long pos = pos0;
     bool ok = true;
     int made = 0;  // descriptions handed out
-    auto produce = [&]() -> Seg {
+    bool last = false;
+    auto produce = [&]() {  // the next segment's description, empty behind the last one
       Seg sg = {};
       while (pos < pos_end) {
         while (u >= info.units(a.Hkv)) {
@@ -362,7 +436,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
           u = 0;
           v = 0;
         }
-        if (seq >= a.S) break;  // (the lengths changed under the kernel)
+        if (seq >= a.S) {  // (the lengths changed under the kernel)
+          pos = pos_end;
+          break;
+        }
         const int take = (int)min((long long)(span - v), pos_end - pos);
         const int b0 = max(0, v - kUnit), b1 = max(0, v + take - kUnit);
         const long long ustart = pos - v;
@@ -391,44 +468,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       }
       const int e = made % kSegRing;
       if (made >= kSegRing)
-        ok = ok && __all_sync(kAll, wait_or_abort(&ctl->seg_empty[e], ((made / kSegRing) - 1) & 1, abort_flag, a.err));
+        ok = ok && __all_sync(kAll, wait_for(&ctl->seg_empty[e], ((made / kSegRing) - 1) & 1, abort_flag, a.err));
       if (ok && lane == 0) {
         ctl->seg[e] = sg;
         mbar_arrive(&ctl->seg_full[e]);
       }
       ++made;
-      if (!ok) sg.b1 = sg.b0;
-      return sg;
+      last = sg.b1 == sg.b0;
     };
     // Batches of up to four blocks of a segment: the table entries of a batch are loaded two
     // batches ahead (lane i: page i), its tile scales one ahead, for while the copies keep HBM
     // busy such a load takes some microseconds.
     struct Batch {
-      int seq, h, b, nb, page_end, raw;
-    };
-    // A segment's description is handed out before the first copies of the one in front of it, as the
-    // queries' warps look one segment ahead.
-    Seg front = {}, behind = produce();
-    int fb = 0;  // the next batch's first block, in the front segment
-    bool more = true;
-    auto fetch = [&]() -> Batch {
-      Batch x = {0, 0, 0, 0, 0, 0};
-      if (more && fb == front.b1) {
-        front = behind;
-        fb = front.b0;
-        more = front.b1 > front.b0;
-        if (more) behind = produce();
-      }
-      if (!more) return x;
-      x.seq = front.seq;
-      x.h = front.h;
-      x.b = fb;
-      x.nb = min(4, front.b1 - fb);
-      x.page_end = min(8 * (fb + x.nb), (front.base + front.n + 15) >> 4);
-      fb += x.nb;
-      const int page = 8 * x.b + lane;
-      if (page < x.page_end) x.raw = a.tables[(size_t)x.seq * a.max_blocks + page];
-      return x;
+      int j, seq, h, b, nb, page_end, raw;  // j: the segment's number
     };
     float sk = 1.f, sv = 0.f;
     auto scales = [&](Batch& x) {  // checks the entries; block-scaled pools: loads their scales
@@ -446,66 +498,107 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
         }
       }
     };
-    Batch cur = fetch(), nxt = fetch();
-    scales(cur);
-    int g = 0;  // blocks issued
-    while (ok && cur.nb > 0) {
-      const Batch far = fetch();
-      // a tile without a finite scale holds NaN: marked by -1
-      const float csk = fabsf(sk) < INFINITY ? sk : -1.f, csv = fabsf(sv) < INFINITY ? sv : -1.f;
+    int g = 0, gk = 0;    // blocks issued: whole, and their K
+    int fj = -1, fb = 0;  // the segment that batches are fetched from, and the next one's first block
+    Seg front = {};
+    bool more = true;
+    Batch cur = {}, nxt = {};
+#pragma unroll 1
+    while (ok) {
+      Batch far = {};
+      if (more && fb == front.b1) {
+        // A segment is described before the first copies of the one in front of it, as the queries' warps look
+        // one segment ahead.
+        ++fj;
+#pragma unroll 1
+        while (ok && !last && made < fj + 2) produce();
+        if (!ok) break;
+        __syncwarp();
+        front = ctl->seg[fj % kSegRing];
+        fb = front.b0;
+        more = front.b1 > front.b0;
+      }
+      if (more) {
+        far.j = fj;
+        far.seq = front.seq;
+        far.h = front.h;
+        far.b = fb;
+        far.nb = min(4, front.b1 - fb);
+        far.page_end = min(8 * (fb + far.nb), (front.base + front.n + 15) >> 4);
+        const int page = 8 * fb + lane;
+        if (page < far.page_end) far.raw = a.tables[(size_t)far.seq * a.max_blocks + page];
+        fb += far.nb;
+      }
+      // a tile without a finite scale holds NaN, for the rows that see it (put_back); here it counts for nothing
+      float csk = sk, csv = sv;
+      if (BLK && !(fabsf(sk) < INFINITY && fabsf(sv) < INFINITY)) {
+        csk = 1.f;
+        csv = 0.f;
+        ctl->bad[cur.j & 7] = cur.j + 1;
+      }
       scales(nxt);
+#pragma unroll 1
       for (int j = 0; j < cur.nb; ++j, ++g) {
         const int slot = g % R, pb = 8 * j, b = cur.b + j;
-        if (g >= R) ok = __all_sync(kAll, wait_or_abort(&ctl->kv_empty[slot], ((g / R) - 1) & 1, abort_flag, a.err));
-        if (!ok) break;
         const int cnt = min(8, cur.page_end - 8 * b);
         if constexpr (BLK) {
           const int e = g % kScaleRing;
           if (g >= kScaleRing)
-            ok = __all_sync(kAll, wait_or_abort(&ctl->sc_empty[e], ((g / kScaleRing) - 1) & 1, abort_flag, a.err));
+            ok = __all_sync(kAll, wait_for(&ctl->sc_empty[e], ((g / kScaleRing) - 1) & 1, abort_flag, a.err));
           if (!ok) break;
           if (lane >= pb && lane < pb + 8) ctl->sc[e][lane - pb] = make_float2(csk, csv);
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->sc_full[e]);
         }
-        if (lane == 0) mbar_arrive_expect_tx(&ctl->kv_full[slot], (uint32_t)cnt * 32u * L::kRow);
         const int i = lane - pb;  // this lane's page of the block
-        if (i >= 0 && i < cnt) {
-          const int row0 = (cur.raw * a.Hkv + cur.h) * 16;
-          uint8_t* kd = sm + slot * L::kSlot + i * 16 * L::kPart;
-          uint8_t* vd = kd + R * L::kSlot;
+        const int row0 = (cur.raw * a.Hkv + cur.h) * 16;
+        auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* full, uint64_t* empty) {
+          if (g >= R) ok = __all_sync(kAll, ok && wait_for(empty, ((g / R) - 1) & 1, abort_flag, a.err));
+          if (!ok) return;
+          if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)cnt * 16u * L::kRow);
+          if (i >= 0 && i < cnt) {
 #pragma unroll
-          for (int hh = 0; hh < L::kHalves; ++hh) {
-            tma_load_2d(kd + hh * 16384, &tmk, 128 * hh, row0, &ctl->kv_full[slot], policy);
-            tma_load_2d(vd + hh * 16384, &tmv, 128 * hh, row0, &ctl->kv_full[slot], policy);
+            for (int hh = 0; hh < L::kHalves; ++hh)
+              tma_load_2d(dst + i * 16 * L::kPart + hh * 16384, map, 128 * hh, row0, full, policy);
           }
-        }
+        };
+        load(&tmk, sm + slot * L::kSlot, &ctl->k_full[slot], &ctl->k_empty[slot]);
+        if (ok) ++gk;
+        load(&tmv, sm + (R + slot) * L::kSlot, &ctl->v_full[slot], &ctl->v_empty[slot]);
+        if (!ok) break;
       }
-      if (!ok) break;
       cur = nxt;
       nxt = far;
+      if (!more && cur.nb == 0 && nxt.nb == 0) break;
     }
     // no copy may still target shared memory when the CTA exits
-    if (lane == 0)
+    if (lane == 0) {
+#pragma unroll 1
+      for (int j = max(0, gk - R); j < gk; ++j)
+        if (!mbar_wait(&ctl->k_full[j % R], (j / R) & 1)) record_error(a.err, PA_ERR_TIMEOUT);
+#pragma unroll 1
       for (int j = max(0, g - R); j < g; ++j)
-        if (!mbar_wait(&ctl->kv_full[j % R], (j / R) & 1)) record_error(a.err, PA_ERR_TIMEOUT);
-  } else if (warp == 1) {
+        if (!mbar_wait(&ctl->v_full[j % R], (j / R) & 1)) record_error(a.err, PA_ERR_TIMEOUT);
+    }
+  } else if (warp == 0) {
     // ---------------------------------------------------------- MMA issue
     if (lane == 0) {
-      const uint64_t kdesc0 = L::kPart == 64
-                                  ? (uint64_t)((smem_addr(sm) & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) |
-                                        ((uint64_t)(512 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)4 << 61)
-                                  : kmajor(smem_addr(sm));
-      const uint64_t vdesc0 = mnmajor(smem_addr(sm + (F8 ? L::kVT : R * L::kSlot)));
-      bool run = true;
+      constexpr uint32_t kHi128 = (1024u >> 4) | (1u << 14) | (2u << 29);  // 128-byte swizzle, 8 rows 1024 bytes apart
+      constexpr uint32_t kHiK = L::kPart == 64 ? (512u >> 4) | (1u << 14) | (4u << 29) : kHi128;
+      const uint32_t k_lo = ((smem_addr(sm) & 0x3FFFFu) >> 4) | (1u << 16);
+      const uint32_t v_lo = ((smem_addr(sm + (F8 ? L::kVT : R * L::kSlot)) & 0x3FFFFu) >> 4) | ((16384u >> 4) << 16);
       // cursors over the blocks: Q K^T, two blocks ahead of P V
       int gq = 0, jq = -1, bq = 0, bq1 = 0, qbase = 0, tq = 0;
       bool q_end = false;
       int gp = 0, jp = -1, bp = 0, bp0 = 0, bp1 = 0, pbase = 0, tp = 0;
-      auto seg_wait = [&](int j) { return wait_or_abort(&ctl->seg_full[j % kSegRing], (j / kSegRing) & 1, abort_flag, a.err); };
+      // A wait costs this thread some 150 cycles even when its phase is complete.  So the next one's barrier
+      // is tested while the MMAs in between are issued.  (The phase in front of the tested one is known to be
+      // complete: this thread has waited for it.)
+      bool k_ready = false, p_ready = false, v_ready = false;
+      auto seg_wait = [&](int j) { return wait_for(&ctl->seg_full[j % kSegRing], (j / kSegRing) & 1, abort_flag, a.err); };
       auto issue_qk = [&]() -> bool {
-        if (q_end) return true;
         if (bq == bq1) {
+          if (q_end) return true;
           ++jq;
           if (!seg_wait(jq)) return false;
           const Seg& sg = ctl->seg[jq % kSegRing];
@@ -516,159 +609,204 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
             q_end = true;
             return true;
           }
-          if (!wait_or_abort(&ctl->q_ready[jq & 1], (jq >> 1) & 1, abort_flag, a.err)) return false;
+          if (!wait_for(&ctl->q_ready[jq & 1], (jq >> 1) & 1, abort_flag, a.err)) return false;
         }
         const int slot = gq % R, sb = gq & 1;
-        if (!wait_or_abort(&ctl->kv_full[slot], (gq / R) & 1, abort_flag, a.err)) return false;
+        if (!k_ready && !wait_for(&ctl->k_full[slot], (gq / R) & 1, abort_flag, a.err)) return false;
+        k_ready = false;
         tc_fence_after();
         if constexpr (!F8)
           if (128 * bq + 127 >= qbase) {  // V of a block that reaches the tree is looked through first
             mbar_arrive(&ctl->tail_ready[tq & 1]);
             ++tq;
           }
-        const uint64_t kd = kdesc0 + (uint64_t)(slot * (L::kSlot >> 4));
-        const uint32_t qcol = tmem + kQCol + 64 * (jq & 1);
+        const uint32_t lo = k_lo + (uint32_t)(slot * (L::kSlot >> 4));
+        const uint32_t qcol = tmem + kQCol + 64 * (jq & 1), scol = tmem + sb * 128;
         if constexpr (F8) {
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
-              mma_f8_ts(tmem + sb * 128, qcol + 32 * t + 8 * k, kd + 2 * k, kIdescQK, (uint32_t)(t | k));
+              mma_lo<true>(scol, qcol + 32 * t + 8 * k, lo + 2 * k, kHiK, kIdescQK, (uint32_t)(t | k));
         } else {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_f16_ts(tmem + sb * 128, qcol + 8 * k, kd + (k >> 2) * (16384 >> 4) + (k & 3) * 2, kIdescQK, (uint32_t)k);
+          for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_lo<false>(scol, qcol + 32 * h + 8 * k, lo + h * (16384 >> 4) + k * 2, kHiK, kIdescQK, (uint32_t)(h | k));
         }
         mma_commit(&ctl->s_full[sb]);
-        if constexpr (F8) mma_commit(&ctl->kv_empty[slot]);
+        mma_commit(&ctl->k_empty[slot]);
         ++gq;
         if (++bq == bq1) mma_commit(&ctl->q_free[jq & 1]);  // the segment's queries are read
         return true;
       };
-      run = issue_qk() && issue_qk();
-      while (run) {
+#pragma unroll 1
+      for (int lead = 0;; ++lead) {
+       if (lead >= 2) {
         if (bp == bp1) {
           ++jp;
-          if (!(run = seg_wait(jp))) break;
+          if (!seg_wait(jp)) break;
           const Seg& sg = ctl->seg[jp % kSegRing];
           bp = bp0 = sg.b0;
           bp1 = sg.b1;
           pbase = sg.base;
           mbar_arrive(&ctl->seg_empty[jp % kSegRing]);
           if (bp == bp1) break;
+          if (jp > 0 && !wait_for(&ctl->o_free, (jp - 1) & 1, abort_flag, a.err)) break;  // O is read out
         }
         const int vb = gp & 1;
-        run = wait_or_abort(&ctl->p_full[vb], (gp >> 1) & 1, abort_flag, a.err);
-        if constexpr (F8) {
-          run = run && wait_or_abort(&ctl->vt_full[vb], (gp >> 1) & 1, abort_flag, a.err);
-        } else if (run && 128 * bp + 127 >= pbase) {
-          run = wait_or_abort(&ctl->tail_done[tp & 1], (tp >> 1) & 1, abort_flag, a.err);
-          ++tp;
+        if (!p_ready && !wait_for(&ctl->p_full[vb], (gp >> 1) & 1, abort_flag, a.err)) break;
+        if constexpr (!F8) {
+          if (!v_ready && !wait_for(&ctl->v_full[gp % R], (gp / R) & 1, abort_flag, a.err)) break;
+          if (128 * bp + 127 >= pbase) {
+            if (!wait_for(&ctl->tail_done[tp & 1], (tp >> 1) & 1, abort_flag, a.err)) break;
+            ++tp;
+          }
         }
-        if (!run) break;
+        k_ready = mbar_test(&ctl->k_full[gq % R], (gq / R) & 1);
         tc_fence_after();
-        const uint64_t vd = vdesc0 + (uint64_t)(F8 ? vb * (L::kVTBlock >> 4) : (gp % R) * (L::kSlot >> 4));
+        const uint32_t lo = v_lo + (uint32_t)(F8 ? vb * (L::kVTBlock >> 4) : (gp % R) * (L::kSlot >> 4));
+        const uint32_t pcol = tmem + vb * 128, add = bp > bp0;
 #pragma unroll
         for (int part = 0; part < (PSPLIT ? 2 : 1); ++part)
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            mma_f16_ts(tmem + kOCol, tmem + vb * 128 + 32 * (k >> 1) + 16 * part + 8 * (k & 1), vd + k * (2048 >> 4),
-                       kIdescPV, (uint32_t)((bp > bp0) | k | part));
+            mma_lo<false>(tmem + kOCol, pcol + 32 * (k >> 1) + 16 * part + 8 * (k & 1), lo + k * (2048 >> 4), kHi128, kIdescPV,
+                          part | k ? 1u : add);
         if constexpr (F8) mma_commit(&ctl->vt_empty[vb]);
-        else mma_commit(&ctl->kv_empty[gp % R]);  // K and V of the block are read
-        if (bp + 1 == bp1) mma_commit(&ctl->o_full);
+        else mma_commit(&ctl->v_empty[gp % R]);
         ++gp;
-        ++bp;
-        run = issue_qk();
+        if (++bp == bp1) mma_commit(&ctl->o_full);
+        p_ready = mbar_test(&ctl->p_full[gp & 1], (gp >> 1) & 1);
+        if constexpr (!F8) v_ready = mbar_test(&ctl->v_full[gp % R], (gp / R) & 1);
+       }
+        if (!issue_qk()) break;
       }
       // every MMA issued above has finished before TMEM is released
       mma_commit(&ctl->drain);
       if (!mbar_wait(&ctl->drain, 0)) record_error(a.err, PA_ERR_TIMEOUT);
     }
     __syncwarp();
-  } else if (warp < 4 || warp >= 12) {
-    // ---------------------------------------------------------- V, queries and masks
-    const bool has_v = warp < 4 || warp >= 14, has_q = warp >= 12;
-    const int ct = 32 * (warp < 4 ? warp - 2 : warp - 12) + lane;  // 0 .. 127 among those that take V
-    const int qr = 32 * (warp & 3) + lane;                          // this lane's row
-    constexpr int QW = D / 2;                                       // 32-bit words of a query
-    uint32_t qw[QW];
-    uint64_t mw[PA_TREE_MAX_NODES / 64];
+  } else if (warp < 4) {
+    // ---------------------------------------------------------- masks
     bool ok = true;
-    // The queries and masks of segment j, loaded in one piece of the work and stored in another, so that
-    // nothing waits for the loads.
-    auto load_rows = [&](const Seg& sg) {
-      const int nodes = min(a.tile_nodes, sg.n - sg.tile * a.tile_nodes), rows = nodes * a.G;
-      const int tl = qr / a.G, hh = qr - tl * a.G;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          a.q + ((size_t)(sg.q0 + sg.tile * a.tile_nodes + tl) * a.Hq + (size_t)sg.h * a.G + hh) * D);
-#pragma unroll
-      for (int c = 0; c < QW / 4; ++c) {
-        const uint4 x = qr < rows ? src[c] : make_uint4(0, 0, 0, 0);
-        qw[4 * c] = x.x;
-        qw[4 * c + 1] = x.y;
-        qw[4 * c + 2] = x.z;
-        qw[4 * c + 3] = x.w;
+    for (int j = 0; ok; ++j) {
+      const int e = j % kSegRing, rr = j % kRowRing;
+      ok = __all_sync(kAll, wait_for(&ctl->seg_full[e], (j / kSegRing) & 1, abort_flag, a.err));
+      if (!ok) break;
+      const Seg sg = ctl->seg[e];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->seg_empty[e]);
+      if (sg.b1 == sg.b0) break;
+      // segment j - 2's phase of q_ready is over, and the rows of segment j - kRowRing are done
+      if (j >= 2) ok = __all_sync(kAll, wait_for(&ctl->q_free[j & 1], ((j >> 1) - 1) & 1, abort_flag, a.err));
+      if (j >= kRowRing) ok = __all_sync(kAll, ok && wait_for(&ctl->row_free[rr], ((j / kRowRing) - 1) & 1, abort_flag, a.err));
+      if (!ok) break;
+      if (a.mask && 128 * sg.b1 > sg.base) {
+        const int node0 = sg.tile * a.tile_nodes, nodes = min(a.tile_nodes, sg.n - node0);
+        const uint64_t* src = a.mask + (size_t)(sg.q0 + node0) * a.words;
+#pragma unroll 1
+        for (int i = threadIdx.x - 64; i < nodes * a.words; i += 64) ctl->mask[rr][i / a.words][i % a.words] = src[i];
       }
-      if (a.mask) {
-#pragma unroll
-        for (int w = 0; w < PA_TREE_MAX_NODES / 64; ++w) {
-          mw[w] = 0;
-          if (qr < nodes && w < a.words)
-            mw[w] = a.mask[(size_t)(sg.q0 + sg.tile * a.tile_nodes + qr) * a.words + w];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->q_ready[j & 1]);
+    }
+  } else if (warp >= 12) {
+    // ---------------------------------------------------------- V, queries and output
+    const int ct = threadIdx.x - 12 * 32;  // 0 .. 127: a key of V, a row of Q and O
+    const int qr = ct;
+    constexpr int QW = D / 2;  // 32-bit words of an output row
+    const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    bool ok = true;
+    // A thread's own row of queries of segment j.  FP8: the warps are busy with V, so the row is copied to shared
+    // memory in the background (chunk c at place c ^ (row mod 16): no bank conflicts) and taken up
+    // some blocks later.  16-bit pools: loaded where it is stored; the warps have little else to do.
+    uint8_t* stage = sm + L::kQ + ct * (D * 2);
+    const int turn = ct & (D / 8 - 1);
+    auto query_row = [&](int j) -> const uint4* {
+      const Seg& sg = ctl->seg[j % kSegRing];
+      const int rows = min(a.tile_nodes, sg.n - sg.tile * a.tile_nodes) * a.G;
+      const int row = qr - first_lane(rows), tl = row / a.G, hh = row - tl * a.G;
+      if (row < 0 || row >= rows) return nullptr;
+      return reinterpret_cast<const uint4*>(
+          a.q + ((long long)(sg.q0 + sg.tile * a.tile_nodes + tl) * a.Hq + (long long)sg.h * a.G + hh) * D);
+    };
+    auto load_rows = [&](int j) {
+      if constexpr (F8) {
+        const uint4* src = query_row(j);
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          uint8_t* to = stage + ((c ^ turn) << 4);
+          if (src) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(src + c) : "memory");
+          else *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
         }
       }
     };
     auto store_rows = [&](int j) {
       // segment j - 2's queries are read, and the rows of segment j - kRowRing are done
-      if (j >= 2) ok = __all_sync(kAll, ok && wait_or_abort(&ctl->q_free[j & 1], ((j >> 1) - 1) & 1, abort_flag, a.err));
+      if (j >= 2) ok = __all_sync(kAll, ok && wait_for(&ctl->q_free[j & 1], ((j >> 1) - 1) & 1, abort_flag, a.err));
       if (j >= kRowRing)
-        ok = __all_sync(kAll, ok && wait_or_abort(&ctl->row_free[j % kRowRing], ((j / kRowRing) - 1) & 1, abort_flag, a.err));
+        ok = __all_sync(kAll, ok && wait_for(&ctl->row_free[j % kRowRing], ((j / kRowRing) - 1) & 1, abort_flag, a.err));
+      if constexpr (F8) asm volatile("cp.async.wait_all;" ::: "memory");
       if (!ok) return;
       tc_fence_after();
-      if (a.mask) {
-#pragma unroll
-        for (int w = 0; w < PA_TREE_MAX_NODES / 64; ++w) ctl->mask[j % kRowRing][qr][w] = mw[w];
-      }
-      const uint32_t qcol = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kQCol + 64 * (j & 1);
+      const uint32_t qcol = trow + kQCol + 64 * (j & 1);
       float row_scale = fabsf(a.qk_scale_log2);
       if constexpr (!F8) {
-        if (a.qk_scale_log2 < 0.f) {  // a negative scale flips the queries' signs
+        const uint4* src = query_row(j);
+        const uint32_t flip = a.qk_scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale flips the queries' signs
+#pragma unroll 1
+        for (int part = 0; part < D / 64; ++part) {
+          uint32_t qw[32];
 #pragma unroll
-          for (int w = 0; w < QW; ++w) qw[w] ^= 0x80008000u;
+          for (int c = 0; c < 8; ++c) {
+            const uint4 x = src ? src[8 * part + c] : make_uint4(0, 0, 0, 0);
+            qw[4 * c] = x.x ^ flip;
+            qw[4 * c + 1] = x.y ^ flip;
+            qw[4 * c + 2] = x.z ^ flip;
+            qw[4 * c + 3] = x.w ^ flip;
+          }
+          tmem_st32u(qcol + 32 * part, qw);
         }
-#pragma unroll
-        for (int w = 0; w < QW; w += 32) tmem_st32u(qcol + w, qw + w);
       } else {
         // scaled by a power of two (the largest |q| in [128, 256)) and split into two E4M3 terms
-        float amax = 0.f;
-#pragma unroll
-        for (int w = 0; w < QW; ++w)
-          amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_float(qw[w] & 0xFFFFu)), fabsf(bf16_bits_to_float(qw[w] >> 16))));
+        uint32_t top = 0;  // the largest magnitude's bits, of either half of a word
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 x = lds128(stage + ((c ^ turn) << 4));
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+        }
+        const float amax = bf16_bits_to_float(max(top & 0xFFFFu, top >> 16));
         int ex = 0;
-        if (amax > 0.f) frexpf(amax, &ex);
+        if (amax > 0.f && amax < INFINITY) frexpf(amax, &ex);
         const float sgn = a.qk_scale_log2 < 0.f ? -1.f : 1.f;
         const float qs = sgn * (amax > 0.f ? ldexpf(1.f, 8 - ex) : 1.f);
         row_scale *= amax > 0.f ? ldexpf(1.f, ex - 8) : 1.f;
+#pragma unroll 1
+        for (int part = 0; part < D / 32; ++part) {
+          uint32_t qhi[8], qlo[8];  // 4 dims per word
 #pragma unroll
-        for (int part = 0; part < QW / 32; ++part) {
-          uint32_t qhi[16], qlo[16];  // 4 dims per word
+          for (int c = 0; c < 4; ++c) {
+            const uint4 x = lds128(stage + (((4 * part + c) ^ turn) << 4));
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const uint32_t w0 = qw[32 * part + 2 * c], w1 = qw[32 * part + 2 * c + 1];
-            const float2 x01 = make_float2(bf16_bits_to_float(w0 & 0xFFFFu) * qs, bf16_bits_to_float(w0 >> 16) * qs);
-            const float2 x23 = make_float2(bf16_bits_to_float(w1 & 0xFFFFu) * qs, bf16_bits_to_float(w1 >> 16) * qs);
-            const uint32_t h01 = __nv_cvt_float2_to_fp8x2(x01, __NV_SATFINITE, __NV_E4M3);
-            const uint32_t h23 = __nv_cvt_float2_to_fp8x2(x23, __NV_SATFINITE, __NV_E4M3);
-            const float2 d01 = unpack2<false>(e4m3x2_to_f16x2(h01));
-            const float2 d23 = unpack2<false>(e4m3x2_to_f16x2(h23));
-            const uint32_t l01 = __nv_cvt_float2_to_fp8x2(make_float2(x01.x - d01.x, x01.y - d01.y), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t l23 = __nv_cvt_float2_to_fp8x2(make_float2(x23.x - d23.x, x23.y - d23.y), __NV_SATFINITE, __NV_E4M3);
-            qhi[c] = (h01 & 0xFFFFu) | (h23 << 16);
-            qlo[c] = (l01 & 0xFFFFu) | (l23 << 16);
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t w0 = w[2 * h], w1 = w[2 * h + 1];
+              const float2 x01 = make_float2(bf16_bits_to_float(w0 & 0xFFFFu) * qs, bf16_bits_to_float(w0 >> 16) * qs);
+              const float2 x23 = make_float2(bf16_bits_to_float(w1 & 0xFFFFu) * qs, bf16_bits_to_float(w1 >> 16) * qs);
+              const uint32_t h01 = __nv_cvt_float2_to_fp8x2(x01, __NV_SATFINITE, __NV_E4M3);
+              const uint32_t h23 = __nv_cvt_float2_to_fp8x2(x23, __NV_SATFINITE, __NV_E4M3);
+              const float2 d01 = unpack2<false>(e4m3x2_to_f16x2(h01));
+              const float2 d23 = unpack2<false>(e4m3x2_to_f16x2(h23));
+              const uint32_t l01 = __nv_cvt_float2_to_fp8x2(make_float2(x01.x - d01.x, x01.y - d01.y), __NV_SATFINITE, __NV_E4M3);
+              const uint32_t l23 = __nv_cvt_float2_to_fp8x2(make_float2(x23.x - d23.x, x23.y - d23.y), __NV_SATFINITE, __NV_E4M3);
+              qhi[2 * c + h] = (h01 & 0xFFFFu) | (h23 << 16);
+              qlo[2 * c + h] = (l01 & 0xFFFFu) | (l23 << 16);
+            }
           }
-          tmem_st16u(qcol + 16 * part, qhi);
-          tmem_st16u(qcol + 32 + 16 * part, qlo);
+          tmem_st8u(qcol + 8 * part, qhi);
+          tmem_st8u(qcol + 32 + 8 * part, qlo);
         }
       }
       // (a zero factor would turn a masked -inf into NaN)
@@ -678,73 +816,142 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->q_ready[j & 1]);
     };
-    auto read_seg = [&](int j, Seg& sg) {
-      const int e = j % kSegRing;
-      ok = __all_sync(kAll, ok && wait_or_abort(&ctl->seg_full[e], (j / kSegRing) & 1, abort_flag, a.err));
-      sg = {};
-      if (ok) sg = ctl->seg[e];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->seg_empty[e]);
-    };
-    Seg sg, ahead;
-    read_seg(0, sg);
-    if (has_q && ok && sg.b1 > sg.b0) {
-      load_rows(sg);
-      store_rows(0);
-    }
-    int g = 0, t = 0;
-    for (int j = 0; ok && sg.b1 > sg.b0; ++j) {
-      read_seg(j + 1, ahead);
-      const bool rows_ahead = has_q && ok && ahead.b1 > ahead.b0;
-      if (rows_ahead) load_rows(ahead);
-      const int ctx = sg.base + sg.n;
-      for (int b = sg.b0; b < sg.b1; ++b, ++g) {
-        const int slot = g % R;
-        const int nvalid = min(128, ctx - 128 * b);  // keys behind the context: zero
-        const int nplain = sg.base - 128 * b;        // keys from here on are nodes
-        bool odd = false;                            // infinities or NaN among them
-        if constexpr (F8) {
-          if (has_v) {
-            const int half = g & 1;
-            ok = __all_sync(kAll, wait_or_abort(&ctl->kv_full[slot], (g / R) & 1, abort_flag, a.err));
-            if (ok && g >= 2) ok = __all_sync(kAll, wait_or_abort(&ctl->vt_empty[half], ((g >> 1) - 1) & 1, abort_flag, a.err));
-            if (!ok) break;
-            const uint8_t* vr = sm + (R + slot) * L::kSlot;
-            uint8_t* vt = sm + L::kVT + half * L::kVTBlock;
-            // consecutive lanes take consecutive keys of one 16-byte chunk
-#pragma unroll 4
-            for (int ch = 0; ch < D / 16; ++ch) {
-              const int key = ct;
-              uint4 w = make_uint4(0, 0, 0, 0);
-              // a row's chunks are permuted by its line's place: 128-byte lines, or 64-byte rows two to a line
-              const uint32_t off = L::kPart == 64 ? key * 64 + ((ch ^ ((key >> 1) & 3)) << 4) : key * 128 + ((ch ^ (key & 7)) << 4);
-              if (key < nvalid) w = lds128(vr + off);
-              if (nplain < 128 && key >= nplain) odd |= take_out<KIND>(w);
-              const uint32_t cw[4] = {w.x, w.y, w.z, w.w};
-              uint32_t hv[8];
+    // The rows of segment j: the output, or a partial state.
+    auto write_rows = [&](int j) {
+      const Seg& sg = ctl->seg[j % kSegRing];
+      ok = __all_sync(kAll, ok && wait_for(&ctl->row_free[j % kRowRing], (j / kRowRing) & 1, abort_flag, a.err));
+      ok = __all_sync(kAll, ok && wait_for(&ctl->o_full, j & 1, abort_flag, a.err));
+      if (!ok) return;
+      tc_fence_after();
+      const int rows = min(a.tile_nodes, sg.n - sg.tile * a.tile_nodes) * a.G;
+      const int r = qr - first_lane(rows), tl = r / a.G, hh = r - tl * a.G;
+      if ((qr | 31) >= first_lane(rows)) {  // (whole warps)
+        const bool live = r >= 0 && r < rows, whole = sg.b0 == 0 && sg.b1 == sg.nblk;
+        const bool odd = *(volatile int*)&ctl->bad[j & 7] == j + 1;
+        const float4 fin = ctl->fin[j % kRowRing][qr];
+        const float Ls = fin.z + fin.w;
+        const float inv = whole ? (Ls > 0.f ? (BLK ? fin.y : a.v_scale) / Ls : 0.f) : BLK ? fin.y : 1.f;
+        const int own = sg.tile * a.tile_nodes + tl;
+        const long long qrow = (long long)sg.q0 + own;
+        const long long orow = (qrow * a.Hq + (long long)sg.h * a.G + hh) * D;
+        const long long prow = (long long)(2 * blockIdx.x + (j > 0)) * kRows + r;
+        const uint32_t oc = trow + kOCol;
+        if (OUT != PA_FP32 && whole && !odd) {
+          // packed as they come, so that O is free before the first store
+          uint32_t w[QW];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) e4m3x4_to_f16x2x2(cw[q], hv[2 * q], hv[2 * q + 1]);
-              uint8_t* row = vt + (ch >> 2) * 16384 + key * 128;
-              const int c0 = (ch & 3) * 2;
-              *reinterpret_cast<uint4*>(row + ((c0 ^ (key & 7)) << 4)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-              *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (key & 7)) << 4)) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
-            }
-            if (odd) ctl->bad[j & 7] = j + 1;
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&ctl->vt_full[half]);
-              mbar_arrive(&ctl->kv_empty[slot]);
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            tmem_ld32(oc + 32 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[16 * c + e] = pack2<OUT == PA_BF16>(o[2 * e] * inv, o[2 * e + 1] * inv);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->o_free);
+          if (live) {
+            uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow);
+#pragma unroll
+            for (int c = 0; c < QW / 4; ++c) to[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            tmem_ld32(oc + 32 * c, o);
+            tmem_wait_ld();
+            if (live) {
+              float sc = inv;
+              if (odd) {
+                float x[32];  // (a copy: o stays in registers where nothing is put back)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = o[e] * inv;
+                sc = 1.f;
+                put_back<KIND, D>(a, sg, qrow, own, 32 * c, x);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = x[e];
+              }
+              if (whole) store_row32<OUT>(a.out, orow + 32 * c, o, sc);
+              else store_row32<PA_FP32>(a.ws_o, prow * D + 32 * c, o, sc);
             }
           }
-        } else if (has_v && nplain < 128) {
+          if (live && !whole) a.ws_ml[prow] = make_float2(fin.x, Ls);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->o_free);
+        }
+      } else {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->o_free);
+      }
+    };
+    // Segment j's first block of V, then the output of j - 1 (whose last products are done about then), and
+    // between j's other blocks the queries of j + 1.  A description is given back with its output.
+    int g = 0, t = 0;
+    for (int j = -1; ok; ++j) {
+      int b0 = 0, b1 = 0, base = 0, ctx = 0;
+      if (j >= 0) {
+        const Seg& sg = ctl->seg[j % kSegRing];
+        b0 = sg.b0;
+        b1 = sg.b1;
+        base = sg.base;
+        ctx = base + sg.n;
+      }
+      const bool end = j >= 0 && b1 == b0;
+      bool rows_ahead = false;
+      if (!end) {
+        ok = __all_sync(kAll, wait_for(&ctl->seg_full[(j + 1) % kSegRing], ((j + 1) / kSegRing) & 1, abort_flag, a.err));
+        if (!ok) break;
+        rows_ahead = ctl->seg[(j + 1) % kSegRing].b1 > ctl->seg[(j + 1) % kSegRing].b0;
+      }
+      for (int b = b0;; ++b) {
+       if (b < b1) {
+        const int slot = g % R;
+        const int nvalid = min(128, ctx - 128 * b);  // keys behind the context: zero
+        const int nplain = base - 128 * b;           // keys from here on are nodes
+        bool odd = false;                            // infinities or NaN among them
+        if constexpr (F8) {
+          const int half = g & 1;
+          ok = __all_sync(kAll, wait_for(&ctl->v_full[slot], (g / R) & 1, abort_flag, a.err));
+          if (ok && g >= 2) ok = __all_sync(kAll, wait_for(&ctl->vt_empty[half], ((g >> 1) - 1) & 1, abort_flag, a.err));
+          if (!ok) break;
+          const uint8_t* vr = sm + (R + slot) * L::kSlot;
+          uint8_t* vt = sm + L::kVT + half * L::kVTBlock;
+          // consecutive lanes take consecutive keys of one 16-byte chunk
+#pragma unroll 4
+          for (int ch = 0; ch < D / 16; ++ch) {
+            const int key = ct;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            // a row's chunks are permuted by its line's place: 128-byte lines, or 64-byte rows two to a line
+            const uint32_t off = L::kPart == 64 ? key * 64 + ((ch ^ ((key >> 1) & 3)) << 4) : key * 128 + ((ch ^ (key & 7)) << 4);
+            if (key < nvalid) w = lds128(vr + off);
+            if (nplain < 128 && key >= nplain) odd |= take_out<KIND>(w);
+            const uint32_t cw[4] = {w.x, w.y, w.z, w.w};
+            uint32_t hv[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) e4m3x4_to_f16x2x2(cw[q], hv[2 * q], hv[2 * q + 1]);
+            uint8_t* row = vt + (ch >> 2) * 16384 + key * 128;
+            const int c0 = (ch & 3) * 2;
+            *reinterpret_cast<uint4*>(row + ((c0 ^ (key & 7)) << 4)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+            *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (key & 7)) << 4)) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
+          }
+          if (odd) ctl->bad[j & 7] = j + 1;
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&ctl->p_full[half]);
+            mbar_arrive(&ctl->v_empty[slot]);
+          }
+        } else if (nplain < 128) {
           // read in place: rows behind the context are zeroed, nodes' rows looked through
-          ok = __all_sync(kAll, wait_or_abort(&ctl->tail_ready[t & 1], (t >> 1) & 1, abort_flag, a.err));
-          ok = ok && __all_sync(kAll, wait_or_abort(&ctl->kv_full[slot], (g / R) & 1, abort_flag, a.err));
+          ok = __all_sync(kAll, wait_for(&ctl->tail_ready[t & 1], (t >> 1) & 1, abort_flag, a.err));
+          ok = ok && __all_sync(kAll, wait_for(&ctl->v_full[slot], (g / R) & 1, abort_flag, a.err));
           if (!ok) break;
           uint8_t* vr = sm + (R + slot) * L::kSlot;
           constexpr int CH = D / 8;  // 16-byte chunks per key
           const int first = max(0, nplain);
+#pragma unroll 1
           for (int idx = ct; idx < (128 - first) * CH; idx += 128) {
             const int key = first + idx / CH, c = idx % CH;
             uint4* p = reinterpret_cast<uint4*>(vr + (c >> 3) * 16384 + key * 128 + (c & 7) * 16);
@@ -764,35 +971,46 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
           if (lane == 0) mbar_arrive(&ctl->tail_done[t & 1]);
           ++t;
         }
-        if (rows_ahead && b == sg.b0) store_rows(j + 1);
-        if (!ok) break;
+        ++g;
+       }
+        if (b == b0) {
+          if (j > 0) {
+            write_rows(j - 1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->seg_empty[(j - 1) % kSegRing]);
+          }
+          if (rows_ahead) load_rows(j + 1);
+        }
+        // (the loads take some microseconds while the copies keep HBM busy; the queries are needed two blocks
+        // before the segment's end)
+        if (rows_ahead && b == min(b0 + 3, max(b1 - 1, b0))) store_rows(j + 1);
+        if (!ok || b + 1 >= b1) break;
       }
-      sg = ahead;
+      if (end) break;
     }
   } else {
     // ---------------------------------------------------------- softmax rows
-    // Two threads per row, as in the prefill: row r in TMEM lane r; half hf takes keys 64 hf ..
+    // Two threads per row, as in the prefill; half hf takes keys 64 hf ..
     // 64 hf + 63 of every block and the head dim's half hf of Q and O.  The two warps of 32
     // rows exchange partials through shared memory (one phase of their barrier each).  Warps whose
-    // rows are all behind the tile's only keep the barriers in step.
+    // lanes hold no row only keep the barriers in step.
     const int sw = warp - 4, hf = sw >> 2, quad = sw & 3;
-    const int r = quad * 32 + lane;
-    const int tl = r / a.G, hh = r - tl * a.G;  // node of the tile, head of the group
+    const int ln = quad * 32 + lane;  // the row's lane
     const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
     int xk = 0;  // next exchange phase
     bool ok = true;
     auto exchange = [&](float mine, float& lo_half, float& hi_half) {
-      ctl->xbuf[xk & 1][r][hf] = mine;
+      ctl->xbuf[xk & 1][ln][hf] = mine;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->xchg[quad]);
-      ok = __all_sync(kAll, (ok && wait_or_abort(&ctl->xchg[quad], xk & 1, abort_flag, a.err)));
-      lo_half = ctl->xbuf[xk & 1][r][0];
-      hi_half = ctl->xbuf[xk & 1][r][1];
+      ok = __all_sync(kAll, (ok && wait_for(&ctl->xchg[quad], xk & 1, abort_flag, a.err)));
+      lo_half = ctl->xbuf[xk & 1][ln][0];
+      hi_half = ctl->xbuf[xk & 1][ln][1];
       ++xk;
     };
     auto read_seg = [&](int j, Seg& sg) {
       const int e = j % kSegRing;
-      ok = __all_sync(kAll, ok && wait_or_abort(&ctl->seg_full[e], (j / kSegRing) & 1, abort_flag, a.err));
+      ok = __all_sync(kAll, ok && wait_for(&ctl->seg_full[e], (j / kSegRing) & 1, abort_flag, a.err));
       sg = {};
       if (ok) sg = ctl->seg[e];
       __syncwarp();
@@ -804,17 +1022,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       read_seg(j, cur);
       if (!ok || cur.b1 == cur.b0) break;
       const int rows = min(a.tile_nodes, cur.n - cur.tile * a.tile_nodes) * a.G;
-      const bool active = quad * 32 < rows;
-      const int own = cur.tile * a.tile_nodes + min(tl, rows / a.G - 1);  // this row's node
-      const long long qrow = (long long)cur.q0 + own;
-      const uint64_t* words = a.mask ? ctl->mask[j % kRowRing][own - cur.tile * a.tile_nodes] : nullptr;
+      const int lane0 = first_lane(rows), r = max(ln - lane0, 0);
+      const bool active = quad * 32 >= lane0;
+      const int tl = min(r / a.G, rows / a.G - 1), own = cur.tile * a.tile_nodes + tl;  // this row's node
+      const uint64_t* words = a.mask ? ctl->mask[j % kRowRing][tl] : nullptr;
       float m = -INFINITY, l = 0.f, vref = 0.f, row_scale = 1.f;
       for (int b = cur.b0; b < cur.b1; ++b, ++g) {
         const int sb = g & 1, se = g % kScaleRing;
         const bool first = b == cur.b0;
         float ov = 1.f, vinv = 1.f;  // factor for this row's O; 1 / vref
         if constexpr (BLK) {         // V weights are taken relative to the largest V scale seen (<= 1)
-          ok = __all_sync(kAll, ok && wait_or_abort(&ctl->sc_full[se], (g / kScaleRing) & 1, abort_flag, a.err));
+          ok = __all_sync(kAll, ok && wait_for(&ctl->sc_full[se], (g / kScaleRing) & 1, abort_flag, a.err));
           float vb = vref;
 #pragma unroll
           for (int i = 0; i < 8; ++i) vb = fmaxf(vb, ctl->sc[se][i].y);
@@ -826,9 +1044,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
         }
         const int j0 = 128 * b + 64 * hf - cur.base;  // this thread's first key, as a node
         const bool masked = j0 + 63 >= 0;
-        ok = __all_sync(kAll, ok && wait_or_abort(&ctl->s_full[sb], (g >> 1) & 1, abort_flag, a.err));
+        ok = __all_sync(kAll, ok && wait_for(&ctl->s_full[sb], (g >> 1) & 1, abort_flag, a.err));
         // (S was made from the segment's queries, so its masks and factors are there too)
-        if (first) row_scale = ctl->row_scale[j % kRowRing][r];
+        if (first) row_scale = ctl->row_scale[j % kRowRing][ln];
         const uint64_t vis = active && masked ? sees64(words, a.words, own, cur.n, j0) : ~0ull;
         const uint32_t sbase = trow + sb * 128;
         if (active) {
@@ -855,15 +1073,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
                 for (int e = 0; e < 32; ++e)
                   if (!(w >> e & 1)) v[e] = -INFINITY;
               }
-              if constexpr (BLK) {
-#pragma unroll
-                for (int hp = 0; hp < 2; ++hp)
-                  if (ctl->sc[se][2 * (2 * hf + cc) + hp].x < 0.f) {  // keys of no finite scale: NaN where seen
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                      if (vis >> (32 * cc + 16 * hp + e) & 1) v[16 * hp + e] = NAN;
-                  }
-              }
               pm[cc][0] = max16(v);
               pm[cc][1] = max16(v + 16);
             }
@@ -886,8 +1095,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
           // of its barrier is never mistaken)
           if (ok && !first && __any_sync(kAll, ov != 1.f)) {
             const int gl = g - 1;
-            ok = __all_sync(kAll, F8 ? wait_or_abort(&ctl->vt_empty[gl & 1], (gl >> 1) & 1, abort_flag, a.err)
-                                     : wait_or_abort(&ctl->kv_empty[gl % R], (gl / R) & 1, abort_flag, a.err));
+            ok = __all_sync(kAll, F8 ? wait_for(&ctl->vt_empty[gl & 1], (gl >> 1) & 1, abort_flag, a.err)
+                                     : wait_for(&ctl->v_empty[gl % R], (gl / R) & 1, abort_flag, a.err));
             if (ok) {
               tc_fence_after();
 #pragma unroll 1
@@ -913,8 +1122,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
 #pragma unroll
               for (int hp = 0; hp < 2; ++hp) {
                 const float2 f2 = make_float2(pf[cc][hp], pf[cc][hp]), nm = make_float2(-mref, -mref);
-                const float sc = BLK ? ctl->sc[se][2 * c + hp].y : 1.f;
-                const float vm = BLK ? fmaxf(sc, 0.f) * vinv : 1.f;
+                const float vm = BLK ? ctl->sc[se][2 * c + hp].y * vinv : 1.f;
                 const float2 vm2 = make_float2(vm, vm);
                 float2 t01 = make_float2(0.f, 0.f), t23 = t01;
                 float* x = v + 16 * hp;
@@ -936,12 +1144,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
                   x[e + 3] = pb.y;
                 }
                 rs += (t01.x + t01.y) + (t23.x + t23.y);
-                if constexpr (BLK)
-                  if (sc < 0.f) {  // values of no finite scale: NaN where seen
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                      if (vis >> (32 * cc + 16 * hp + e) & 1) x[e] = NAN;
-                  }
               }
               uint32_t ph[16], pl[16];  // in V's type: bfloat16 for bfloat16 pools, else binary16
 #pragma unroll
@@ -967,52 +1169,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
         }
         if (!ok) break;
       }
+      // what the output takes besides O
+      if (hf == 0) ctl->fin[j % kRowRing][ln].x = m, ctl->fin[j % kRowRing][ln].y = vref, ctl->fin[j % kRowRing][ln].z = l;
+      else ctl->fin[j % kRowRing][ln].w = l;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->row_free[j % kRowRing]);
-      // The segment's rows: the output, or a partial state.
-      float l0 = 0.f, l1 = 0.f;
-      if (active) exchange(l, l0, l1);
-      const float Ls = l0 + l1;
-      ok = __all_sync(kAll, ok && wait_or_abort(&ctl->o_full, j & 1, abort_flag, a.err));
-      if (ok && active) {
-        tc_fence_after();
-        const bool whole = cur.b0 == 0 && cur.b1 == cur.nblk;
-        const bool odd = *(volatile int*)&ctl->bad[j & 7] == j + 1;
-        const size_t prow = (size_t)(2 * blockIdx.x + (j > 0)) * kRows + r;
-        const float vs = BLK ? vref : 1.f;
-        const float inv = whole ? (Ls > 0.f ? (BLK ? vref : a.v_scale) / Ls : 0.f) : vs;
-        const size_t orow = ((size_t)qrow * a.Hq + (size_t)cur.h * a.G + hh) * D + DH * hf;
-#pragma unroll 1
-        for (int cc = 0; cc < DH / 32; ++cc) {
-          float o[32];
-          tmem_ld32(trow + kOCol + DH * hf + 32 * cc, o);
-          tmem_wait_ld();
-          if (r < rows) {
-            float sc = inv;
-            if (odd) {
-              float x[32];  // (a copy: o stays in registers where nothing is put back)
-#pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = o[e] * inv;
-              sc = 1.f;
-              put_back<KIND, D>(a, cur, qrow, own, DH * hf + 32 * cc, x);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = x[e];
-            }
-            if (whole) store_row32<OUT>(a.out, orow + 32 * cc, o, sc);
-            else store_row32<PA_FP32>(a.ws_o, prow * D + DH * hf + 32 * cc, o, sc);
-          }
-        }
-        if (!whole && hf == 0 && r < rows) a.ws_ml[prow] = make_float2(m, Ls);
-      }
     }
   }
 
   tc_fence_before();
   __syncthreads();
   grid_dependents_launch();
-  if (warp == 1) {
+  if (warp == 0) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(ctl->tmem), "r"(kTmemCols) : "memory");
   }
 }
 
