@@ -93,13 +93,13 @@ struct Ctrl {
   uint64_t seg_full[kSegRing], seg_empty[kSegRing];
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], vt_empty[2];
   uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
-  uint64_t q_ready[2], q_free[2], row_free[kRowRing], o_full, o_free, drain, xchg[4];
+  uint64_t q_ready[2], q_free[2], row_free[kRowRing], o_full, o_free, drain;
   uint64_t tail_ready[2], tail_done[2];  // 16-bit pools: blocks that reach the tree, by their parity
   uint64_t mask[kRowRing][128][PA_TREE_MAX_NODES / 64];  // a tile's nodes' mask words
   float row_scale[kRowRing][128];        // each row's score factor
   float4 fin[kRowRing][128];             // each row's (m, V scale of O, the two threads' l) at the segment's end
   float2 sc[kScaleRing][8];              // block-scaled pools: (K scale, V scale) of each page of a block
-  float xbuf[2][128][2];                 // the two half-row threads' partials
+  float xbuf[2][128][2];                 // the two half-row threads' maxima
   long long warp_sums[kThreads / 32];
   long long start_off;
   int start_seq;
@@ -132,6 +132,7 @@ struct TreeArgs {
   int T, S, Hq, Hkv, G, tile_nodes, max_nodes, words, max_blocks, num_blocks, ctas;
   float qk_scale_log2;  // softmax_scale * log2(e) (* k_scale of a static FP8 pool)
   float v_scale;        // static FP8 pool's V scale, else 1
+  int wide;             // out is 32-byte aligned
   unsigned int* err;
 };
 
@@ -194,6 +195,13 @@ __device__ __forceinline__ uint64_t sees64(const uint64_t* w, int words, int own
 
 __device__ __forceinline__ bool sees(const TreeArgs& a, long long row, int own, int j) {
   return a.mask ? a.mask[row * a.words + (j >> 6)] >> (j & 63) & 1 : j <= own;
+}
+
+// Eight words, 32-byte aligned: a whole sector by one lane.  (A warp's lanes write rows that lie apart, and L1
+// takes a cycle for each line of an instruction.)
+__device__ __forceinline__ void store8(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
 }
 
 // The infinities and NaN among 16 bytes of V, taken out (true if there were any).
@@ -331,8 +339,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       mbar_init(&ctl->sc_full[i], 1);
       mbar_init(&ctl->sc_empty[i], 8);
     }
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) mbar_init(&ctl->xchg[i], 2);
 #pragma unroll 1
     for (int i = 0; i < 8; ++i) ctl->bad[i] = 0;
     mbar_init(&ctl->o_full, 1);
@@ -851,9 +857,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->o_free);
           if (live) {
-            uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow);
+            uint16_t* to = static_cast<uint16_t*>(a.out) + orow;
+            if (a.wide) {
 #pragma unroll
-            for (int c = 0; c < QW / 4; ++c) to[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+              for (int c = 0; c < QW / 8; ++c) store8(to + 16 * c, w + 8 * c);
+            } else {
+#pragma unroll
+              for (int c = 0; c < QW / 4; ++c)
+                reinterpret_cast<uint4*>(to)[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+            }
           }
         } else {
 #pragma unroll 1
@@ -873,7 +885,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
                 for (int e = 0; e < 32; ++e) o[e] = x[e];
               }
               if (whole) store_row32<OUT>(a.out, orow + 32 * c, o, sc);
-              else store_row32<PA_FP32>(a.ws_o, prow * D + 32 * c, o, sc);
+              else {
+                uint32_t w[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * sc);
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) store8(a.ws_o + prow * D + 32 * c + e, w + e);
+              }
             }
           }
           if (live && !whole) a.ws_ml[prow] = make_float2(fin.x, Ls);
@@ -999,14 +1017,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
     const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
     int xk = 0;  // next exchange phase
     bool ok = true;
-    auto exchange = [&](float mine, float& lo_half, float& hi_half) {
-      ctl->xbuf[xk & 1][ln][hf] = mine;
+    // The two warps of 32 rows tell each other their halves' maxima, and whether all is well (a NaN says that it
+    // is not; a maximum of NaN alone counts for nothing).  They meet at a hardware barrier, which has no
+    // time limit: so both leave at a meeting that says so, and a warp that leaves for any other reason, its
+    // list's end among them, comes to one more meeting, which is the other's next one.
+    bool parted = false;
+    auto exchange = [&](float mine) -> float {
+      float* x = &ctl->xbuf[xk & 1][ln][0];
+      x[hf] = !ok ? NAN : mine == mine ? mine : -INFINITY;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->xchg[quad]);
-      ok = __all_sync(kAll, (ok && wait_for(&ctl->xchg[quad], xk & 1, abort_flag, a.err)));
-      lo_half = ctl->xbuf[xk & 1][ln][0];
-      hi_half = ctl->xbuf[xk & 1][ln][1];
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
+      const float other = x[hf ^ 1];
+      ok = __all_sync(kAll, ok && other == other);
+      parted = !ok;
       ++xk;
+      return other;
     };
     auto read_seg = [&](int j, Seg& sg) {
       const int e = j % kSegRing;
@@ -1020,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
     for (int j = 0; ok; ++j) {
       Seg cur;
       read_seg(j, cur);
-      if (!ok || cur.b1 == cur.b0) break;
+      if (!ok || cur.b1 == cur.b0) break;  // (behind the loop: the last meeting)
       const int rows = min(a.tile_nodes, cur.n - cur.tile * a.tile_nodes) * a.G;
       const int lane0 = first_lane(rows), r = max(ln - lane0, 0);
       const bool active = quad * 32 >= lane0;
@@ -1081,9 +1106,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
             else  // one positive factor: the largest product is the largest score times it
               mh = fmaxf(fmax3f(pm[0][0], pm[0][1], pm[1][0]), pm[1][1]) * row_scale;
           }
-          float m0, m1;
-          exchange(mh, m0, m1);
-          const float mx = fmaxf(m0, m1);
+          const float mx = fmaxf(mh, exchange(mh));
+          if (!ok) break;
           if (mx > m + kGrow) {  // the first seen keys, or a maximum that grew
             const float to = mx - kTop, alpha = fast_exp2(m - to);
             l *= alpha;
@@ -1169,12 +1193,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
         }
         if (!ok) break;
       }
+      if (!ok) break;
       // what the output takes besides O
       if (hf == 0) ctl->fin[j % kRowRing][ln].x = m, ctl->fin[j % kRowRing][ln].y = vref, ctl->fin[j % kRowRing][ln].z = l;
       else ctl->fin[j % kRowRing][ln].w = l;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->row_free[j % kRowRing]);
     }
+    if (!parted) exchange(0.f);
   }
 
   tc_fence_before();
@@ -1345,7 +1371,7 @@ Workspace layout(int ctas, int D) {
   Workspace w;
   w.ml = 2 * (size_t)ctas * kRows * D * 4;
   w.jobs = w.ml + 2 * (size_t)ctas * kRows * 8;
-  w.total = w.jobs + (size_t)ctas * 16;
+  w.total = w.jobs + (size_t)ctas * 16 + 16;  // (room to start on 32 bytes)
   return w;
 }
 
@@ -1424,7 +1450,7 @@ int pa_decode_tree(pa_pool* pool, int layer, void* out, int out_dtype, const voi
   a.v = pool->v + (size_t)layer * pool->layer_bytes;
   a.ksc = pool->block_scaled ? layer_scales(pool, pool->k, layer) : nullptr;
   a.vsc = pool->block_scaled ? layer_scales(pool, pool->v, layer) : nullptr;
-  uint8_t* base = static_cast<uint8_t*>(workspace);
+  uint8_t* base = reinterpret_cast<uint8_t*>(((uintptr_t)workspace + 31) & ~(uintptr_t)31);
   a.ws_o = reinterpret_cast<float*>(base);
   a.ws_ml = reinterpret_cast<float2*>(base + ws.ml);
   a.jobs = reinterpret_cast<int4*>(base + ws.jobs);
@@ -1441,6 +1467,7 @@ int pa_decode_tree(pa_pool* pool, int layer, void* out, int out_dtype, const voi
   const bool f8 = d.kv_dtype == PA_FP8_E4M3;
   a.qk_scale_log2 = softmax_scale * 1.4426950408889634f * (f8 ? d.k_scale : 1.f);
   a.v_scale = f8 ? d.v_scale : 1.f;
+  a.wide = ((uintptr_t)out & 31u) == 0;
   a.err = err;
   // one schedule holds at most kBalancedMaxSeqs sequences: larger batches in turn
   for (int s = 0; s < S; s += kBalancedMaxSeqs) {
