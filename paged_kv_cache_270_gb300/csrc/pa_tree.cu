@@ -61,6 +61,9 @@ constexpr int kRowRing = 4;  // segments whose masks and score factors are held
 constexpr float kTop = 7.f, kGrow = 15.f;
 constexpr float kMinFactor = 1.17549435e-38f;  // the smallest normal number
 
+// Tables of at most this many pages are not split: reading one alone takes a CTA no longer than the merge of its pieces.
+constexpr int kWholePages = 32;
+
 enum Kind { K_E4M3 = 0, K_E4M3B = 1, K_BF16 = 2, K_F16 = 3 };
 
 template <int KIND, int D>
@@ -103,7 +106,7 @@ struct Ctrl {
   long long warp_sums[kThreads / 32];
   long long start_off;
   int start_seq;
-  int bad[8];  // segment j has infinities or NaN in its nodes' V or a tile without a finite scale: bad[j % 8] == j + 1
+  int bad[kScaleRing];  // segment j has infinities or NaN in its nodes' V or a tile without a finite scale: bad[j % 8] == j + 1
   uint32_t tmem;
   int abort;
 };
@@ -129,6 +132,7 @@ struct TreeArgs {
   float* ws_o;       // [2 ctas][128][D]
   float2* ws_ml;     // [2 ctas][128] (m in log2 units, l)
   int4* jobs;        // [ctas] units to merge: (sequence, kv head and tile, last CTA, slot)
+  int whole;         // CTAs take whole units
   int T, S, Hq, Hkv, G, tile_nodes, max_nodes, words, max_blocks, num_blocks, ctas;
   float qk_scale_log2;  // softmax_scale * log2(e) (* k_scale of a static FP8 pool)
   float v_scale;        // static FP8 pool's V scale, else 1
@@ -309,23 +313,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
   volatile int* abort_flag = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 0) {
-#pragma unroll 1
-    for (int i = 0; i < kSegRing; ++i) {
+  if (warp == 3) {  // a barrier of each kind per lane
+    const int i = lane;
+    if (i < kSegRing) {
       mbar_init(&ctl->seg_full[i], 1);
       mbar_init(&ctl->seg_empty[i], 15);  // MMA, 2 for masks, 8 softmax, 4 for V
     }
-#pragma unroll 1
-    for (int i = 0; i < kRowRing; ++i) mbar_init(&ctl->row_free[i], 8);
-#pragma unroll 1
-    for (int i = 0; i < R; ++i) {
+    if (i < kScaleRing) {
+      mbar_init(&ctl->sc_full[i], 1);
+      mbar_init(&ctl->sc_empty[i], 8);
+      ctl->bad[i] = 0;
+    }
+    if (i < kRowRing) mbar_init(&ctl->row_free[i], 8);
+    if (i < R) {
       mbar_init(&ctl->k_full[i], 1);
       mbar_init(&ctl->k_empty[i], 1);           // the Q K MMAs
       mbar_init(&ctl->v_full[i], 1);
       mbar_init(&ctl->v_empty[i], F8 ? 4 : 1);  // FP8: the warps that convert it; 16-bit: the P V MMAs
     }
-#pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
+    if (i < 2) {
       mbar_init(&ctl->s_full[i], 1);
       mbar_init(&ctl->p_full[i], F8 ? 12 : 8);  // softmax; FP8: and the four warps that convert V
       mbar_init(&ctl->vt_empty[i], 1);
@@ -334,18 +340,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       mbar_init(&ctl->tail_ready[i], 1);
       mbar_init(&ctl->tail_done[i], 4);
     }
-#pragma unroll 1
-    for (int i = 0; i < kScaleRing; ++i) {
-      mbar_init(&ctl->sc_full[i], 1);
-      mbar_init(&ctl->sc_empty[i], 8);
+    if (i == 0) {
+      mbar_init(&ctl->o_full, 1);
+      mbar_init(&ctl->o_free, 4);
+      mbar_init(&ctl->drain, 1);
+      ctl->abort = 0;
+      ctl->start_seq = -1;
     }
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) ctl->bad[i] = 0;
-    mbar_init(&ctl->o_full, 1);
-    mbar_init(&ctl->o_free, 4);
-    mbar_init(&ctl->drain, 1);
-    ctl->abort = 0;
-    ctl->start_seq = -1;
     fence_barrier_init();
   }
   if (warp == 1 && lane == 0) {
@@ -362,7 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
   // ---------------------------------------------------------------- schedule
   // Positions: a unit of nblk blocks takes kUnitCost + nblk of them, its blocks behind; units in
   // (sequence, kv head, tile) order.  Each CTA takes T positions.
+  // (For short tables, a.whole: a unit takes one position.)
   constexpr int kUnit = L::kUnitCost;
+  auto span_of = [&](const SeqInfo& i) { return a.whole ? 1 : i.nblk + kUnit; };
   const int per = (a.S + kThreads - 1) / kThreads;
   const int s0 = min(a.S, (int)threadIdx.x * per), s1 = min(a.S, s0 + per);
   long long mine = 0;
@@ -370,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
   for (int s = s0; s < s1; ++s) {
     const SeqInfo i = seq_info(a, seq_raw(a, s));
     if (i.bad) record_error(a.err, PA_ERR_BOUNDS);
-    mine += i.units(a.Hkv) * (i.nblk + kUnit);
+    mine += i.units(a.Hkv) * span_of(i);
   }
   long long before, total = 0;
   {
@@ -390,14 +393,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
     }
     before = ahead + x - mine;
   }
-  const long long T = max((total + a.ctas - 1) / a.ctas, (long long)kUnit + 1);
+  const long long T = max((total + a.ctas - 1) / a.ctas, a.whole ? 1ll : (long long)kUnit + 1);
   const long long pos0 = (long long)blockIdx.x * T, pos_end = min(total, pos0 + T);
   if (pos0 < total && before <= pos0 && pos0 < before + mine) {
     long long cum = before;
   #pragma unroll 1
   for (int s = s0; s < s1; ++s) {
       const SeqInfo i = seq_info(a, seq_raw(a, s));
-      const long long c = i.units(a.Hkv) * (i.nblk + kUnit);
+      const long long c = i.units(a.Hkv) * span_of(i);
       if (pos0 < cum + c) {
         ctl->start_seq = s;
         ctl->start_off = pos0 - cum;
@@ -424,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
     int seq = ctl->start_seq;
     SeqInfo info = seq_info(a, seq_raw(a, seq));
     SeqRaw ahead = seq_raw(a, seq + 1);
-    int span = info.nblk + kUnit;
+    int span = span_of(info);
     long long u = ctl->start_off / span;
     int v = (int)(ctl->start_off - u * span);
     long long pos = pos0;
@@ -438,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
           if (++seq >= a.S) break;
           info = seq_info(a, ahead);
           ahead = seq_raw(a, seq + 1);
-          span = info.nblk + kUnit;
+          span = span_of(info);
           u = 0;
           v = 0;
         }
@@ -447,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
           break;
         }
         const int take = (int)min((long long)(span - v), pos_end - pos);
-        const int b0 = max(0, v - kUnit), b1 = max(0, v + take - kUnit);
+        const int b0 = a.whole ? 0 : max(0, v - kUnit), b1 = a.whole ? info.nblk : max(0, v + take - kUnit);
         const long long ustart = pos - v;
         const int unit = (int)u, nblk = info.nblk;
         pos += take;
@@ -833,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       const int r = qr - first_lane(rows), tl = r / a.G, hh = r - tl * a.G;
       if ((qr | 31) >= first_lane(rows)) {  // (whole warps)
         const bool live = r >= 0 && r < rows, whole = sg.b0 == 0 && sg.b1 == sg.nblk;
-        const bool odd = *(volatile int*)&ctl->bad[j & 7] == j + 1;
+        const bool odd = *(volatile int*)&ctl->bad[j % kScaleRing] == j + 1;
         const float4 fin = ctl->fin[j % kRowRing][qr];
         const float Ls = fin.z + fin.w;
         const float inv = whole ? (Ls > 0.f ? (BLK ? fin.y : a.v_scale) / Ls : 0.f) : BLK ? fin.y : 1.f;
@@ -922,6 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
         ok = __all_sync(kAll, wait_for(&ctl->seg_full[(j + 1) % kSegRing], ((j + 1) / kSegRing) & 1, abort_flag, a.err));
         if (!ok) break;
         rows_ahead = ctl->seg[(j + 1) % kSegRing].b1 > ctl->seg[(j + 1) % kSegRing].b0;
+        if (rows_ahead) load_rows(j + 1);
       }
       for (int b = b0;; ++b) {
        if (b < b1) {
@@ -954,7 +958,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
             *reinterpret_cast<uint4*>(row + ((c0 ^ (key & 7)) << 4)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
             *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (key & 7)) << 4)) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
           }
-          if (odd) ctl->bad[j & 7] = j + 1;
+          if (odd) ctl->bad[j % kScaleRing] = j + 1;
           fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) {
@@ -983,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
               }
             }
           }
-          if (odd) ctl->bad[j & 7] = j + 1;
+          if (odd) ctl->bad[j % kScaleRing] = j + 1;
           fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->tail_done[t & 1]);
@@ -991,17 +995,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
         }
         ++g;
        }
-        if (b == b0) {
-          if (j > 0) {
-            write_rows(j - 1);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->seg_empty[(j - 1) % kSegRing]);
-          }
-          if (rows_ahead) load_rows(j + 1);
+        // The next queries: between the blocks of a long segment (their loads take some microseconds while the copies
+        // keep HBM busy), at once in a short one, whose end needs them soon.
+        if (rows_ahead && b == (b1 - b0 < 4 ? b0 : b0 + 3)) store_rows(j + 1);
+        if (b == b0 && j > 0) {
+          write_rows(j - 1);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->seg_empty[(j - 1) % kSegRing]);
         }
-        // (the loads take some microseconds while the copies keep HBM busy; the queries are needed two blocks
-        // before the segment's end)
-        if (rows_ahead && b == min(b0 + 3, max(b1 - 1, b0))) store_rows(j + 1);
         if (!ok || b + 1 >= b1) break;
       }
       if (end) break;
@@ -1284,7 +1285,7 @@ struct Launch {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_kernel<KIND, D, OUT, PSPLIT>, a, *tk, *tv);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || a.whole) return e;
     cfg.gridDim = dim3(a.ctas, 8);
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
@@ -1468,6 +1469,7 @@ int pa_decode_tree(pa_pool* pool, int layer, void* out, int out_dtype, const voi
   a.qk_scale_log2 = softmax_scale * 1.4426950408889634f * (f8 ? d.k_scale : 1.f);
   a.v_scale = f8 ? d.v_scale : 1.f;
   a.wide = ((uintptr_t)out & 31u) == 0;
+  a.whole = max_blocks_per_seq <= kWholePages;
   a.err = err;
   // one schedule holds at most kBalancedMaxSeqs sequences: larger batches in turn
   for (int s = 0; s < S; s += kBalancedMaxSeqs) {

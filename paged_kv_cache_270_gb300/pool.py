@@ -219,21 +219,23 @@ class KVPool:
 
     def _rope_args(self, q, k, v, positions, slot_mapping, q_out, n_axes, stream):
         """Checks what the rotary writes share; returns q_out and the C call's last arguments."""
-        qs = _token_rows(q, "q", self.in_dtype, self.device)
-        ks = _token_rows(k, "k", self.in_dtype, self.device)
-        vs = _token_rows(v, "v", self.in_dtype, self.device)
-        _all_need(self.device, (positions, "positions", torch.int32), (slot_mapping, "slot_mapping", torch.int64))
-        T, Hq, D = q.shape
+        dt, dev = self.in_dtype, self.device
+        qs = _token_rows(q, "q", dt, dev)
+        ks = _token_rows(k, "k", dt, dev)
+        vs = _token_rows(v, "v", dt, dev)
+        _all_need(dev, (positions, "positions", torch.int32), (slot_mapping, "slot_mapping", torch.int64))
+        shape = q.shape
+        T, Hq, D = shape
         kv = (T, self.n_kv_heads, self.head_dim)
         if D != self.head_dim or k.shape != kv or v.shape != kv:
             raise ValueError("q must be [T, n_q_heads, head_dim], k and v [T, n_kv_heads, head_dim]")
         if positions.numel() != n_axes * T or slot_mapping.numel() != T:
             raise ValueError("positions and slot_mapping must hold one entry per token (positions: and axis)")
         if q_out is None:
-            q_out = self._new((T, Hq, D), q.dtype, stream)
+            q_out = self._new(shape, dt, stream)
         else:
-            _need(q_out, "q_out", self.in_dtype, self.device)
-            if q_out.shape != q.shape:
+            _all_need(dev, (q_out, "q_out", dt))
+            if q_out.shape != shape:
                 raise ValueError("q_out must have q's shape")
         return q_out, (q.data_ptr(), qs, q_out.data_ptr(), Hq, k.data_ptr(), ks, v.data_ptr(), vs,
                        positions.data_ptr(), slot_mapping.data_ptr(), T)
@@ -248,6 +250,14 @@ class KVPool:
         self._launch(N.pa_rope_and_cache, (self.handle, layer, rope, *args), stream)
         return q_out
 
+    def _head_weight(self, w, name, heads) -> int:
+        """The address of a norm's weights, [head_dim] or [heads, head_dim]."""
+        _all_need(self.device, (w, name, self.in_dtype))
+        shape, D = w.shape, self.head_dim
+        if shape != (D,) and shape != (heads, D):
+            raise ValueError(f"{name} must be [head_dim] or [heads, head_dim]")
+        return w.data_ptr()
+
     def norm_rope_and_cache(self, rope: N.pa_rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                             positions: torch.Tensor, slot_mapping: torch.Tensor,
                             q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
@@ -259,21 +269,19 @@ class KVPool:
         side is not normalised).  With `axes` (``make_rope_axes``) positions is [n_axes, T]."""
         n_axes = axes.n_axes if axes is not None else 1
         q_out, args = self._rope_args(q, k, v, positions, slot_mapping, q_out, n_axes, stream)
-        per_head = False
-        for w, name, heads in ((q_weight, "q_weight", q.shape[1]), (k_weight, "k_weight", self.n_kv_heads)):
-            if w is None:
-                continue
-            _need(w, name, self.in_dtype, self.device)
-            if w.shape not in ((self.head_dim,), (heads, self.head_dim)):
-                raise ValueError(f"{name} must be [head_dim] or [heads, head_dim]")
-            per_head = w.dim() == 2
-        if q_weight is not None and k_weight is not None and q_weight.dim() != k_weight.dim():
-            raise ValueError("q_weight and k_weight must both be [head_dim] or both [heads, head_dim]")
+        qw = kw = per_head = 0
+        if q_weight is not None:
+            qw = self._head_weight(q_weight, "q_weight", q.shape[1])
+            per_head = q_weight.dim() - 1
+        if k_weight is not None:
+            kw = self._head_weight(k_weight, "k_weight", self.n_kv_heads)
+            if q_weight is not None and k_weight.dim() - 1 != per_head:
+                raise ValueError("q_weight and k_weight must both be [head_dim] or both [heads, head_dim]")
+            per_head = k_weight.dim() - 1
         if n_axes > 1 and (positions.dim() != 2 or positions.shape[0] != n_axes):
             raise ValueError("positions must be [n_axes, T]")
-        self._launch(N.pa_norm_rope_and_cache,
-                     (self.handle, layer, rope, axes, q_weight.data_ptr() if q_weight is not None else 0,
-                      k_weight.data_ptr() if k_weight is not None else 0, per_head, eps, weight_offset, *args), stream)
+        self._launch(N.pa_norm_rope_and_cache, (self.handle, layer, rope, axes, qw, kw, per_head, eps, weight_offset, *args),
+                     stream)
         return q_out
 
     def copy_blocks(self, pairs: torch.Tensor, layer: int = 0, stream=None) -> None:
