@@ -725,7 +725,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
     // ---------------------------------------------------------- V, queries and output
     const int ct = threadIdx.x - 12 * 32;  // 0 .. 127: a key of V, a row of Q and O
     const int qr = ct;
-    constexpr int QW = D / 2;  // 32-bit words of an output row
     const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     bool ok = true;
     // A thread's own row of queries of segment j.  FP8: the warps are busy with V, so the row is copied to shared
@@ -845,63 +844,55 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
         const long long orow = (qrow * a.Hq + (long long)sg.h * a.G + hh) * D;
         const long long prow = (long long)(2 * blockIdx.x + (j > 0)) * kRows + r;
         const uint32_t oc = trow + kOCol;
-        if (OUT != PA_FP32 && whole && !odd) {
-          // packed as they come, so that O is free before the first store
-          uint32_t w[QW];
+        // (A loop, though O is free only behind it: straight code that reads all of O first, run once a
+        // segment, is 1-2% slower over the measured batches.)
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          tmem_ld32(oc + 32 * c, o);
+          tmem_wait_ld();
+          if (!live) continue;
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            float o[32];
-            tmem_ld32(oc + 32 * c, o);
-            tmem_wait_ld();
+          for (int e = 0; e < 32; ++e) o[e] *= inv;
+          if (odd) {
+            float x[32];  // (a copy: o stays in registers where nothing is put back)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[16 * c + e] = pack2<OUT == PA_BF16>(o[2 * e] * inv, o[2 * e + 1] * inv);
+            for (int e = 0; e < 32; ++e) x[e] = o[e];
+            put_back<KIND, D>(a, sg, qrow, own, 32 * c, x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = x[e];
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->o_free);
-          if (live) {
-            uint16_t* to = static_cast<uint16_t*>(a.out) + orow;
-            if (a.wide) {
+          uint32_t w[32];
+          if (OUT != PA_FP32 && whole) {
 #pragma unroll
-              for (int c = 0; c < QW / 8; ++c) store8(to + 16 * c, w + 8 * c);
+            for (int e = 0; e < 16; ++e) w[e] = pack2<OUT == PA_BF16>(o[2 * e], o[2 * e + 1]);
+            uint16_t* to = static_cast<uint16_t*>(a.out) + orow + 32 * c;
+            if (a.wide) {
+              store8(to, w);
+              store8(to + 16, w + 8);
             } else {
 #pragma unroll
-              for (int c = 0; c < QW / 4; ++c)
-                reinterpret_cast<uint4*>(to)[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+              for (int e = 0; e < 4; ++e)
+                reinterpret_cast<uint4*>(to)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            }
+          } else {
+            float* to = whole ? static_cast<float*>(a.out) + orow + 32 * c : a.ws_o + prow * D + 32 * c;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e]);
+            if (a.wide || !whole) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) store8(to + e, w + e);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                reinterpret_cast<uint4*>(to)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
             }
           }
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            float o[32];
-            tmem_ld32(oc + 32 * c, o);
-            tmem_wait_ld();
-            if (live) {
-              float sc = inv;
-              if (odd) {
-                float x[32];  // (a copy: o stays in registers where nothing is put back)
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = o[e] * inv;
-                sc = 1.f;
-                put_back<KIND, D>(a, sg, qrow, own, 32 * c, x);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = x[e];
-              }
-              if (whole) store_row32<OUT>(a.out, orow + 32 * c, o, sc);
-              else {
-                uint32_t w[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * sc);
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) store8(a.ws_o + prow * D + 32 * c + e, w + e);
-              }
-            }
-          }
-          if (live && !whole) a.ws_ml[prow] = make_float2(fin.x, Ls);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->o_free);
         }
+        if (live && !whole) a.ws_ml[prow] = make_float2(fin.x, Ls);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->o_free);
       } else {
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->o_free);
