@@ -135,6 +135,77 @@ def test_many_sequences():
     S = 4500
     b = Batch("bf16", 1, 2, 64, [3 + s % 5 for s in range(S)], [1 + s % 3 for s in range(S)], seed=8)
     b.check(b.run())
+    assert b.pool.device_error() == N.PA_OK
+    b.pool.close()
+
+
+@pytest.mark.parametrize("kv", KINDS)
+def test_infinite_and_nan_queries(kv):
+    """A query that holds an infinity or a NaN spoils its own row alone."""
+    b = Batch(kv, 2, 4, 128, [300, 20], [9, 20], seed=13)
+    want = b.run()
+    b.q[2, 1, 5], b.q[11, 6, 100], b.q[12, 0, 0] = math.inf, -math.inf, math.nan
+    out = b.run()
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    for t, h in ((2, 1), (11, 6), (12, 0)):
+        bad[t, h] = True
+        assert out[t, h].isnan().all()
+    assert torch.equal(out[~bad], want[~bad])
+    b.pool.close()
+
+
+def test_two_streams_at_once():
+    """Two calls that may overlap, each with a workspace of its own."""
+    b = Batch("fp8_e4m3", 8, 8, 128, [4000] * 6, [16] * 6, seed=14)
+    c = Batch("bf16", 8, 4, 64, [3000, 1, 700], [16, 1, 30], seed=15)
+    want = b.run(), c.run()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = b.run(stream=s1), c.run(stream=s2)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert b.pool.device_error() == N.PA_OK
+    b.pool.close()
+    c.pool.close()
+
+
+@pytest.mark.parametrize("off", [0, 8, 16])
+def test_output_alignment(off):
+    """An output that starts on 16 bytes but not on 32."""
+    b = Batch("bf16", 2, 4, 128, [2000, 300], [16, 30], seed=16)
+    want = b.run(), b.run(out_dtype=torch.float32)
+    for w in want:
+        n = off * 2 // w.element_size()
+        buf = torch.zeros(w.numel() + n, dtype=w.dtype, device="cuda")
+        out = buf[n:].view(w.shape)
+        b.run(out=out)
+        assert torch.equal(out, w)
+    b.pool.close()
+
+
+@pytest.mark.parametrize("kv", KINDS)
+def test_lost_tiles(kv):
+    """A page of NaN in the history reaches every node; in block-scaled pools, a scale of NaN or infinity
+    reaches exactly the nodes that see a token of its tile."""
+    b = Batch(kv, 2, 4, 128, [200, 70], [30, 40], seed=17)
+    want = b.run()
+    if b.pool.block_scaled:
+        for which, s, page, val in (("k", 0, 12, math.nan), ("v", 1, 3, math.inf)):
+            b.pool.scale_view(which)[int(b.tables_np[s, page]), 1] = val
+        out = b.run()
+        for s, page in ((0, 12), (1, 3)):
+            base = b.ctx[s] - b.sizes[s]
+            for r in range(b.sizes[s]):
+                row = int(b.q_start_np[s]) + r
+                seen = any(t < base or b.sees[s][r, t - base] for t in range(16 * page, min(16 * page + 16, b.ctx[s])))
+                assert out[row, 4:].isnan().all() if seen else torch.equal(out[row], want[row]), (s, r)
+                assert torch.equal(out[row, :4], want[row, :4])  # the other kv head
+    else:
+        b.pool.layer_view("v")[int(b.tables_np[0, 2]), 1] = 0x7F if b.pool.elem_bytes == 1 else 0xFF
+        out = b.run()
+        assert out[:30, 4:].isnan().all()
+        assert torch.equal(out[:30, :4], want[:30, :4]) and torch.equal(out[30:], want[30:])
     b.pool.close()
 
 
