@@ -598,6 +598,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       const uint32_t k_lo = ((smem_addr(sm) & 0x3FFFFu) >> 4) | (1u << 16);
       const uint32_t v_lo = ((smem_addr(sm + (F8 ? L::kVT : R * L::kSlot)) & 0x3FFFFu) >> 4) | ((16384u >> 4) << 16);
       // cursors over the blocks: Q K^T, two blocks ahead of P V
+      // (a block's place in the ring of three and that round's parity are counted along: a remainder by three costs
+      // this thread some 50 cycles)
+      int kslot = 0, kpar = 0, vslot = 0, vpar = 0;
       int gq = 0, jq = -1, bq = 0, bq1 = 0, qbase = 0, tq = 0;
       bool q_end = false;
       int gp = 0, jp = -1, bp = 0, bp0 = 0, bp1 = 0, pbase = 0, tp = 0;
@@ -621,8 +624,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
           }
           if (!wait_for(&ctl->q_ready[jq & 1], (jq >> 1) & 1, abort_flag, a.err)) return false;
         }
-        const int slot = gq % R, sb = gq & 1;
-        if (!k_ready && !wait_for(&ctl->k_full[slot], (gq / R) & 1, abort_flag, a.err)) return false;
+        const int slot = kslot, sb = gq & 1;
+        if (!k_ready && !wait_for(&ctl->k_full[slot], kpar, abort_flag, a.err)) return false;
         k_ready = false;
         tc_fence_after();
         if constexpr (!F8)
@@ -648,6 +651,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
         mma_commit(&ctl->s_full[sb]);
         mma_commit(&ctl->k_empty[slot]);
         ++gq;
+        if (++kslot == R) {
+          kslot = 0;
+          kpar ^= 1;
+        }
         if (++bq == bq1) mma_commit(&ctl->q_free[jq & 1]);  // the segment's queries are read
         return true;
       };
@@ -668,15 +675,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
         const int vb = gp & 1;
         if (!p_ready && !wait_for(&ctl->p_full[vb], (gp >> 1) & 1, abort_flag, a.err)) break;
         if constexpr (!F8) {
-          if (!v_ready && !wait_for(&ctl->v_full[gp % R], (gp / R) & 1, abort_flag, a.err)) break;
+          if (!v_ready && !wait_for(&ctl->v_full[vslot], vpar, abort_flag, a.err)) break;
           if (128 * bp + 127 >= pbase) {
             if (!wait_for(&ctl->tail_done[tp & 1], (tp >> 1) & 1, abort_flag, a.err)) break;
             ++tp;
           }
         }
-        k_ready = mbar_test(&ctl->k_full[gq % R], (gq / R) & 1);
+        k_ready = mbar_test(&ctl->k_full[kslot], kpar);
         tc_fence_after();
-        const uint32_t lo = v_lo + (uint32_t)(F8 ? vb * (L::kVTBlock >> 4) : (gp % R) * (L::kSlot >> 4));
+        const uint32_t lo = v_lo + (uint32_t)(F8 ? vb * (L::kVTBlock >> 4) : vslot * (L::kSlot >> 4));
         const uint32_t pcol = tmem + vb * 128, add = bp > bp0;
 #pragma unroll
         for (int part = 0; part < (PSPLIT ? 2 : 1); ++part)
@@ -685,11 +692,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
             mma_lo<false>(tmem + kOCol, pcol + 32 * (k >> 1) + 16 * part + 8 * (k & 1), lo + k * (2048 >> 4), kHi128, kIdescPV,
                           part | k ? 1u : add);
         if constexpr (F8) mma_commit(&ctl->vt_empty[vb]);
-        else mma_commit(&ctl->v_empty[gp % R]);
+        else mma_commit(&ctl->v_empty[vslot]);
         ++gp;
+        if (++vslot == R) {
+          vslot = 0;
+          vpar ^= 1;
+        }
         if (++bp == bp1) mma_commit(&ctl->o_full);
         p_ready = mbar_test(&ctl->p_full[gp & 1], (gp >> 1) & 1);
-        if constexpr (!F8) v_ready = mbar_test(&ctl->v_full[gp % R], (gp / R) & 1);
+        if constexpr (!F8) v_ready = mbar_test(&ctl->v_full[vslot], vpar);
        }
         if (!issue_qk()) break;
       }
@@ -901,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
     };
     // Segment j's first block of V, then the output of j - 1 (whose last products are done about then), and
     // between j's other blocks the queries of j + 1.  A description is given back with its output.
-    int g = 0, t = 0;
+    int g = 0, t = 0, vs = 0, vp = 0;  // (vs, vp: the block's place in its ring, that round's parity)
     for (int j = -1; ok; ++j) {
       int b0 = 0, b1 = 0, base = 0, ctx = 0;
       if (j >= 0) {
@@ -921,13 +932,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       }
       for (int b = b0;; ++b) {
        if (b < b1) {
-        const int slot = g % R;
+        const int slot = vs;
         const int nvalid = min(128, ctx - 128 * b);  // keys behind the context: zero
         const int nplain = base - 128 * b;           // keys from here on are nodes
         bool odd = false;                            // infinities or NaN among them
         if constexpr (F8) {
           const int half = g & 1;
-          ok = __all_sync(kAll, wait_for(&ctl->v_full[slot], (g / R) & 1, abort_flag, a.err));
+          ok = __all_sync(kAll, wait_for(&ctl->v_full[slot], vp, abort_flag, a.err));
           if (ok && g >= 2) ok = __all_sync(kAll, wait_for(&ctl->vt_empty[half], ((g >> 1) - 1) & 1, abort_flag, a.err));
           if (!ok) break;
           const uint8_t* vr = sm + (R + slot) * L::kSlot;
@@ -960,7 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
         } else if (nplain < 128) {
           // read in place: rows behind the context are zeroed, nodes' rows looked through
           ok = __all_sync(kAll, wait_for(&ctl->tail_ready[t & 1], (t >> 1) & 1, abort_flag, a.err));
-          ok = ok && __all_sync(kAll, wait_for(&ctl->v_full[slot], (g / R) & 1, abort_flag, a.err));
+          ok = ok && __all_sync(kAll, wait_for(&ctl->v_full[slot], vp, abort_flag, a.err));
           if (!ok) break;
           uint8_t* vr = sm + (R + slot) * L::kSlot;
           constexpr int CH = D / 8;  // 16-byte chunks per key
@@ -986,6 +997,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
           ++t;
         }
         ++g;
+        if (++vs == R) {
+          vs = 0;
+          vp ^= 1;
+        }
        }
         // The next queries: between the blocks of a long segment (their loads take some microseconds while the copies
         // keep HBM busy), at once in a short one, whose end needs them soon.
