@@ -1223,7 +1223,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
 
 // Joins the pieces of units that several CTAs shared: out = sum_i 2^(m_i - M) O_i / sum_i
 // 2^(m_i - M) l_i.  Piece i > 0 of CTA c's unit is the first segment of CTA c + i.  A warp
-// per row, all of a row's head dim in 16-byte loads.
+// per row: a lane per piece for the weights, then the pieces' rows, whose loads do not
+// wait for each other (one sequence of 131072 tokens, one kv head, 152 pieces: 50 us with both
+// kernels; a running maximum from piece to piece 179).
 template <int D, int OUT>
 __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeArgs a) {
   grid_dependency_wait();
@@ -1235,28 +1237,47 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeArgs a) {
   const int h = job.y / info.tiles, tile = job.y - h * info.tiles;
   const int rows = min(a.tile_nodes, info.n - tile * a.tile_nodes) * a.G;
   const int pieces = job.z - c0 + 1;
-  constexpr int LPR = D / 4;        // lanes of a row
-  constexpr int RPW = 32 / LPR;     // rows of a warp
+  constexpr int LPR = D / 4, PPW = 32 / LPR;  // lanes of a row; pieces that a warp reads at once
   const int sub = lane / LPR, d4 = lane % LPR;
-  for (int r = (blockIdx.y * 4 + (threadIdx.x >> 5)) * RPW + sub; r < rows; r += gridDim.y * 4 * RPW) {
+  for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 4) {
     auto prow = [&](int i) { return (size_t)(i == 0 ? job.w : 2 * (c0 + i)) * kRows + r; };
-    float M = -INFINITY;
-    for (int i = 0; i < pieces; ++i) M = fmaxf(M, a.ws_ml[prow(i)].x);
+    float2 ml = make_float2(-INFINITY, 0.f);  // of the piece whose number is the lane's
+    if (lane < pieces) ml = a.ws_ml[prow(lane)];
+    float M = ml.x;
+    for (int i = lane + 32; i < pieces; i += 32) M = fmaxf(M, a.ws_ml[prow(i)].x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, off));
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float Ls = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < pieces; ++i) {
-      const float2 ml = a.ws_ml[prow(i)];
-      const float4 x = reinterpret_cast<const float4*>(a.ws_o)[prow(i) * (D / 4) + d4];
-      // a piece without any seen key holds zeros
-      const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : fast_exp2(ml.x - M);
-      if (w != 0.f) {
-        Ls += w * ml.y;
-        o.x += w * x.x;
-        o.y += w * x.y;
-        o.z += w * x.z;
-        o.w += w * x.w;
+    for (int base = 0; base < pieces; base += 32) {
+      float w = 0.f;
+      if (base + lane < pieces) {
+        if (base > 0) ml = a.ws_ml[prow(base + lane)];
+        // a piece without any seen key holds zeros, or the NaN of a score
+        w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : fast_exp2(ml.x - M);
+        if (w != 0.f) Ls += w * ml.y;
       }
+      const int cnt = min(32, pieces - base);
+#pragma unroll 8
+      for (int i = 0; i < cnt; i += PPW) {
+        const float wi = __shfl_sync(kAll, w, (i + sub) & 31);
+        const float4 x = reinterpret_cast<const float4*>(a.ws_o)[prow(base + min(i + sub, cnt - 1)) * (D / 4) + d4];
+        if (i + sub < cnt && wi != 0.f) {
+          o.x += wi * x.x;
+          o.y += wi * x.y;
+          o.z += wi * x.z;
+          o.w += wi * x.w;
+        }
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) Ls += __shfl_xor_sync(kAll, Ls, off);
+    if constexpr (PPW == 2) {
+      o.x += __shfl_xor_sync(kAll, o.x, 16);
+      o.y += __shfl_xor_sync(kAll, o.y, 16);
+      o.z += __shfl_xor_sync(kAll, o.z, 16);
+      o.w += __shfl_xor_sync(kAll, o.w, 16);
+      if (sub) continue;
     }
     const float f = Ls > 0.f ? a.v_scale / Ls : Ls == 0.f ? 0.f : NAN;
     const int node = r / a.G, hh = r - node * a.G;
@@ -1294,7 +1315,9 @@ struct Launch {
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_kernel<KIND, D, OUT, PSPLIT>, a, *tk, *tv);
     if (e != cudaSuccess || a.whole) return e;
-    cfg.gridDim = dim3(a.ctas, 8);
+    // Units of eight pieces and more have a warp per row; otherwise a warp takes two, as the CTAs that find
+    // no unit cost more (one sequence of 131072 tokens and one kv head 50 us, 73 with 16; 64 x 2048 74.5, 75.4 with 32).
+    cfg.gridDim = dim3(a.ctas, 8ll * a.S * a.Hkv <= a.ctas ? kRows / 4 : kRows / 8);
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, OUT>, a);
