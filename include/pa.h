@@ -640,7 +640,7 @@ PA_API int pa_decode_tree_workspace_bytes(const pa_pool* pool, int n_q_heads, in
  *   out, q         device [T][n_q_heads][head_dim]; sequence s's nodes are rows
  *                  q_start[s] .. q_start[s+1] - 1; types as for pa_decode.  Rows behind
  *                  q_start[S] are padding: neither read nor written
- *   T              rows of q and out
+ *   T              rows of q and out, which must not overlap
  *   q_start_dev    device int32 [S + 1], non-decreasing, at most T, q_start[0] >= 0
  *   ctx_lens_dev   device int32 [S]: tokens of each sequence in the cache, its nodes included:
  *                  node j is token ctx - nodes + j
@@ -660,8 +660,8 @@ PA_API int pa_decode_tree_workspace_bytes(const pa_pool* pool, int n_q_heads, in
  * one above T, a context shorter than its nodes or longer than 16 * max_blocks_per_seq
  * is skipped (its rows are not written), a table entry outside [0, num_blocks) gives
  * an undefined result for its sequence; both set PA_ERR_BOUNDS in the device error
- * word.  PA_ERR_UNSUPPORTED for tables of more than 2^27 - 256 blocks.  Equal inputs give
- * equal bits on equal devices. */
+ * word.  PA_ERR_UNSUPPORTED for more than 65535 sequences or tables of more than 2^27 - 256
+ * blocks.  Equal inputs give equal bits on equal devices. */
 PA_API int pa_decode_tree(pa_pool* pool, int layer, void* out, int out_dtype, const void* q, int T,
                           const int32_t* q_start_dev, const int32_t* block_tables_dev,
                           int max_blocks_per_seq, const int32_t* ctx_lens_dev, int S, int n_q_heads,
@@ -676,7 +676,7 @@ PA_API int pa_decode_tree(pa_pool* pool, int layer, void* out, int out_dtype, co
  *   path_lens_dev  device int32 [S]: 0 .. max_path
  *   q_start_dev, block_tables_dev, ctx_lens_dev  as for pa_decode_tree
  *   new_lens_dev   device int32 [S], out: the context length after it,
- *                  ctx - nodes + path_len; another buffer than ctx_lens_dev
+ *                  ctx - nodes + path_len; another buffer than the inputs
  * 16-bit and FP8 pools move the bytes.  In PA_FP8_E4M3_BLOCK pools a destination tile's
  * scale grows to s = max(s_old, fl32(m / 448)), m the largest |fl32(decode(c) * s_src)| of
  * the rows that come from other tiles; if it grew, the codes of the tile's 16 rows become
@@ -687,7 +687,7 @@ PA_API int pa_decode_tree(pa_pool* pool, int layer, void* out, int out_dtype, co
  * [0, max_path] or above the nodes, or lengths that pa_decode_tree would skip
  * set PA_ERR_BOUNDS; nothing of that sequence moves, and new_lens gets its context
  * length unchanged.  A table entry outside [0, num_blocks) sets PA_ERR_BOUNDS, and the rows in
- * that block are skipped. */
+ * that block are skipped.  PA_ERR_UNSUPPORTED as for pa_decode_tree. */
 PA_API int pa_tree_accept(pa_pool* pool, int layer, int n_layers, const int32_t* paths_dev,
                           int max_path, const int32_t* path_lens_dev, const int32_t* q_start_dev,
                           const int32_t* block_tables_dev, int max_blocks_per_seq,

@@ -273,8 +273,12 @@ int pa_tree_accept(pa_pool* pool, int layer, int n_layers, const int32_t* paths_
   if (S == 0) return PA_OK;
   if (!path_lens_dev || !q_start_dev || !block_tables_dev || !ctx_lens_dev || !new_lens_dev || (max_path > 0 && !paths_dev))
     return fail(PA_ERR_INVALID, "null argument");
-  if (new_lens_dev == ctx_lens_dev)
-    return fail(PA_ERR_INVALID, "new_lens must be another buffer than ctx_lens, which every head reads");
+  const size_t lens_bytes = (size_t)S * 4;
+  if (overlap(new_lens_dev, lens_bytes, ctx_lens_dev, lens_bytes) ||
+      overlap(new_lens_dev, lens_bytes, path_lens_dev, lens_bytes) ||
+      overlap(new_lens_dev, lens_bytes, q_start_dev, lens_bytes + 4) ||
+      overlap(new_lens_dev, lens_bytes, paths_dev, lens_bytes * max_path))
+    return fail(PA_ERR_INVALID, "new_lens must be another buffer than the inputs, which every head reads");
   unsigned int* err = device_error_word();
   if (!err) return PA_ERR_CUDA;
   AcceptArgs a = {};

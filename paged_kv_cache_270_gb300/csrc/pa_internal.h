@@ -94,6 +94,12 @@ int prefill_tc_set_wait_limit(unsigned long long ns);  // and the tree's
 int weights_set_wait_limit(unsigned long long ns);
 int tree_set_wait_limit(unsigned long long ns);
 
+// Whether two ranges of bytes meet.
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na && nb && x < y + nb && y < x + na;
+}
+
 // Argument checks of the decode entry points.
 int in_dtype_of(int kv_dtype);
 int check_shape(const pa_pool* pool, int S, int n_q_heads, int max_blocks);

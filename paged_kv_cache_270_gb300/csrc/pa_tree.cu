@@ -1451,6 +1451,9 @@ int pa_decode_tree(pa_pool* pool, int layer, void* out, int out_dtype, const voi
   st = check_decode_ptrs(out, q, block_tables_dev, ctx_lens_dev);
   if (st) return st;
   if (!q_start_dev) return fail(PA_ERR_INVALID, "null argument");
+  const size_t elems = (size_t)T * n_q_heads * pool->desc.head_dim;
+  if (overlap(out, elems * (out_dtype == PA_FP32 ? 4 : 2), q, elems * 2))
+    return fail(PA_ERR_INVALID, "out must not overlap q");
   if ((uintptr_t)tree_mask_dev & 7u) return fail(PA_ERR_INVALID, "tree_mask must be 8-byte aligned");
   if (!workspace || ((uintptr_t)workspace & 15u))
     return fail(PA_ERR_INVALID, "a 16-byte aligned workspace is needed");

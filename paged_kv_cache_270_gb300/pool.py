@@ -465,7 +465,7 @@ class KVPool:
         q [T, Hq, D] are sequence s's nodes, the last ones of its ctx_lens[s] cached tokens.  Each
         attends to the history in front of them and to the nodes whose bits are set in its row of
         `mask`, int64 [T, ceil(max_nodes / 64)] (None: those before it and itself).  Rows of q
-        and out behind q_start[S] are neither read nor written."""
+        and out behind q_start[S] are neither read nor written; out must not overlap q."""
         dev = self.device
         _all_need(dev, (q, "q", self.in_dtype), (q_start, "q_start", torch.int32),
                   (block_tables, "block_tables", torch.int32), (ctx_lens, "ctx_lens", torch.int32))
@@ -505,7 +505,7 @@ class KVPool:
                     layer: int = 0, n_layers: int | None = None, stream=None) -> torch.Tensor:
         """Move the K and V of the accepted nodes paths[s, :path_lens[s]] (ascending) of each sequence's
         tree right behind its history, in `n_layers` layers from `layer` on (None: all that follow).
-        Returns the new context lengths (`new_lens`, which must not be ctx_lens itself)."""
+        Returns the new context lengths (`new_lens`, which must not be one of the inputs)."""
         _all_need(self.device, (paths, "paths", torch.int32), (path_lens, "path_lens", torch.int32),
                   (q_start, "q_start", torch.int32), (block_tables, "block_tables", torch.int32),
                   (ctx_lens, "ctx_lens", torch.int32))

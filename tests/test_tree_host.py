@@ -86,7 +86,7 @@ def test_decode_tree_refusals(lib):
     h = _pool()
 
     def call(**kw):
-        a = dict(layer=0, out=A, dt=N.PA_FP16, q=A, T=9, qs=A, tables=A, width=4, ctx=A, S=3, Hq=4, nodes=8, mask=A,
+        a = dict(layer=0, out=A + 8192, dt=N.PA_FP16, q=A, T=9, qs=A, tables=A, width=4, ctx=A, S=3, Hq=4, nodes=8, mask=A,
                  scale=0.1, ws=A, ws_bytes=1 << 40)
         a.update(kw)
         N.pa_decode_tree(h, *a.values(), 0)
@@ -101,7 +101,9 @@ def test_decode_tree_refusals(lib):
                         (dict(width=0), INV), (dict(width=1 << 27), UNS), (dict(scale=math.nan), INV),
                         (dict(scale=math.inf), INV), (dict(out=0), INV), (dict(q=0), INV), (dict(qs=0), INV),
                         (dict(tables=0), INV), (dict(ctx=0), INV), (dict(out=A + 8), INV), (dict(q=A + 2), INV),
-                        (dict(mask=A + 4), INV), (dict(ws=0), INV), (dict(ws=A + 8), INV)])
+                        (dict(mask=A + 4), INV), (dict(ws=0), INV), (dict(ws=A + 8), INV), (dict(out=A), INV),
+                        (dict(out=A + 9 * 512 - 16), INV), (dict(q=A + 8192 + 9 * 512 - 16), INV),
+                        (dict(dt=N.PA_FP32, q=A + 8192 + 9 * 1024 - 16), INV)])
         for bad in (dict(Hq=3), dict(nodes=0), dict(nodes=257)):
             a = dict(Hq=4, nodes=8)
             a.update(bad)
@@ -116,7 +118,7 @@ def test_tree_accept_refusals(lib):
     h = _pool()
 
     def call(**kw):
-        a = dict(layer=0, n=2, paths=A, P=5, lens=A, qs=A, tables=A, width=4, ctx=A, S=3, new=A + 64)
+        a = dict(layer=0, n=2, paths=A, P=5, lens=A, qs=A, tables=A, width=4, ctx=A, S=3, new=A + 4096)
         a.update(kw)
         N.pa_tree_accept(h, *a.values(), 0)
 
@@ -126,6 +128,8 @@ def test_tree_accept_refusals(lib):
                         (dict(P=-1), INV), (dict(P=257), INV), (dict(S=-1), INV), (dict(width=0), INV),
                         (dict(width=1 << 27), UNS), (dict(paths=0), INV), (dict(lens=0), INV), (dict(qs=0), INV),
                         (dict(tables=0), INV), (dict(ctx=0), INV), (dict(new=0), INV), (dict(new=A), INV),
+                        (dict(ctx=A + 4096 - 8), INV), (dict(ctx=A + 4096 + 8), INV), (dict(lens=A + 4096), INV),
+                        (dict(qs=A + 4096 - 12), INV), (dict(paths=A + 4096 - 56), INV),
                         (dict(S=0x7FFFFFFF, n=2), UNS)])
     finally:
         N.pa_pool_destroy(h)
