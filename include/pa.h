@@ -408,7 +408,8 @@ typedef struct pa_rope_axes {
  *   eps             finite, >= 0 (with 0 a head of zeros gives NaN)
  *   weight_offset   finite; 1 for models whose weights are kept as w - 1
  *   positions_dev   device int32 [n_axes][T], axis by axis
- * The squares are added up in fp32, and all is rounded once at the end.  Everything
+ * The squares are added up in fp32 (a head whose sum passes its range gives zeros),
+ * and all is rounded once at the end.  Everything
  * else is as for pa_rope_and_cache (q_out may be q; v is stored as it is). */
 PA_API int pa_norm_rope_and_cache(pa_pool* pool, int layer, const pa_rope* rope,
                                   const pa_rope_axes* axes, const void* q_weight,

@@ -3,8 +3,13 @@
 //
 // Node path[i] goes to place i.  The path ascends, so path[i] >= i: a place is never
 // the source of a later one, and a warp that goes through the path in order, its loads
-// before its stores, needs no copy.  Every (layer, sequence, kv head) is a warp
-// of its own; rows move as 16-byte vectors.
+// before its stores, needs no copy.  A (layer, sequence, kv head) belongs to one warp;
+// rows move as 16-byte vectors.
+//
+// There is little to move (the floor of 64 paths in 32 layers is 1.9 us of HBM's time), so what
+// counts is the chain of dependent loads: lengths, path, table, rows (block-scaled tiles: and
+// scales).  One layer, 64 paths, bf16: 2.9 us; 32 layers, FP8: 5.6 us; 32 layers, 33 paths,
+// block-scaled: 18.7 us, issue slots 45% busy with the new codes (a quotient per value).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -23,6 +23,13 @@
 //  * what a row does not see must not touch it.  A masked key's weight is 0, but 0 times an
 //    infinity or a NaN among V is not: such values of nodes are taken out of the block in shared
 //    memory, and put back for the rows that see them when the output is written.
+//
+// What bounds it: 16-bit pools HBM (64 sequences of 512-4096 tokens, 16 nodes of 32 / 8 heads, bf16:
+// 104 us and 6 of the merge, 6.0 TB/s); FP8 pools the chain of hand-offs of a block (scores, maximum, weights, the
+// second product), 2200-2450 cycles where HBM takes 1400 and the products 1030 (128 sequences of
+// 4096, 16 nodes of 64 / 8 heads: 267 us and 8, 4.2 TB/s).  Trees above 128 rows read their pages once
+// per tile and are bound by the same chain (4 of 131072, 32 nodes of 64 / 8 heads, two tiles: 490 us
+// and 8, 0.60 of the products' rate, HBM at 55%).  Calls with little to read take their latency: 8 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
