@@ -22,7 +22,7 @@
 // pa_norm_rope_and_cache adds, before the turn, x rsqrt(mean(x^2) + eps) (offset + w) per head:
 // the D / 16 threads of a row sum their squares in fp32 with shuffles.  The same 8192 tokens:
 // 67.7 us, 4.7 TB/s, issue slots 61% busy: the norm's instructions per element, which the
-// copy cannot hide.  64 tokens of 32 / 8 heads (bf16) 4.5 us; 2037 of 32 / 8 heads with a scale per tile 30.4.
+// copy cannot hide.  64 tokens of 32 / 8 heads (bf16) 4.5 us; 2037 of 32 / 8 heads with a scale per tile 25.6.
 // Weights held in fp32 registers or in shared memory, packed arithmetic and other
 // warps per CTA were all slower.
 #include <cuda_runtime.h>
@@ -461,22 +461,20 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_cache_block_kernel(co
     __syncthreads();
   }
   if (!live) return;
-  const bool normed = EXT && !is_v && a.kw;
-  UnitNorm norm = {};
-  float rs[ITERS];
-  if (normed) {
-    norm.offset = a.w_offset;
-    norm.w = a.kw + (long long)h * a.k_wstride;
-    norm.w0 = *reinterpret_cast<const uint4*>(norm.w + 8 * v0);
-    norm.w1 = *reinterpret_cast<const uint4*>(norm.w + 8 * v1);
+  uint32_t mb = 0;  // largest |y|: without the sign bit, magnitudes order like their bits (a NaN above all)
+  auto widen = [&](int i, const float (&y)[16]) {
+    if (i * ROWS + r0 < n) {
 #pragma unroll
-    for (int i = 0; i < ITERS; ++i) {
-      UnitIn<LAY> in = {};
-      in.x0 = x[i][0];
-      in.x1 = x[i][1];
-      rs[i] = row_rsqrt<true, D, LAY>(in, a.eps);
+      for (int j = 0; j < 16; ++j) mb = max(mb, __float_as_uint(y[j]) & 0x7FFFFFFFu);
     }
-  }
+  };
+  // EXT: the norm makes values too dear to make twice, so they are kept, half of them in registers, half
+  // in shared memory ([vector][lane], so without conflicts), which leaves room for four CTAs on an SM:
+  // 2037 tokens of 32 / 8 heads 25.6 us, 30.4 made twice, 27.0 with three CTAs.
+  constexpr bool ODD = LAY == ROPE_HALF_ODD;
+  constexpr int IN_REGS = ITERS / 2, SLOTS = EXT ? ITERS - IN_REGS : 1;
+  __shared__ float4 ys[EXT ? kRopeWarps : 1][SLOTS][4][EXT ? 32 : 1];
+  float yr[IN_REGS][16];
   auto values = [&](int i, float (&y)[16]) {
     UnitIn<LAY> in;
     in.x0 = x[i][0];
@@ -484,20 +482,76 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_cache_block_kernel(co
     if (is_v) {
       plain_unit<true, LAY>(in, y);
     } else {
-      if constexpr (LAY == ROPE_HALF_ODD) load_unit<LAY, false>(row_at(i), u, rot, in);
-      if (normed) norm.rs = rs[i];
-      turn_unit<true, D, LAY, false>(in, u, rot, cs[i * ROWS + r0], y, normed ? &norm : nullptr);
+      if constexpr (ODD) load_unit<LAY, false>(row_at(i), u, rot, in);
+      turn_unit<true, D, LAY, false>(in, u, rot, cs[i * ROWS + r0], y);
     }
   };
-  uint32_t mb = 0;  // largest |y|: without the sign bit, magnitudes order like their bits (a NaN above all)
-#pragma unroll
-  for (int i = 0; i < ITERS; ++i)
-    if (i * ROWS + r0 < n) {
-      float y[16];
-      values(i, y);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) mb = max(mb, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+  if constexpr (EXT) {
+    const bool normed = !is_v && a.kw;
+    UnitNorm norm = {};
+    if (normed) {
+      norm.offset = a.w_offset;
+      norm.w = a.kw + (long long)h * a.k_wstride;
+      norm.w0 = *reinterpret_cast<const uint4*>(norm.w + 8 * v0);
+      norm.w1 = *reinterpret_cast<const uint4*>(norm.w + 8 * v1);
     }
+#pragma unroll
+    for (int step = 0; step < ITERS; ++step) {
+      const int i = ODD ? step : ITERS - 1 - step;
+      if (i * ROWS >= n) continue;
+      constexpr int L = ODD ? ROPE_INTER : LAY;  // (an odd row's partners are not read again)
+      float y[16];
+      UnitIn<L> in;
+      in.x0 = x[i][0];
+      in.x1 = x[i][1];
+      const int slot_of = i < IN_REGS ? 0 : i - IN_REGS;
+      if (is_v) {
+        plain_unit<true, L>(in, y);
+      } else {
+        if (normed) norm.rs = row_rsqrt<true, D, L>(in, a.eps);
+        if constexpr (ODD) {
+          // partners through shared memory: the rows of this step
+          plain_unit<true, L>(in, y);
+          if (normed) scale_unit<true>(norm, y);
+          float* row = reinterpret_cast<float*>(ys[warp][slot_of]) + r0 * D;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            reinterpret_cast<float4*>(row + 16 * u)[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+          __syncwarp();
+          const int half = rot >> 1;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int e = 16 * u + j;
+            if (e < rot) {
+              const float2 t = cs[i * ROWS + r0][e < half ? e : e - half];
+              const float p = row[e < half ? e + half : e - half];
+              y[j] = e < half ? y[j] * t.x - p * t.y : y[j] * t.x + p * t.y;
+            }
+          }
+          __syncwarp();
+        } else {
+          turn_unit<true, D, L, false>(in, u, rot, cs[i * ROWS + r0], y, normed ? &norm : nullptr);
+        }
+      }
+      widen(i, y);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (i < IN_REGS) yr[i < IN_REGS ? i : 0][j] = y[j];
+      if (i >= IN_REGS) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          ys[warp][slot_of][j][lane] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < ITERS; ++i)
+      if (i * ROWS + r0 < n) {
+        float y[16];
+        values(i, y);
+        widen(i, y);
+      }
+  }
   mb = __reduce_max_sync(0xffffffffu, mb);
   const float s_run = __fdiv_rn(__uint_as_float(mb), 448.f);
   const bool grow = off0 == 0 || s_run > s_old;
@@ -524,7 +578,20 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_cache_block_kernel(co
   for (int i = 0; i < ITERS; ++i)
     if (i * ROWS + r0 < n) {
       float y[16];
-      values(i, y);
+      if constexpr (EXT) {
+        if (i < IN_REGS) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) y[j] = yr[i < IN_REGS ? i : 0][j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 f = ys[warp][i < IN_REGS ? 0 : i - IN_REGS][j][lane];
+            y[4 * j] = f.x, y[4 * j + 1] = f.y, y[4 * j + 2] = f.z, y[4 * j + 3] = f.w;
+          }
+        }
+      } else {
+        values(i, y);
+      }
       uint8_t* dst = tile + (size_t)(off0 + i * ROWS + r0) * D;
       *reinterpret_cast<uint2*>(dst + 8 * v0) = codes8(y, s);
       *reinterpret_cast<uint2*>(dst + 8 * v1) = codes8(y + 8, s);
