@@ -139,6 +139,24 @@ def test_against_numpy(kv, case):
     t.pool.close()
 
 
+@pytest.mark.parametrize("kv", KINDS)
+@pytest.mark.parametrize("S,H,D,layers", [(310, 8, 64, 5), (90, 3, 128, 37), (700, 1, 64, 9)])
+def test_many_pairs(kv, S, H, D, layers):
+    """More (sequence, layer, kv head) pairs than the GPU has warps: several to a warp, paths of
+    no move, of one, and of more rows than a warp has lanes."""
+    rng = np.random.default_rng(S)
+    sizes = [int(rng.integers(60, 100)) if s % 45 == 7 else int(rng.integers(0, 17)) for s in range(S)]
+    ctx = [n + int(rng.integers(0, 40)) for n in sizes]
+    paths = [sorted(rng.permutation(n)[:int(rng.integers(0, n + 1))].tolist()) for n in sizes]
+    t = Trees(kv, H, D, ctx, sizes, paths, layers, seed=S)
+    before = t.state()
+    lens = t.pool.tree_accept(**t.args)
+    assert t.pool.device_error() == N.PA_OK
+    assert lens.tolist() == [c - n + len(p) for c, n, p in zip(ctx, sizes, paths)]
+    t.check(t.expected(before))
+    t.pool.close()
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3_block"])
 def test_some_layers(kv):
     t = Trees(kv, 2, 128, [50], [30], [[3, 7, 20]], layers=4)
