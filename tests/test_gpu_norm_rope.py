@@ -68,6 +68,10 @@ CASES = [  # kv, T, Hq, H, D, rope, sections (None: one axis), order, weights, o
     ("fp8_e4m3_block", 41, 16, 5, 64, dict(rot_dim=32, layout="interleaved"), None, "", "head", 1.0, False),
     ("fp8_e4m3_block", 16, 2, 2, 128, dict(rot_dim=44), [8, 7, 7], "turns", "shared", 0.0, True),
     ("fp8_e4m3_block", 35, 3, 3, 128, dict(rot_dim=128), [16, 24, 24], "sections", "none", 0.0, False),
+    ("fp8_e4m3_block", 51, 11, 11, 128, dict(rot_dim=90), [15, 15, 15], "turns", "head", 1.0, True),
+    ("fp8_e4m3_block", 30, 9, 9, 64, dict(rot_dim=62, gain=0.7), None, "", "k", 0.0, False),
+    ("fp8_e4m3_block", 64, 5, 1, 64, dict(rot_dim=64), [12, 10, 10], "sections", "shared", 0.0, False),
+    ("fp8_e4m3_block", 29, 2, 2, 128, dict(rot_dim=126, layout="interleaved"), None, "", "shared", 0.0, True),
 ]
 
 

@@ -57,6 +57,17 @@ def test_long_history(kv):
 
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("kv", KINDS)
+def test_one_unit_on_every_sm(kv, D):
+    """One kv head and one long sequence: as many pieces as SMs, and a tree whose nodes see little of it."""
+    for ctx, sizes, G in (([20011], [37], 3), ([4100, 700], [1, 1], 8)):
+        b = Batch(kv, 1, G, D, ctx, sizes, mask="random", seed=2)
+        for dt in (None, torch.float32):
+            b.check(b.run(out_dtype=dt))
+        b.pool.close()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kv", KINDS)
 def test_what_a_node_does_not_see(kv, D):
     """Infinities and NaN in keys and values of unseen nodes, and in slots behind the context,
     change nothing; those that a node sees do (FP8 has no infinity: NaN)."""
