@@ -109,7 +109,8 @@ struct Ctrl {
   uint64_t mask[kRowRing][128][PA_TREE_MAX_NODES / 64];  // a tile's nodes' mask words
   float row_scale[kRowRing][128];        // each row's score factor
   float4 fin[kRowRing][128];             // each row's (m, V scale of O, the two threads' l) at the segment's end
-  float2 sc[kScaleRing][8];              // block-scaled pools: (K scale, V scale) of each page of a block
+  float4 sc[kScaleRing][8];  // block-scaled pools: (K scale, V scale, its log2, its reciprocal) of each page of a block
+  float2 sc_top[kScaleRing];             // a block's largest V scale and its log2
   float xbuf[2][128][2];                 // the two half-row threads' maxima
   long long warp_sums[kThreads / 32];
   long long start_off;
@@ -553,6 +554,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
         csv = 0.f;
         ctl->bad[cur.j & 7] = cur.j + 1;
       }
+      float lgv = 0.f, rcv = 0.f, top = 0.f;
+      if constexpr (BLK) {
+        csv = top = fmaxf(csv, 0.f);
+        rcv = 1.f / csv;
+        lgv = log2f(csv);
+#pragma unroll
+        for (int off = 1; off < 8; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+      }
       scales(nxt);
 #pragma unroll 1
       for (int j = 0; j < cur.nb; ++j, ++g) {
@@ -563,7 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
           if (g >= kScaleRing)
             ok = __all_sync(kAll, wait_for(&ctl->sc_empty[e], ((g / kScaleRing) - 1) & 1, abort_flag, a.err));
           if (!ok) break;
-          if (lane >= pb && lane < pb + 8) ctl->sc[e][lane - pb] = make_float2(csk, csv);
+          if (lane >= pb && lane < pb + 8) ctl->sc[e][lane - pb] = make_float4(csk, csv, lgv, rcv);
+          if (lane == pb) ctl->sc_top[e] = make_float2(top, log2f(top));
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->sc_full[e]);
         }
@@ -1067,21 +1077,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       const bool active = quad * 32 >= lane0;
       const int tl = min(r / a.G, rows / a.G - 1), own = cur.tile * a.tile_nodes + tl;  // this row's node
       const uint64_t* words = a.mask ? ctl->mask[j % kRowRing][tl] : nullptr;
-      float m = -INFINITY, l = 0.f, vref = 0.f, row_scale = 1.f;
+      float m = -INFINITY, l = 0.f, vref = 0.f, lvref = 0.f, row_scale = 1.f;
       for (int b = cur.b0; b < cur.b1; ++b, ++g) {
         const int sb = g & 1, se = g % kScaleRing;
         const bool first = b == cur.b0;
         float ov = 1.f, vinv = 1.f;  // factor for this row's O; 1 / vref
         if constexpr (BLK) {         // V weights are taken relative to the largest V scale seen (<= 1)
           ok = __all_sync(kAll, ok && wait_for(&ctl->sc_full[se], (g / kScaleRing) & 1, abort_flag, a.err));
-          float vb = vref;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) vb = fmaxf(vb, ctl->sc[se][i].y);
-          if (vb > vref) {
-            ov = vref / vb;
-            vref = vb;
+          const float2 top = ctl->sc_top[se];
+          if (top.x > vref) {
+            ov = vref / top.x;
+            vref = top.x;
+            lvref = top.y;
           }
-          vinv = vref > 0.f ? 1.f / vref : 0.f;
+          if constexpr (PSPLIT) vinv = vref > 0.f ? 1.f / vref : 0.f;
         }
         const int j0 = 128 * b + 64 * hf - cur.base;  // this thread's first key, as a node
         const bool masked = j0 + 63 >= 0;
@@ -1161,8 +1170,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
               float* v = sv[cc];
 #pragma unroll
               for (int hp = 0; hp < 2; ++hp) {
-                const float2 f2 = make_float2(pf[cc][hp], pf[cc][hp]), nm = make_float2(-mref, -mref);
-                const float vm = BLK ? ctl->sc[se][2 * c + hp].y * vinv : 1.f;
+                // The page's V scale over vref (2^-64 at least: below, no weight is left in 16 bits) goes into the
+                // exponent, and its inverse times the sum of the page's weights into l: a product per page in the
+                // place of one per weight.  fp32 outputs multiply: in the exponent the ratio would be rounded.
+                float shift = 0.f, back = 1.f, vm = 1.f;
+                if constexpr (BLK && !PSPLIT) {
+                  const float4 sp = ctl->sc[se][2 * c + hp];
+                  shift = fmaxf(sp.z - lvref, -64.f);
+                  back = fminf(vref * sp.w, 0x1p64f);
+                } else if constexpr (BLK) {
+                  vm = ctl->sc[se][2 * c + hp].y * vinv;
+                }
+                const float2 f2 = make_float2(pf[cc][hp], pf[cc][hp]), nm = make_float2(shift - mref, shift - mref);
                 const float2 vm2 = make_float2(vm, vm);
                 float2 t01 = make_float2(0.f, 0.f), t23 = t01;
                 float* x = v + 16 * hp;
@@ -1174,7 +1193,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
                   float2 pb = make_float2(fast_exp2(zb.x), fast_exp2(zb.y));
                   t01 = __fadd2_rn(t01, pa);
                   t23 = __fadd2_rn(t23, pb);
-                  if constexpr (BLK) {
+                  if constexpr (BLK && PSPLIT) {
                     pa = __fmul2_rn(pa, vm2);
                     pb = __fmul2_rn(pb, vm2);
                   }
@@ -1183,7 +1202,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
                   x[e + 2] = pb.x;
                   x[e + 3] = pb.y;
                 }
-                rs += (t01.x + t01.y) + (t23.x + t23.y);
+                rs += ((t01.x + t01.y) + (t23.x + t23.y)) * back;
               }
               uint32_t ph[16], pl[16];  // in V's type: bfloat16 for bfloat16 pools, else binary16
 #pragma unroll
