@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       }
       float lgv = 0.f, rcv = 0.f, top = 0.f;
       if constexpr (BLK) {
-        csv = top = fmaxf(csv, 0.f);
+        csv = top = csv >= kMinFactor ? csv : 0.f;  // (subnormal scales count as 0: their reciprocal is no number)
         rcv = 1.f / csv;
         lgv = log2f(csv);
 #pragma unroll

@@ -220,6 +220,23 @@ def test_lost_tiles(kv):
     b.pool.close()
 
 
+@pytest.mark.parametrize("up", [True, False])
+def test_tile_scales_far_apart(up):
+    """Block-scaled tiles of V whose scales differ by more than 16-bit weights hold, zeros and subnormal
+    ones among them, the largest at the end or at the start of the history."""
+    b = Batch("fp8_e4m3_block", 2, 3, 128, [900, 330, 150], [9, 20, 5], seed=23)
+    steps = [0.0, 2.0 ** -140, 2.0 ** -100, 2.0 ** -75, 2.0 ** -63, 2.0 ** -40, 2.0 ** -20, 2.0 ** -9, 1.0]
+    sc = b.pool.scale_view("v")
+    for s, n in enumerate(b.ctx):
+        last = (n - b.sizes[s]) // 16 - 1  # the last page of history alone
+        for page in range(last + 1):
+            i = page if up else last - page
+            sc[int(b.tables_np[s, page])] = 0.01 * steps[i * len(steps) // (last + 1)]
+    b.check(b.run())
+    b.check(b.run(out_dtype=torch.float32))
+    b.pool.close()
+
+
 def _bad(b, **kw):
     out = torch.full((b.T, b.H * b.G, b.D), 7.0, dtype=b.pool.in_dtype, device="cuda")
     a = dict(q_start=b.q_start, tables=b.tables, ctx=b.ctx_t, max_nodes=b.max_nodes, mask=b.mask)
