@@ -57,7 +57,7 @@ __device__ __forceinline__ Path check_path(const AcceptArgs& a, int s) {
   bool bad = q0 < 0 || n < 0 || n > PA_TREE_MAX_NODES || p.ctx < n || p.ctx > 16ll * a.max_blocks || len < 0 || len > a.max_path ||
              len > n;
   if (!bad) {
-    int before = -1;  // the node in front of this round's
+    int before = -1;  // the node in front of these 32
     for (int i0 = 0; i0 < len; i0 += 32) {
       const int node = i0 + lane < len ? a.paths[(long long)s * a.max_path + i0 + lane] : 0x7FFFFFFF;
       int prev = __shfl_up_sync(kAll, node, 1);
