@@ -656,9 +656,11 @@ PA_API int pa_decode_tree_workspace_bytes(const pa_pool* pool, int n_q_heads, in
  * Grouped-query heads, block tables and softmax_scale are as for pa_decode.  Sequences
  * without nodes are skipped; a node that sees nothing (no history, no bit) gets
  * zeros.  What a node does not see does not touch its result, whatever the cache holds there
- * (infinities and NaN among it).  The weights keep their precision in the product with
- * V.  A V scale of a PA_FP8_E4M3_BLOCK tile below the smallest normal fp32 number counts
- * as 0.  A sequence with more than max_nodes nodes, a decreasing or negative q_start or
+ * (infinities, NaN and tiles' scales among it).  In the product with V the weights keep
+ * their precision (two terms), but for FP8 pools with bf16 outputs, which round each weight to
+ * binary16 (2^-12 of it, a sixteenth of the output's own rounding).  A key counts while its weight, times its
+ * tile's V scale in PA_FP8_E4M3_BLOCK pools, is above 2^-31 of the row's largest; such scales may lie any
+ * distance apart.  A V scale below the smallest normal fp32 number counts as 0.  A sequence with more than max_nodes nodes, a decreasing or negative q_start or
  * one above T, a context shorter than its nodes or longer than 16 * max_blocks_per_seq
  * is skipped (its rows are not written), a table entry outside [0, num_blocks) gives
  * an undefined result for its sequence; both set PA_ERR_BOUNDS in the device error

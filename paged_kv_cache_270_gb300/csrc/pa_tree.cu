@@ -108,10 +108,11 @@ struct Ctrl {
   uint64_t tail_ready[2], tail_done[2];  // 16-bit pools: blocks that reach the tree, by their parity
   uint64_t mask[kRowRing][128][PA_TREE_MAX_NODES / 64];  // a tile's nodes' mask words
   float row_scale[kRowRing][128];        // each row's score factor
-  float4 fin[kRowRing][128];             // each row's (m, V scale of O, the two threads' l) at the segment's end
-  float4 sc[kScaleRing][8];  // block-scaled pools: (K scale, V scale, its log2, its reciprocal) of each page of a block
-  float2 sc_top[kScaleRing];             // a block's largest V scale and its log2
-  float xbuf[2][128][2];                 // the two half-row threads' maxima
+  float4 fin[kRowRing][128];             // each row's (m, 2^(r - m), the two threads' l) at the segment's end
+  // block-scaled pools, each page of a block: K scale, log2 of the V scale, and the exponent and factor that the
+  // weights take for it (16-bit outputs: all of the log2, and 1; fp32 outputs: a whole number, and what is left)
+  float4 sc[kScaleRing][8];
+  float2 xbuf[2][2][128];                // the two half-row threads' maxima (one scale: of floats)
   long long warp_sums[kThreads / 32];
   long long start_off;
   int start_seq;
@@ -554,13 +555,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
         csv = 0.f;
         ctl->bad[cur.j & 7] = cur.j + 1;
       }
-      float lgv = 0.f, rcv = 0.f, top = 0.f;
+      float lgv = 0.f, ev = 0.f, fv = 1.f;
       if constexpr (BLK) {
-        csv = top = csv >= kMinFactor ? csv : 0.f;  // (subnormal scales count as 0: their reciprocal is no number)
-        rcv = 1.f / csv;
-        lgv = log2f(csv);
-#pragma unroll
-        for (int off = 1; off < 8; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+        csv = csv >= kMinFactor ? csv : 0.f;  // (subnormal scales count as 0)
+        ev = lgv = log2f(csv);
+        if constexpr (PSPLIT) {
+          ev = floorf(lgv);
+          fv = csv > 0.f ? ldexpf(csv, -(int)ev) : 0.f;
+        }
       }
       scales(nxt);
 #pragma unroll 1
@@ -572,8 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
           if (g >= kScaleRing)
             ok = __all_sync(kAll, wait_for(&ctl->sc_empty[e], ((g / kScaleRing) - 1) & 1, abort_flag, a.err));
           if (!ok) break;
-          if (lane >= pb && lane < pb + 8) ctl->sc[e][lane - pb] = make_float4(csk, csv, lgv, rcv);
-          if (lane == pb) ctl->sc_top[e] = make_float2(top, log2f(top));
+          if (lane >= pb && lane < pb + 8) ctl->sc[e][lane - pb] = make_float4(csk, lgv, ev, fv);
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->sc_full[e]);
         }
@@ -1048,13 +1049,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
     // time limit: so both leave at a meeting that says so, and a warp that leaves for any other reason, its
     // list's end among them, comes to one more meeting, which is the other's next one.
     bool parted = false;
-    auto exchange = [&](float mine) -> float {
-      float* x = &ctl->xbuf[xk & 1][ln][0];
-      x[hf] = !ok ? NAN : mine == mine ? mine : -INFINITY;
+    auto exchange = [&](float2 mine) -> float2 {  // (.y: block-scaled pools; a NaN there counts for nothing by itself)
+      using X = std::conditional_t<BLK, float2, float>;
+      X* x = reinterpret_cast<X*>(ctl->xbuf[xk & 1]);
+      mine.x = !ok ? NAN : mine.x == mine.x ? mine.x : -INFINITY;
+      if constexpr (BLK) x[128 * hf + ln] = mine;
+      else x[128 * hf + ln] = mine.x;
       __syncwarp();
       asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
-      const float other = x[hf ^ 1];
-      ok = __all_sync(kAll, ok && other == other);
+      float2 other = make_float2(0.f, 0.f);
+      if constexpr (BLK) other = x[128 * (hf ^ 1) + ln];
+      else other.x = x[128 * (hf ^ 1) + ln];
+      ok = __all_sync(kAll, ok && other.x == other.x);
       parted = !ok;
       ++xk;
       return other;
@@ -1077,21 +1083,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       const bool active = quad * 32 >= lane0;
       const int tl = min(r / a.G, rows / a.G - 1), own = cur.tile * a.tile_nodes + tl;  // this row's node
       const uint64_t* words = a.mask ? ctl->mask[j % kRowRing][tl] : nullptr;
-      float m = -INFINITY, l = 0.f, vref = 0.f, lvref = 0.f, row_scale = 1.f;
+      // l is relative to 2^m and O to 2^r.  Block-scaled pools: m follows the largest score, r the largest score
+      // plus log2 of its tile's V scale, so O's weights are as large as 16 bits hold whatever the tiles' scales are, and
+      // only seen keys move either.  One scale: r is m.
+      float m = -INFINITY, l = 0.f, r_o = -INFINITY, row_scale = 1.f;
       for (int b = cur.b0; b < cur.b1; ++b, ++g) {
         const int sb = g & 1, se = g % kScaleRing;
         const bool first = b == cur.b0;
-        float ov = 1.f, vinv = 1.f;  // factor for this row's O; 1 / vref
-        if constexpr (BLK) {         // V weights are taken relative to the largest V scale seen (<= 1)
+        float ov = 1.f;  // factor for this row's O
+        if constexpr (BLK)
           ok = __all_sync(kAll, ok && wait_for(&ctl->sc_full[se], (g / kScaleRing) & 1, abort_flag, a.err));
-          const float2 top = ctl->sc_top[se];
-          if (top.x > vref) {
-            ov = vref / top.x;
-            vref = top.x;
-            lvref = top.y;
-          }
-          if constexpr (PSPLIT) vinv = vref > 0.f ? 1.f / vref : 0.f;
-        }
         const int j0 = 128 * b + 64 * hf - cur.base;  // this thread's first key, as a node
         const bool masked = j0 + 63 >= 0;
         ok = __all_sync(kAll, ok && wait_for(&ctl->s_full[sb], (g >> 1) & 1, abort_flag, a.err));
@@ -1100,7 +1101,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
         const uint64_t vis = active && masked ? sees64(words, a.words, own, cur.n, j0) : ~0ull;
         const uint32_t sbase = trow + sb * 128;
         if (active) {
-          float mh = -INFINITY;
+          float mh = -INFINITY, mo = -INFINITY;
           float sv[2][32];  // this thread's 64 scores of the block, read from TMEM once
           float pf[2][2];   // the score factor of each of the thread's four pages
 #pragma unroll
@@ -1126,20 +1127,42 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
               pm[cc][0] = max16(v);
               pm[cc][1] = max16(v + 16);
             }
-            if constexpr (BLK)
-              mh = fmaxf(fmax3f(pm[0][0] * pf[0][0], pm[0][1] * pf[0][1], pm[1][0] * pf[1][0]), pm[1][1] * pf[1][1]);
-            else  // one positive factor: the largest product is the largest score times it
+            if constexpr (BLK) {
+              float po[2][2];
+#pragma unroll
+              for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+                for (int hp = 0; hp < 2; ++hp) {
+                  pm[cc][hp] *= pf[cc][hp];
+                  po[cc][hp] = pm[cc][hp] + ctl->sc[se][2 * (2 * hf + cc) + hp].y;
+                }
+              mh = fmaxf(fmax3f(pm[0][0], pm[0][1], pm[1][0]), pm[1][1]);
+              mo = fmaxf(fmax3f(po[0][0], po[0][1], po[1][0]), po[1][1]);
+            } else {  // one positive factor: the largest product is the largest score times it
               mh = fmaxf(fmax3f(pm[0][0], pm[0][1], pm[1][0]), pm[1][1]) * row_scale;
+            }
           }
-          const float mx = fmaxf(mh, exchange(mh));
+          const float2 other = exchange(make_float2(mh, mo));
+          const float mx = fmaxf(mh, other.x);
           if (!ok) break;
-          if (mx > m + kGrow) {  // the first seen keys, or a maximum that grew
-            const float to = mx - kTop, alpha = fast_exp2(m - to);
+          // The first seen keys, or a maximum that grew.  (fp32 outputs with scales of tiles: whole numbers, so that the
+          // exponents below are exact.)
+          if (mx > m + kGrow) {
+            const float to = (BLK && PSPLIT ? ceilf(mx) : mx) - kTop, alpha = fast_exp2(m - to);
             l *= alpha;
-            ov *= alpha;
+            if constexpr (!BLK) ov = alpha;
             m = to;
           }
-          const float mref = m == -INFINITY ? 0.f : m;  // (nothing seen yet: every weight is 0)
+          if constexpr (BLK) {
+            const float mxo = fmaxf(mo, other.y);
+            if (mxo > r_o + kGrow) {
+              const float to = (PSPLIT ? ceilf(mxo) : mxo) - kTop;
+              ov = fast_exp2(r_o - to);
+              r_o = to;
+            }
+          }
+          // (nothing seen yet, or nothing but values of 0: every weight is 0, or counts in l alone)
+          const float mref = m == -INFINITY ? 0.f : m, rref = !BLK ? mref : r_o == -INFINITY ? 0.f : r_o;
           // O is rescaled once the previous block's P V is done (see the prefill for why this phase
           // of its barrier is never mistaken)
           if (ok && !first && __any_sync(kAll, ov != 1.f)) {
@@ -1170,18 +1193,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
               float* v = sv[cc];
 #pragma unroll
               for (int hp = 0; hp < 2; ++hp) {
-                // The page's V scale over vref (2^-64 at least: below, no weight is left in 16 bits) goes into the
-                // exponent, and its inverse times the sum of the page's weights into l: a product per page in the
-                // place of one per weight.  fp32 outputs multiply: in the exponent the ratio would be rounded.
-                float shift = 0.f, back = 1.f, vm = 1.f;
-                if constexpr (BLK && !PSPLIT) {
+                // Block-scaled pools: a weight times its V scale is 2^(score + log2 scale - r); most of the scale goes
+                // into the exponent, so that it costs a product per page in the place of one per weight.  l takes
+                // the page's sum back to 2^(score - m).  The exponent is kept above what l needs (2^-64 of
+                // the largest score's weight); where that bound holds, O gets what is 0 in 16 bits.
+                float nmp = -mref, back = 1.f, vm = 1.f;
+                if constexpr (BLK) {
                   const float4 sp = ctl->sc[se][2 * c + hp];
-                  shift = fmaxf(sp.z - lvref, -64.f);
-                  back = fminf(vref * sp.w, 0x1p64f);
-                } else if constexpr (BLK) {
-                  vm = ctl->sc[se][2 * c + hp].y * vinv;
+                  nmp = fmaxf(sp.z - rref, -64.f - mref);
+                  back = fast_exp2(-(nmp + mref));
+                  vm = sp.w;
                 }
-                const float2 f2 = make_float2(pf[cc][hp], pf[cc][hp]), nm = make_float2(shift - mref, shift - mref);
+                const float2 f2 = make_float2(pf[cc][hp], pf[cc][hp]), nm = make_float2(nmp, nmp);
                 const float2 vm2 = make_float2(vm, vm);
                 float2 t01 = make_float2(0.f, 0.f), t23 = t01;
                 float* x = v + 16 * hp;
@@ -1230,12 +1253,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       }
       if (!ok) break;
       // what the output takes besides O
-      if (hf == 0) ctl->fin[j % kRowRing][ln].x = m, ctl->fin[j % kRowRing][ln].y = vref, ctl->fin[j % kRowRing][ln].z = l;
+      if (hf == 0) {
+        const float y = !BLK ? 1.f : r_o == -INFINITY ? 0.f : fast_exp2(r_o - m);
+        ctl->fin[j % kRowRing][ln].x = m, ctl->fin[j % kRowRing][ln].y = y, ctl->fin[j % kRowRing][ln].z = l;
+      }
       else ctl->fin[j % kRowRing][ln].w = l;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->row_free[j % kRowRing]);
     }
-    if (!parted) exchange(0.f);
+    if (!parted) exchange(make_float2(0.f, 0.f));
   }
 
   tc_fence_before();
