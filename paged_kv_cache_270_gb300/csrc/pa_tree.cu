@@ -818,6 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
         const float amax = bf16_bits_to_float(max(top & 0xFFFFu, top >> 16));
         int ex = 8;
         if (amax > 0.f && amax < INFINITY) frexpf(amax, &ex);
+        ex = max(ex, -118);  // (2^(8 - ex) and its inverse are normal numbers; of rows below 2^-118 the last bits are lost)
         // (E4M3 has no infinity: a row that holds one, or a NaN, becomes NaN, as its scores would)
         const float qs = amax < INFINITY ? copysignf(ldexpf(1.f, 8 - ex), a.qk_scale_log2) : NAN;
         row_scale *= ldexpf(1.f, ex - 8);
@@ -847,8 +848,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
           tmem_st8u(qcol + 32 + 8 * part, qlo);
         }
       }
-      // (a zero factor would turn a masked -inf into NaN)
-      ctl->row_scale[j % kRowRing][qr] = fmaxf(row_scale, kMinFactor);
+      // (a zero factor would turn a masked -inf into NaN; with scales of tiles it is bounded with the tile's)
+      ctl->row_scale[j % kRowRing][qr] = BLK ? row_scale : fmaxf(row_scale, kMinFactor);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
