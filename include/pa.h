@@ -656,7 +656,8 @@ PA_API int pa_decode_tree_workspace_bytes(const pa_pool* pool, int n_q_heads, in
  * Grouped-query heads, block tables and softmax_scale are as for pa_decode.  Sequences
  * without nodes are skipped; a node that sees nothing (no history, no bit) gets
  * zeros.  What a node does not see does not touch its result, whatever the cache holds there
- * (infinities, NaN and tiles' scales among it).  In the product with V the weights keep
+ * (infinities, NaN and tiles' scales among it).  An infinity or a NaN in the values (V)
+ * that it does see makes the result infinite or NaN there, however small its weight is.  In the product with V the weights keep
  * their precision (two terms), but for FP8 pools with bf16 outputs, which round each weight to
  * binary16 (2^-12 of it, a sixteenth of the output's own rounding).  A key counts while its weight, times its
  * tile's V scale in PA_FP8_E4M3_BLOCK pools, is above 2^-31 of the row's largest; such scales may lie any

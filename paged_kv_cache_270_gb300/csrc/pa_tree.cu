@@ -1315,11 +1315,13 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeArgs a) {
       for (int i = 0; i < cnt; i += PPW) {
         const float wi = __shfl_sync(kAll, w, (i + sub) & 31);
         const float4 x = reinterpret_cast<const float4*>(a.ws_o)[prow(base + min(i + sub, cnt - 1)) * (D / 4) + d4];
-        if (i + sub < cnt && wi != 0.f) {
-          o.x += wi * x.x;
-          o.y += wi * x.y;
-          o.z += wi * x.z;
-          o.w += wi * x.w;
+        if (i + sub < cnt) {
+          // a piece whose weight is below fp32's range leaves its infinities and NaN (one without seen keys has none)
+          auto part = [&](float v) { return wi != 0.f ? wi * v : fabsf(v) < INFINITY ? 0.f : v; };
+          o.x += part(x.x);
+          o.y += part(x.y);
+          o.z += part(x.z);
+          o.w += part(x.w);
         }
       }
     }
