@@ -282,6 +282,7 @@ int pa_tree_accept(pa_pool* pool, int layer, int n_layers, const int32_t* paths_
   if (overlap(new_lens_dev, lens_bytes, ctx_lens_dev, lens_bytes) ||
       overlap(new_lens_dev, lens_bytes, path_lens_dev, lens_bytes) ||
       overlap(new_lens_dev, lens_bytes, q_start_dev, lens_bytes + 4) ||
+      overlap(new_lens_dev, lens_bytes, block_tables_dev, lens_bytes * max_blocks_per_seq) ||
       overlap(new_lens_dev, lens_bytes, paths_dev, lens_bytes * max_path))
     return fail(PA_ERR_INVALID, "new_lens must be another buffer than the inputs, which every head reads");
   unsigned int* err = device_error_word();
