@@ -84,7 +84,17 @@ def make_rope_axes(sections, order: str = "sections") -> N.pa_rope_axes:
             raise ValueError(f"sections {sections} cannot take turns")
     else:
         raise ValueError("order must be 'sections' or 'turns'")
-    return N.pa_rope_axes(n, (N.ctypes.c_uint8 * 64)(*of))
+    axes = N.pa_rope_axes(n, (N.ctypes.c_uint8 * 64)(*of))
+    axes.pairs = pairs
+    return axes
+
+
+def _check_pairs(axes, rope) -> None:
+    """The sections of make_rope_axes must be those of this embedding's pairs.  (Axes filled by hand name all
+    64 pairs, so they fit any.)"""
+    pairs = getattr(axes, "pairs", None)
+    if pairs is not None and 2 * pairs != rope.rot_dim:
+        raise ValueError(f"axes of {pairs} pairs do not fit an embedding of {rope.rot_dim} dimensions")
 
 
 def _token_rows(t: torch.Tensor, name: str, dtype, device) -> int:
@@ -267,7 +277,10 @@ class KVPool:
         """``rope_and_cache`` that first divides every head of q and of k by its root mean square
         and multiplies it with `weight_offset` + its weights ([D], or [heads, D] for both; None: that
         side is not normalised).  With `axes` (``make_rope_axes``) positions is [n_axes, T]."""
-        n_axes = axes.n_axes if axes is not None else 1
+        n_axes = 1
+        if axes is not None:
+            _check_pairs(axes, rope)
+            n_axes = axes.n_axes
         q_out, args = self._rope_args(q, k, v, positions, slot_mapping, q_out, n_axes, stream)
         qw = kw = per_head = 0
         if q_weight is not None:
