@@ -684,7 +684,7 @@ PA_API int pa_decode_tree(pa_pool* pool, int layer, void* out, int out_dtype, co
  *                  ctx - nodes + path_len; another buffer than the inputs
  * 16-bit and FP8 pools move the bytes.  In PA_FP8_E4M3_BLOCK pools a destination tile's
  * scale grows to s = max(s_old, fl32(m / 448)), m the largest |fl32(decode(c) * s_src)| of
- * the rows that come from other tiles; if it grew, the codes of the tile's 16 rows become
+ * the rows that come from other tiles (a NaN counts for nothing in m and stays a NaN); if it grew, the codes of the tile's 16 rows become
  * E4M3(fl32(fl32(decode(c) * s_old) / s)); a moved row's codes are
  * E4M3(fl32(fl32(decode(c) * s_src) / s)) (0 when s = 0).  Rows behind the path keep their
  * contents up to that.  The blocks that hold nodes must not be shared with another sequence

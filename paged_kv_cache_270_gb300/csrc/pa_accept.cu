@@ -172,7 +172,8 @@ __device__ __forceinline__ uint4 recode(uint4 x, float s_src, float s) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Bits of the largest |code value| times s_src of 16 codes (a NaN above all).
+// Bits of the largest |code value| times s_src of 16 codes.  A NaN counts for nothing: the tile's scale grows for the
+// other values, which would be cut off at the old one.
 __device__ __forceinline__ uint32_t top_bits(uint4 x, float s_src) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   __half2 top = __float2half2_rn(0.f);
@@ -181,10 +182,10 @@ __device__ __forceinline__ uint32_t top_bits(uint4 x, float s_src) {
     uint32_t f[2];
     e4m3x4_to_f16x2x2(w[q], f[0], f[1]);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) top = __hmax2_nan(top, __habs2(*reinterpret_cast<__half2*>(&f[j])));
+    for (int j = 0; j < 2; ++j) top = __hmax2(top, __habs2(*reinterpret_cast<__half2*>(&f[j])));
   }
   const float2 t = __half22float2(top);
-  return max(__float_as_uint(__fmul_rn(t.x, s_src)) & 0x7FFFFFFFu, __float_as_uint(__fmul_rn(t.y, s_src)) & 0x7FFFFFFFu);
+  return __float_as_uint(fmaxf(fmaxf(fabsf(__fmul_rn(t.x, s_src)), fabsf(__fmul_rn(t.y, s_src))), 0.f));
 }
 
 // A scale per tile: a warp per (layer, kv head, K or V), destination tile by
