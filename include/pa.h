@@ -405,7 +405,9 @@ typedef struct pa_rope_axes {
  *   q_weight, k_weight  device [head_dim], or [n_q_heads][head_dim] and
  *                   [n_kv_heads][head_dim] with weights_per_head 1, of the
  *                   pool's input dtype; NULL: that side is not normalised
- *   eps             finite, >= 0 (with 0 a head of zeros gives NaN)
+ *   eps             finite, >= 0 (with 0 a head of zeros gives NaN, and one whose squares
+ *                   leave fp32's normal range, elements below 2^-63, loses precision and
+ *                   in the end becomes infinite)
  *   weight_offset   finite; 1 for models whose weights are kept as w - 1
  *   positions_dev   device int32 [n_axes][T], axis by axis
  * The squares are added up in fp32 (a head whose sum passes its range gives zeros),
@@ -656,16 +658,18 @@ PA_API int pa_decode_tree_workspace_bytes(const pa_pool* pool, int n_q_heads, in
  * Grouped-query heads, block tables and softmax_scale are as for pa_decode.  Sequences
  * without nodes are skipped; a node that sees nothing (no history, no bit) gets
  * zeros.  What a node does not see does not touch its result, whatever the cache holds there
- * (infinities, NaN and tiles' scales among it).  An infinity or a NaN in the values (V)
- * that it does see makes the result infinite or NaN there, however small its weight is.  In the product with V the weights keep
- * their precision (two terms), but for FP8 pools with bf16 outputs, which round each weight to
- * binary16 (2^-12 of it, a sixteenth of the output's own rounding).  A key counts while its weight, times its
- * tile's V scale in PA_FP8_E4M3_BLOCK pools, is above 2^-31 of the row's largest; such scales may lie any
- * distance apart.  A V scale below the smallest normal fp32 number counts as 0.  A sequence with more than max_nodes nodes, a decreasing or negative q_start or
- * one above T, a context shorter than its nodes or longer than 16 * max_blocks_per_seq
- * is skipped (its rows are not written), a table entry outside [0, num_blocks) gives
- * an undefined result for its sequence; both set PA_ERR_BOUNDS in the device error
- * word.  PA_ERR_UNSUPPORTED for more than 65535 sequences or tables of more than 2^27 - 256
+ * (infinities, NaN and tiles' scales among it).  An infinity or a NaN in the values
+ * (V) that it does see makes the result infinite or NaN there, however small its
+ * weight is.  In the product with V the weights keep their precision (two terms), but
+ * for FP8 pools with bf16 outputs, which round each weight to binary16 (2^-12 of it, a
+ * sixteenth of the output's own rounding).  A key counts while its weight, times its
+ * tile's V scale in PA_FP8_E4M3_BLOCK pools, is above 2^-31 of the row's largest; the
+ * scales may lie any distance apart.  A V scale below the smallest normal fp32 number
+ * counts as 0.  A sequence with more than max_nodes nodes, a decreasing or negative
+ * q_start or one above T, a context shorter than its nodes or longer than
+ * 16 * max_blocks_per_seq is skipped (its rows are not written), a table entry outside
+ * [0, num_blocks) gives an undefined result for its sequence; both set PA_ERR_BOUNDS in
+ * the device error word.  PA_ERR_UNSUPPORTED for more than 65535 sequences or tables of more than 2^27 - 256
  * blocks.  Equal inputs give equal bits on equal devices. */
 PA_API int pa_decode_tree(pa_pool* pool, int layer, void* out, int out_dtype, const void* q, int T,
                           const int32_t* q_start_dev, const int32_t* block_tables_dev,
@@ -681,17 +685,19 @@ PA_API int pa_decode_tree(pa_pool* pool, int layer, void* out, int out_dtype, co
  *   path_lens_dev  device int32 [S]: 0 .. max_path
  *   q_start_dev, block_tables_dev, ctx_lens_dev  as for pa_decode_tree
  *   new_lens_dev   device int32 [S], out: the context length after it,
- *                  ctx - nodes + path_len; another buffer than the inputs
+ *                  ctx - nodes + path_len; must not overlap any input
  * 16-bit and FP8 pools move the bytes.  In PA_FP8_E4M3_BLOCK pools a destination tile's
  * scale grows to s = max(s_old, fl32(m / 448)), m the largest |fl32(decode(c) * s_src)| of
- * the rows that come from other tiles (a NaN counts for nothing in m and stays a NaN); if it grew, the codes of the tile's 16 rows become
+ * the rows that come from other tiles (a NaN counts for nothing in m and stays a NaN);
+ * if it grew, the codes of the tile's 16 rows become
  * E4M3(fl32(fl32(decode(c) * s_old) / s)); a moved row's codes are
  * E4M3(fl32(fl32(decode(c) * s_src) / s)) (0 when s = 0).  Rows behind the path keep their
  * contents up to that.  The blocks that hold nodes must not be shared with another sequence
  * (pa_cow_prepare).  A path that is out of range or not ascending, a path_len outside
- * [0, max_path] or above the nodes, or lengths that pa_decode_tree would skip
- * set PA_ERR_BOUNDS; nothing of that sequence moves, and new_lens gets its context
- * length unchanged.  A table entry outside [0, num_blocks) sets PA_ERR_BOUNDS, and the rows in
+ * [0, max_path] or above the nodes, a decreasing or negative q_start, more than
+ * PA_TREE_MAX_NODES nodes, a context shorter than its nodes or longer than 16 *
+ * max_blocks_per_seq set PA_ERR_BOUNDS; nothing of that sequence moves, and new_lens gets
+ * its context length unchanged.  (T and max_nodes of pa_decode_tree are not known here.)  A table entry outside [0, num_blocks) sets PA_ERR_BOUNDS, and the rows in
  * that block are skipped.  PA_ERR_UNSUPPORTED as for pa_decode_tree. */
 PA_API int pa_tree_accept(pa_pool* pool, int layer, int n_layers, const int32_t* paths_dev,
                           int max_path, const int32_t* path_lens_dev, const int32_t* q_start_dev,

@@ -21,8 +21,9 @@
 //
 // pa_norm_rope_and_cache adds, before the turn, x rsqrt(mean(x^2) + eps) (offset + w) per head:
 // the D / 16 threads of a row sum their squares in fp32 with shuffles.  The same 8192 tokens:
-// 67.7 us, 4.7 TB/s, issue slots 61% busy: the norm's instructions per element, which the
-// copy cannot hide.  64 tokens of 32 / 8 heads (bf16) 4.5 us; 2037 of 32 / 8 heads with a scale per tile 25.6.
+// 67.7 us, 4.7 TB/s, with issue slots 67% and DRAM 50% busy: bound by neither, but by what a warp waits for (28% of its
+// time loads, 28% shuffles and fixed latencies, at 6.7 warps a scheduler) and by 1.68 waves of CTAs.  64 tokens of
+// 32 / 8 heads (bf16) 4.6 us; 2037 of 32 / 8 heads with a scale per tile 26.
 // Weights held in fp32 registers or in shared memory, packed arithmetic and other
 // warps per CTA were all slower.
 #include <cuda_runtime.h>

@@ -23,6 +23,9 @@
 //  * what a row does not see must not touch it.  A masked key's weight is 0, but 0 times an
 //    infinity or a NaN among V is not: such values of nodes are taken out of the block in shared
 //    memory, and put back for the rows that see them when the output is written.
+//  * with a scale per tile, O's weights follow a reference of the row's own, the largest score plus log2 of its
+//    tile's V scale among the keys that it sees: a tile that it does not see, or whose weight is small,
+//    takes no bits from the others (24 sequences of 1000-9001 tokens, 40 / 8 heads: 170 us and 8).
 //
 // What bounds it: 16-bit pools HBM (64 sequences of 512-4096 tokens, 16 nodes of 32 / 8 heads, bf16:
 // 104 us and 6 of the merge, 6.0 TB/s); FP8 pools the chain of hand-offs of a block (scores, maximum, weights, the
@@ -407,8 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
   const long long pos0 = (long long)blockIdx.x * T, pos_end = min(total, pos0 + T);
   if (pos0 < total && before <= pos0 && pos0 < before + mine) {
     long long cum = before;
-  #pragma unroll 1
-  for (int s = s0; s < s1; ++s) {
+#pragma unroll 1
+    for (int s = s0; s < s1; ++s) {
       const SeqInfo i = seq_info(a, seq_raw(a, s));
       const long long c = i.units(a.Hkv) * span_of(i);
       if (pos0 < cum + c) {
@@ -678,48 +681,48 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
       };
 #pragma unroll 1
       for (int lead = 0;; ++lead) {
-       if (lead >= 2) {
-        if (bp == bp1) {
-          ++jp;
-          if (!seg_wait(jp)) break;
-          const Seg& sg = ctl->seg[jp % kSegRing];
-          bp = bp0 = sg.b0;
-          bp1 = sg.b1;
-          pbase = sg.base;
-          mbar_arrive(&ctl->seg_empty[jp % kSegRing]);
-          if (bp == bp1) break;
-          if (jp > 0 && !wait_for(&ctl->o_free, (jp - 1) & 1, abort_flag, a.err)) break;  // O is read out
-        }
-        const int vb = gp & 1;
-        if (!p_ready && !wait_for(&ctl->p_full[vb], (gp >> 1) & 1, abort_flag, a.err)) break;
-        if constexpr (!F8) {
-          if (!v_ready && !wait_for(&ctl->v_full[vslot], vpar, abort_flag, a.err)) break;
-          if (128 * bp + 127 >= pbase) {
-            if (!wait_for(&ctl->tail_done[tp & 1], (tp >> 1) & 1, abort_flag, a.err)) break;
-            ++tp;
+        if (lead >= 2) {
+          if (bp == bp1) {
+            ++jp;
+            if (!seg_wait(jp)) break;
+            const Seg& sg = ctl->seg[jp % kSegRing];
+            bp = bp0 = sg.b0;
+            bp1 = sg.b1;
+            pbase = sg.base;
+            mbar_arrive(&ctl->seg_empty[jp % kSegRing]);
+            if (bp == bp1) break;
+            if (jp > 0 && !wait_for(&ctl->o_free, (jp - 1) & 1, abort_flag, a.err)) break;  // O is read out
           }
-        }
-        k_ready = mbar_test(&ctl->k_full[kslot], kpar);
-        tc_fence_after();
-        const uint32_t lo = v_lo + (uint32_t)(F8 ? vb * (L::kVTBlock >> 4) : vslot * (L::kSlot >> 4));
-        const uint32_t pcol = tmem + vb * 128, add = bp > bp0;
+          const int vb = gp & 1;
+          if (!p_ready && !wait_for(&ctl->p_full[vb], (gp >> 1) & 1, abort_flag, a.err)) break;
+          if constexpr (!F8) {
+            if (!v_ready && !wait_for(&ctl->v_full[vslot], vpar, abort_flag, a.err)) break;
+            if (128 * bp + 127 >= pbase) {
+              if (!wait_for(&ctl->tail_done[tp & 1], (tp >> 1) & 1, abort_flag, a.err)) break;
+              ++tp;
+            }
+          }
+          k_ready = mbar_test(&ctl->k_full[kslot], kpar);
+          tc_fence_after();
+          const uint32_t lo = v_lo + (uint32_t)(F8 ? vb * (L::kVTBlock >> 4) : vslot * (L::kSlot >> 4));
+          const uint32_t pcol = tmem + vb * 128, add = bp > bp0;
 #pragma unroll
-        for (int part = 0; part < (PSPLIT ? 2 : 1); ++part)
+          for (int part = 0; part < (PSPLIT ? 2 : 1); ++part)
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_lo<false>(tmem + kOCol, pcol + 32 * (k >> 1) + 16 * part + 8 * (k & 1), lo + k * (2048 >> 4), kHi128, kIdescPV,
-                          part | k ? 1u : add);
-        if constexpr (F8) mma_commit(&ctl->vt_empty[vb]);
-        else mma_commit(&ctl->v_empty[vslot]);
-        ++gp;
-        if (++vslot == R) {
-          vslot = 0;
-          vpar ^= 1;
+            for (int k = 0; k < 8; ++k)
+              mma_lo<false>(tmem + kOCol, pcol + 32 * (k >> 1) + 16 * part + 8 * (k & 1), lo + k * (2048 >> 4), kHi128, kIdescPV,
+                            part | k ? 1u : add);
+          if constexpr (F8) mma_commit(&ctl->vt_empty[vb]);
+          else mma_commit(&ctl->v_empty[vslot]);
+          ++gp;
+          if (++vslot == R) {
+            vslot = 0;
+            vpar ^= 1;
+          }
+          if (++bp == bp1) mma_commit(&ctl->o_full);
+          p_ready = mbar_test(&ctl->p_full[gp & 1], (gp >> 1) & 1);
+          if constexpr (!F8) v_ready = mbar_test(&ctl->v_full[vslot], vpar);
         }
-        if (++bp == bp1) mma_commit(&ctl->o_full);
-        p_ready = mbar_test(&ctl->p_full[gp & 1], (gp >> 1) & 1);
-        if constexpr (!F8) v_ready = mbar_test(&ctl->v_full[vslot], vpar);
-       }
         if (!issue_qk()) break;
       }
       // every MMA issued above has finished before TMEM is released
@@ -950,77 +953,77 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
         if (rows_ahead) load_rows(j + 1);
       }
       for (int b = b0;; ++b) {
-       if (b < b1) {
-        const int slot = vs;
-        const int nvalid = min(128, ctx - 128 * b);  // keys behind the context: zero
-        const int nplain = base - 128 * b;           // keys from here on are nodes
-        bool odd = false;                            // infinities or NaN among them
-        if constexpr (F8) {
-          const int half = g & 1;
-          ok = __all_sync(kAll, wait_for(&ctl->v_full[slot], vp, abort_flag, a.err));
-          if (ok && g >= 2) ok = __all_sync(kAll, wait_for(&ctl->vt_empty[half], ((g >> 1) - 1) & 1, abort_flag, a.err));
-          if (!ok) break;
-          const uint8_t* vr = sm + (R + slot) * L::kSlot;
-          uint8_t* vt = sm + L::kVT + half * L::kVTBlock;
-          // consecutive lanes take consecutive keys of one 16-byte chunk
+        if (b < b1) {
+          const int slot = vs;
+          const int nvalid = min(128, ctx - 128 * b);  // keys behind the context: zero
+          const int nplain = base - 128 * b;           // keys from here on are nodes
+          bool odd = false;                            // infinities or NaN among them
+          if constexpr (F8) {
+            const int half = g & 1;
+            ok = __all_sync(kAll, wait_for(&ctl->v_full[slot], vp, abort_flag, a.err));
+            if (ok && g >= 2) ok = __all_sync(kAll, wait_for(&ctl->vt_empty[half], ((g >> 1) - 1) & 1, abort_flag, a.err));
+            if (!ok) break;
+            const uint8_t* vr = sm + (R + slot) * L::kSlot;
+            uint8_t* vt = sm + L::kVT + half * L::kVTBlock;
+            // consecutive lanes take consecutive keys of one 16-byte chunk
 #pragma unroll 4
-          for (int ch = 0; ch < D / 16; ++ch) {
-            const int key = ct;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            // a row's chunks are permuted by its line's place: 128-byte lines, or 64-byte rows two to a line
-            const uint32_t off = L::kPart == 64 ? key * 64 + ((ch ^ ((key >> 1) & 3)) << 4) : key * 128 + ((ch ^ (key & 7)) << 4);
-            if (key < nvalid) w = lds128(vr + off);
-            if (nplain < 128 && key >= nplain) odd |= take_out<KIND>(w);
-            const uint32_t cw[4] = {w.x, w.y, w.z, w.w};
-            uint32_t hv[8];
+            for (int ch = 0; ch < D / 16; ++ch) {
+              const int key = ct;
+              uint4 w = make_uint4(0, 0, 0, 0);
+              // a row's chunks are permuted by its line's place: 128-byte lines, or 64-byte rows two to a line
+              const uint32_t off = L::kPart == 64 ? key * 64 + ((ch ^ ((key >> 1) & 3)) << 4) : key * 128 + ((ch ^ (key & 7)) << 4);
+              if (key < nvalid) w = lds128(vr + off);
+              if (nplain < 128 && key >= nplain) odd |= take_out<KIND>(w);
+              const uint32_t cw[4] = {w.x, w.y, w.z, w.w};
+              uint32_t hv[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) e4m3x4_to_f16x2x2(cw[q], hv[2 * q], hv[2 * q + 1]);
-            uint8_t* row = vt + (ch >> 2) * 16384 + key * 128;
-            const int c0 = (ch & 3) * 2;
-            *reinterpret_cast<uint4*>(row + ((c0 ^ (key & 7)) << 4)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-            *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (key & 7)) << 4)) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
-          }
-          if (odd) ctl->bad[j % kScaleRing] = j + 1;
-          fence_proxy_async_shared();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&ctl->p_full[half]);
-            mbar_arrive(&ctl->v_empty[slot]);
-          }
-        } else if (nplain < 128) {
-          // read in place: rows behind the context are zeroed, nodes' rows looked through
-          ok = __all_sync(kAll, wait_for(&ctl->tail_ready[t & 1], (t >> 1) & 1, abort_flag, a.err));
-          ok = ok && __all_sync(kAll, wait_for(&ctl->v_full[slot], vp, abort_flag, a.err));
-          if (!ok) break;
-          uint8_t* vr = sm + (R + slot) * L::kSlot;
-          constexpr int CH = D / 8;  // 16-byte chunks per key
-          const int first = max(0, nplain);
+              for (int q = 0; q < 4; ++q) e4m3x4_to_f16x2x2(cw[q], hv[2 * q], hv[2 * q + 1]);
+              uint8_t* row = vt + (ch >> 2) * 16384 + key * 128;
+              const int c0 = (ch & 3) * 2;
+              *reinterpret_cast<uint4*>(row + ((c0 ^ (key & 7)) << 4)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+              *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (key & 7)) << 4)) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
+            }
+            if (odd) ctl->bad[j % kScaleRing] = j + 1;
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&ctl->p_full[half]);
+              mbar_arrive(&ctl->v_empty[slot]);
+            }
+          } else if (nplain < 128) {
+            // read in place: rows behind the context are zeroed, nodes' rows looked through
+            ok = __all_sync(kAll, wait_for(&ctl->tail_ready[t & 1], (t >> 1) & 1, abort_flag, a.err));
+            ok = ok && __all_sync(kAll, wait_for(&ctl->v_full[slot], vp, abort_flag, a.err));
+            if (!ok) break;
+            uint8_t* vr = sm + (R + slot) * L::kSlot;
+            constexpr int CH = D / 8;  // 16-byte chunks per key
+            const int first = max(0, nplain);
 #pragma unroll 1
-          for (int idx = ct; idx < (128 - first) * CH; idx += 128) {
-            const int key = first + idx / CH, c = idx % CH;
-            uint4* p = reinterpret_cast<uint4*>(vr + (c >> 3) * 16384 + key * 128 + (c & 7) * 16);
-            if (key >= nvalid) {
-              *p = make_uint4(0, 0, 0, 0);
-            } else {
-              uint4 w = *p;
-              if (take_out<KIND>(w)) {
-                *p = w;
-                odd = true;
+            for (int idx = ct; idx < (128 - first) * CH; idx += 128) {
+              const int key = first + idx / CH, c = idx % CH;
+              uint4* p = reinterpret_cast<uint4*>(vr + (c >> 3) * 16384 + key * 128 + (c & 7) * 16);
+              if (key >= nvalid) {
+                *p = make_uint4(0, 0, 0, 0);
+              } else {
+                uint4 w = *p;
+                if (take_out<KIND>(w)) {
+                  *p = w;
+                  odd = true;
+                }
               }
             }
+            if (odd) ctl->bad[j % kScaleRing] = j + 1;
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->tail_done[t & 1]);
+            ++t;
           }
-          if (odd) ctl->bad[j % kScaleRing] = j + 1;
-          fence_proxy_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->tail_done[t & 1]);
-          ++t;
+          ++g;
+          if (++vs == R) {
+            vs = 0;
+            vp ^= 1;
+          }
         }
-        ++g;
-        if (++vs == R) {
-          vs = 0;
-          vp ^= 1;
-        }
-       }
         // The next queries: between the blocks of a long segment (their loads take some microseconds while the copies
         // keep HBM busy), at once in a short one, whose end needs them soon.
         if (rows_ahead && b == (b1 - b0 < 4 ? b0 : b0 + 3)) store_rows(j + 1);
