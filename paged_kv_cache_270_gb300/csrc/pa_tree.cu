@@ -25,7 +25,7 @@
 //    memory, and put back for the rows that see them when the output is written.
 //  * with a scale per tile, O's weights follow a reference of the row's own, the largest score plus log2 of its
 //    tile's V scale among the keys that it sees: a tile that it does not see, or whose weight is small,
-//    takes no bits from the others (24 sequences of 1000-9001 tokens, 40 / 8 heads: 170 us and 8).
+//    takes no bits from the others (24 sequences of 1000-9001 tokens, 40 / 8 heads: 166 us and 8).
 //
 // What bounds it: 16-bit pools HBM (64 sequences of 512-4096 tokens, 16 nodes of 32 / 8 heads, bf16:
 // 104 us and 6 of the merge, 6.0 TB/s); FP8 pools the chain of hand-offs of a block (scores, maximum, weights, the
@@ -1166,7 +1166,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
             }
           }
           // (nothing seen yet, or nothing but values of 0: every weight is 0, or counts in l alone)
-          const float mref = m == -INFINITY ? 0.f : m, rref = !BLK ? mref : r_o == -INFINITY ? 0.f : r_o;
+          const float mref = m == -INFINITY ? 0.f : m;
+          const float dref = (BLK && r_o != -INFINITY ? r_o : 0.f) - mref;  // (block-scaled pools) O's reference, from m
           // O is rescaled once the previous block's P V is done (see the prefill for why this phase
           // of its barrier is never mistaken)
           if (ok && !first && __any_sync(kAll, ov != 1.f)) {
@@ -1199,13 +1200,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TreeArgs a, con
               for (int hp = 0; hp < 2; ++hp) {
                 // Block-scaled pools: a weight times its V scale is 2^(score + log2 scale - r); most of the scale goes
                 // into the exponent, so that it costs a product per page in the place of one per weight.  l takes
-                // the page's sum back to 2^(score - m).  The exponent is kept above what l needs (2^-64 of
-                // the largest score's weight); where that bound holds, O gets what is 0 in 16 bits.
+                // the page's sum back to 2^(score - m) by what went into the exponent before its rounding at the
+                // score's size, so that this rounding cancels where one page has the weight.  The exponent is kept
+                // above what l needs (2^-64 of the largest score's weight); where that bound holds, O gets what is 0 in
+                // 16 bits.
                 float nmp = -mref, back = 1.f, vm = 1.f;
                 if constexpr (BLK) {
                   const float4 sp = ctl->sc[se][2 * c + hp];
-                  nmp = fmaxf(sp.z - rref, -64.f - mref);
-                  back = fast_exp2(-(nmp + mref));
+                  const float shift = fmaxf(sp.z - dref, -64.f);
+                  nmp = shift - mref;
+                  back = fast_exp2(-shift);
                   vm = sp.w;
                 }
                 const float2 f2 = make_float2(pf[cc][hp], pf[cc][hp]), nm = make_float2(nmp, nmp);

@@ -102,3 +102,33 @@ def test_large_scale_under_a_small_weight(ctx, page, up, out_dtype):
     check_sharp(b, b.run(out_dtype=out_dtype))
     assert b.pool.device_error() == N.PA_OK
     b.pool.close()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3", "fp8_e4m3_block"])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scores_far_from_zero(kv, sign):
+    """Scores of 10^6 and more, one key far above (or the least far below) the others: its value, rounded once."""
+    b = Batch(kv, 2, 1, 128, [700, 33, 9000], [1, 1, 1], seed=41)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    for s, at in enumerate((650, 3, 100)):
+        b.q[s] = (1e5 * torch.randn(2, 128, device="cuda", generator=g)).bfloat16()
+        q = b.q[s].float() / 1e5
+        n = b.ctx[s]
+        # every key against the query (or along it), the chosen one along it (or a quarter as far)
+        i = np.arange(n)
+        slots = torch.from_numpy(b.tables_np[s, i // 16].astype(np.int64) * 16 + i % 16).cuda()
+        k = (-q if sign > 0 else -4.0 * q).view(1, 2, 128).repeat(n, 1, 1)
+        k[at] *= -1.0 if sign > 0 else 0.25
+        v = torch.randn(n, 2, 128, device="cuda", generator=g).bfloat16()
+        b.pool.reshape_and_cache(k.bfloat16(), v, slots)
+    v_all = values(b.pool, "v")
+    for dt in (None, torch.float32):
+        out = b.run(out_dtype=dt)
+        for s, at in enumerate((650, 3, 100)):
+            want = v_all[int(b.tables_np[s, at // 16]), :, at % 16]
+            # the one weight's rounding for the product with V (tree_reference), ex2's and the sums' 2^-20, and the output's
+            dp = 2.0 ** -17 if kv == "bf16" else 2.0 ** -22 if dt else 2.0 ** -12
+            tol = want.abs() * (torch.finfo(out.dtype).eps / 2 + dp + 2.0 ** -20)
+            assert bool(((out[s].double() - want).abs() <= tol).all()), (dt, s)
+    assert b.pool.device_error() == N.PA_OK
+    b.pool.close()
