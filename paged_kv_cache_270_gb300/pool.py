@@ -93,7 +93,7 @@ def _check_pairs(axes, rope) -> None:
     """The sections of make_rope_axes must be those of this embedding's pairs.  (Axes filled by hand name all
     64 pairs, so they fit any.)"""
     pairs = getattr(axes, "pairs", None)
-    if pairs is not None and 2 * pairs != rope.rot_dim:
+    if pairs is not None and rope is not None and 2 * pairs != rope.rot_dim:
         raise ValueError(f"axes of {pairs} pairs do not fit an embedding of {rope.rot_dim} dimensions")
 
 

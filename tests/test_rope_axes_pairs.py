@@ -54,3 +54,10 @@ def test_axes_filled_by_hand_name_every_pair():
     _call(_pool(launched), P.make_rope(128), axes, 2)
     _call(_pool(launched), P.make_rope(64), axes, 2)
     assert len(launched) == 2
+
+
+def test_no_embedding_is_left_to_the_library():
+    """A missing embedding reaches the library, which refuses it with its own error."""
+    launched = []
+    _call(_pool(launched), None, P.make_rope_axes([24, 20, 20]), 3)
+    assert len(launched) == 1
